@@ -1,4 +1,6 @@
-"""MI355X (gfx950) TQ1_0 (and TQ2_0) x Q8_1 quantized mat-vec.
+"""MI355X (gfx950) TQ1_0 (and TQ2_0) x Q8_1 quantized mat-vec, and the
+attention side of a decoder layer (``attention.py``: rotary positions, a paged
+cache, attention over it).
 
 A thin binding over the C ABI in ``include/bqm.h`` (library ``libbqm.so``,
 built in-tree by ``bit_quantized_mat_amd.build``). Every function here only
@@ -18,6 +20,9 @@ __all__ = [
     "mmvq_id_tq1_0", "mmvq_id_tq1_0_slots", "mmvq_id_tq1_0_workspace_bytes",
     "mmvq_id_tq1_0_noalloc", "NOALLOC_SCRATCH_BYTES",
     "mmvq_tq1_0_block_isums", "tq2_pack", "mmvq_tq2_0", "mmvq_tq2_0_block_isums",
+    "KvCache", "KvBatch", "KvPages", "rope_inv_freq", "rope_table", "rope", "rope_kv_append",
+    "paged_attention", "paged_attention_workspace_bytes", "kv_extend", "kv_fork", "kv_free",
+    "kv_compact", "kv_copy_pages",
     "TQ1_BLOCK_BYTES", "TQ2_BLOCK_BYTES", "Q81_BLOCK_BYTES", "MMVQ_MAX_COLS",
 ]
 
@@ -87,6 +92,7 @@ def library():
                      "mmvq_id_tq1_0_noalloc", "tq1_dequantize", "tq2_pack", "mmvq_tq2_0",
                      "mmvq_tq2_0_block_isums"):
             getattr(L, name).restype = ctypes.c_int
+        _attention_argtypes(L)
         _lib = L
     return _lib
 
@@ -382,3 +388,11 @@ def mmvq_id_tq1_0_noalloc(w, a, ids, E, N, K, T, n_used, out=None, stream=None):
           _dev_tensor(out, "out", (torch.float32,), T * n_used * N * 4, w.device),
           E, N, K, T, n_used, _stream(stream, w.device))
     return out
+
+
+# the attention side: its functions use the helpers above
+from .attention import (KvBatch, KvCache, KvPages, kv_compact, kv_copy_pages,  # noqa: E402
+                        kv_extend, kv_fork, kv_free, paged_attention,
+                        paged_attention_workspace_bytes, rope, rope_inv_freq, rope_kv_append,
+                        rope_table)
+from .attention import argtypes as _attention_argtypes  # noqa: E402

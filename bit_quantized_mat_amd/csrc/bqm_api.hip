@@ -1,5 +1,6 @@
 // bqm_api.hip -- the C ABI declared in include/bqm.h: argument validation on
 // the host, one dispatch point per entry, launches on the caller's stream.
+#include <math.h>
 #include <string.h>
 
 #include <atomic>
@@ -348,6 +349,301 @@ int mmvq_id_tq1_0_slots(const void *w, const void *a, const int32_t *ids, float 
 {
     return mmvq_id_call(w, a, ids, y, E, N, K, T, n_used, true, workspace, workspace_bytes,
                         stream);
+}
+
+// ---- attention side ----------------------------------------------------------
+
+static bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+static bool is_dtype(int d) { return d >= BQM_DTYPE_F32 && d <= BQM_DTYPE_BF16; }
+static uintptr_t bytes_of(int d) { return d == BQM_DTYPE_F32 ? 4 : 2; }
+
+static int check_cache(const bqm_kv_cache *c)
+{
+    if (!c || !c->k || !c->v)
+        return BQM_ERR_NULL;
+    if (c->n_layers < 1 || c->n_layers > (1 << 20) || c->n_pages < 1 || c->n_pages > (1 << 30) ||
+        c->page_size < 1 || c->page_size > 65536 || c->n_heads < 1 || c->n_heads > 65535 ||
+        c->head_dim < 8 || c->head_dim > 256 || c->head_dim % 8 != 0 ||
+        (c->dtype != BQM_DTYPE_F16 && c->dtype != BQM_DTYPE_BF16))
+        return BQM_ERR_SHAPE;
+    const int64_t most = 1ll << 35;
+    for (const int64_t s : {c->page_stride, c->token_stride, c->head_stride, c->layer_stride})
+        if (s < 0 || s > (1ll << 50))
+            return BQM_ERR_SHAPE;
+    // the kernels count 16-byte pieces of a layer in 32 bits
+    const double span = (double)(c->n_pages - 1) * (double)c->page_stride +
+                        (double)(c->page_size - 1) * (double)c->token_stride +
+                        (double)(c->n_heads - 1) * (double)c->head_stride + c->head_dim;
+    if (span >= (double)most)
+        return BQM_ERR_SHAPE;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) ||
+        (c->page_stride | c->token_stride | c->head_stride | c->layer_stride) % 8 != 0)
+        return BQM_ERR_ALIGN;
+    return BQM_OK;
+}
+
+static int check_batch(const bqm_kv_batch *b)
+{
+    if (!b || !b->table || !b->kv_lens || !b->q_starts)
+        return BQM_ERR_NULL;
+    if (b->n_seqs < 1 || b->n_seqs > 65535 || b->max_pages < 1 || b->max_pages > (1 << 24) ||
+        b->table_stride < 0 || b->total_q < 0 || b->total_q > (1 << 23) || b->max_q < 0 ||
+        b->max_kv < 0)
+        return BQM_ERR_SHAPE;
+    if (!aligned4(b->table) || !aligned4(b->kv_lens) || !aligned4(b->q_starts))
+        return BQM_ERR_ALIGN;
+    return BQM_OK;
+}
+
+int rope_table(const double *inv_freq, float *table, int64_t n_pos, int32_t n_freq, double scale,
+               void *stream)
+{
+    if (!inv_freq || !table)
+        return BQM_ERR_NULL;
+    if (n_pos < 1 || n_pos > 0x7fffffff || n_freq < 1 || n_freq > 512)
+        return BQM_ERR_SHAPE;
+    if (!aligned(inv_freq, 8) || !aligned(table, 8))
+        return BQM_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return bqm::launch_rope_table(inv_freq, table, n_pos, n_freq, scale, as_stream(stream));
+}
+
+int rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y,
+         int64_t y_token_stride, int64_t y_head_stride, const int32_t *positions,
+         const float *table, int64_t T, int32_t n_heads, int32_t head_dim, int64_t n_pos,
+         int32_t n_freq, int32_t interleaved, int32_t inverse, int32_t in_dtype,
+         int32_t out_dtype, void *stream)
+{
+    if (!x || !y || !positions || !table)
+        return BQM_ERR_NULL;
+    if (T < 0 || T > (1 << 23) || n_heads < 1 || head_dim < 2 || head_dim > 1024 ||
+        (int64_t)n_heads * head_dim > (1 << 23) || n_freq < 1 || 2 * (int64_t)n_freq > head_dim ||
+        n_pos < 1 || n_pos > 0x7fffffff || !is_dtype(in_dtype) || !is_dtype(out_dtype))
+        return BQM_ERR_SHAPE;
+    for (const int64_t s : {x_token_stride, x_head_stride, y_token_stride, y_head_stride})
+        if (s < 0 || s > (1ll << 38))
+            return BQM_ERR_SHAPE;
+    // in place every value is read and written by one thread: same places only
+    if (x == y && (in_dtype != out_dtype || x_token_stride != y_token_stride ||
+                   x_head_stride != y_head_stride))
+        return BQM_ERR_SHAPE;
+    if (!aligned(x, bytes_of(in_dtype)) || !aligned(y, bytes_of(out_dtype)) ||
+        !aligned4(positions) || !aligned(table, 8))
+        return BQM_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    if (T == 0)
+        return BQM_OK;
+    return bqm::launch_rope(x, x_token_stride, x_head_stride, y, y_token_stride, y_head_stride,
+                            positions, table, T, n_heads, head_dim, n_pos, n_freq,
+                            interleaved != 0, inverse != 0, in_dtype, out_dtype,
+                            as_stream(stream));
+}
+
+int rope_kv_append(const void *q, const void *k, const void *v, int64_t token_stride, void *q_out,
+                   const bqm_kv_cache *cache, const bqm_kv_batch *batch, const int32_t *positions,
+                   const float *table, int64_t n_pos, int32_t n_freq, int32_t interleaved,
+                   int32_t n_q_heads, int32_t in_dtype, void *stream)
+{
+    if (!k || !v || !table || n_q_heads < 0 || (n_q_heads > 0 && (!q || !q_out)))
+        return n_q_heads < 0 ? BQM_ERR_SHAPE : BQM_ERR_NULL;
+    if (int rc = check_cache(cache))
+        return rc;
+    if (int rc = check_batch(batch))
+        return rc;
+    if (((int64_t)n_q_heads + 2 * (int64_t)cache->n_heads) * cache->head_dim > (1 << 23) ||
+        n_freq < 1 || 2 * (int64_t)n_freq > cache->head_dim || n_pos < 1 || n_pos > 0x7fffffff ||
+        token_stride < 0 || token_stride > (1ll << 38) || !is_dtype(in_dtype))
+        return BQM_ERR_SHAPE;
+    const uintptr_t e = bytes_of(in_dtype);
+    if (!aligned(k, e) || !aligned(v, e) || (n_q_heads > 0 && (!aligned(q, e) || !aligned(q_out, 16))) ||
+        !aligned(table, 8) || (positions && !aligned4(positions)))
+        return BQM_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    if (batch->total_q == 0)
+        return BQM_OK;
+    return bqm::launch_rope_append(n_q_heads > 0 ? q : nullptr, k, v, token_stride, q_out, cache,
+                                   batch, positions, table, n_pos, n_freq, interleaved != 0,
+                                   n_q_heads, in_dtype, as_stream(stream));
+}
+
+static bool attention_heads_ok(const bqm_kv_cache *c, int32_t n_q_heads)
+{
+    return n_q_heads >= 1 && n_q_heads <= 65535 && n_q_heads % c->n_heads == 0 &&
+           (int64_t)n_q_heads * c->head_dim <= (1 << 23);
+}
+
+size_t paged_attention_workspace_bytes(const bqm_kv_cache *cache, const bqm_kv_batch *batch,
+                                       int32_t n_q_heads)
+{
+    if (check_cache(cache) || !batch || batch->n_seqs < 1 || batch->n_seqs > 65535 ||
+        batch->max_pages < 1 || batch->total_q < 0 || batch->total_q > (1 << 23) ||
+        batch->max_q < 0 || batch->max_kv < 0 || !attention_heads_ok(cache, n_q_heads))
+        return 0;
+    return bqm::attention_workspace(cache, batch, n_q_heads);
+}
+
+int paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                    const bqm_kv_cache *cache, const bqm_kv_batch *batch, void *out,
+                    int32_t n_q_heads, float scale, int32_t causal, int32_t window,
+                    int32_t out_dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!q || !out)
+        return BQM_ERR_NULL;
+    if (int rc = check_cache(cache))
+        return rc;
+    if (int rc = check_batch(batch))
+        return rc;
+    if (!attention_heads_ok(cache, n_q_heads) || !(scale > 0.0f) || !isfinite(scale) ||
+        window < 0 || (out_dtype != cache->dtype && out_dtype != BQM_DTYPE_F32) ||
+        q_token_stride < 0 || q_token_stride > (1ll << 38) || q_head_stride < 0 ||
+        q_head_stride > (1ll << 38))
+        return BQM_ERR_SHAPE;
+    if (!aligned(q, 16) || !aligned(out, 16) || (q_token_stride | q_head_stride) % 8 != 0)
+        return BQM_ERR_ALIGN;
+    const size_t need = bqm::attention_workspace(cache, batch, n_q_heads);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return BQM_ERR_WORKSPACE;
+    if (workspace && !aligned(workspace, 256))
+        return BQM_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    if (batch->total_q == 0)
+        return BQM_OK;
+    return bqm::launch_paged_attention(q, q_token_stride, q_head_stride, cache, batch, out,
+                                       n_q_heads, scale, causal != 0, window, out_dtype, workspace,
+                                       as_stream(stream));
+}
+
+static int check_pages(const bqm_kv_pages *p)
+{
+    if (!p || !p->table || !p->lens || !p->refs)
+        return BQM_ERR_NULL;
+    if (p->n_pages < 1 || p->n_pages > (1 << 30) || p->n_seqs < 1 || p->n_seqs > 65535 ||
+        p->max_pages < 1 || p->max_pages > (1 << 24) || p->table_stride < p->max_pages)
+        return BQM_ERR_SHAPE;
+    if (!aligned4(p->table) || !aligned4(p->lens) || !aligned4(p->refs))
+        return BQM_ERR_ALIGN;
+    return BQM_OK;
+}
+
+static int check_in_out(const bqm_kv_pages *in, const bqm_kv_pages *out)
+{
+    if (int rc = check_pages(in))
+        return rc;
+    if (int rc = check_pages(out))
+        return rc;
+    if (in->n_pages != out->n_pages || in->n_seqs != out->n_seqs ||
+        in->max_pages != out->max_pages ||
+        (in->table == out->table && in->table_stride != out->table_stride))
+        return BQM_ERR_SHAPE;
+    return BQM_OK;
+}
+
+static int check_pages_workspace(const bqm_kv_pages *p, const void *workspace, size_t bytes)
+{
+    if (!workspace || bytes < bqm::kv_pages_workspace(p->n_pages, p->n_seqs))
+        return BQM_ERR_WORKSPACE;
+    return aligned(workspace, 256) ? BQM_OK : BQM_ERR_ALIGN;
+}
+
+static bool page_size_ok(int32_t n) { return n >= 1 && n <= 65536; }
+
+size_t kv_pages_workspace_bytes(const bqm_kv_pages *pages)
+{
+    if (!pages || pages->n_pages < 1 || pages->n_pages > (1 << 30) || pages->n_seqs < 1 ||
+        pages->n_seqs > 65535)
+        return 0;
+    return bqm::kv_pages_workspace(pages->n_pages, pages->n_seqs);
+}
+
+int kv_extend(const bqm_kv_pages *in, const bqm_kv_pages *out, const int32_t *n_new,
+              int32_t page_size, int32_t *short_of, void *workspace, size_t workspace_bytes,
+              void *stream)
+{
+    if (!n_new || !short_of)
+        return BQM_ERR_NULL;
+    if (int rc = check_in_out(in, out))
+        return rc;
+    if (!page_size_ok(page_size))
+        return BQM_ERR_SHAPE;
+    if (!aligned4(n_new) || !aligned4(short_of))
+        return BQM_ERR_ALIGN;
+    if (int rc = check_pages_workspace(in, workspace, workspace_bytes))
+        return rc;
+    if (int rc = check_device())
+        return rc;
+    return bqm::launch_kv_extend(in, out, n_new, page_size, short_of, workspace,
+                                 as_stream(stream));
+}
+
+int kv_fork(const bqm_kv_pages *in, const bqm_kv_pages *out, const int32_t *parents,
+            const int32_t *children, int32_t n, int32_t page_size, int32_t *moves,
+            int32_t *short_of, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!parents || !children || !moves || !short_of)
+        return BQM_ERR_NULL;
+    if (int rc = check_in_out(in, out))
+        return rc;
+    if (!page_size_ok(page_size) || n < 0 || n > in->n_seqs)
+        return BQM_ERR_SHAPE;
+    if (!aligned4(parents) || !aligned4(children) || !aligned4(moves) || !aligned4(short_of))
+        return BQM_ERR_ALIGN;
+    if (int rc = check_pages_workspace(in, workspace, workspace_bytes))
+        return rc;
+    if (int rc = check_device())
+        return rc;
+    return bqm::launch_kv_fork(in, out, parents, children, n, page_size, moves, short_of,
+                               workspace, as_stream(stream));
+}
+
+int kv_free(const bqm_kv_pages *in, const bqm_kv_pages *out, const int32_t *seqs, int32_t n,
+            void *stream)
+{
+    if (!seqs)
+        return BQM_ERR_NULL;
+    if (int rc = check_in_out(in, out))
+        return rc;
+    if (n < 0 || n > 65535)
+        return BQM_ERR_SHAPE;
+    if (!aligned4(seqs))
+        return BQM_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return bqm::launch_kv_free(in, out, seqs, n, as_stream(stream));
+}
+
+int kv_compact(const bqm_kv_pages *in, const bqm_kv_pages *out, int32_t page_size,
+               int32_t *page_map, int32_t *moves, void *stream)
+{
+    if (!page_map || !moves)
+        return BQM_ERR_NULL;
+    if (int rc = check_in_out(in, out))
+        return rc;
+    if (!page_size_ok(page_size))
+        return BQM_ERR_SHAPE;
+    if (!aligned4(page_map) || !aligned4(moves))
+        return BQM_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return bqm::launch_kv_compact(in, out, page_size, page_map, moves, as_stream(stream));
+}
+
+int kv_copy_pages(const bqm_kv_cache *cache, const int32_t *moves, int64_t n, void *stream)
+{
+    if (!moves)
+        return BQM_ERR_NULL;
+    if (int rc = check_cache(cache))
+        return rc;
+    if (n < 0 || n > (1 << 30))
+        return BQM_ERR_SHAPE;
+    if (!aligned4(moves))
+        return BQM_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return n == 0 ? BQM_OK : bqm::launch_kv_copy_pages(cache, moves, n, as_stream(stream));
 }
 
 const char *bqm_status_string(int status)

@@ -152,4 +152,34 @@ int launch_mmvq_id_pairs(const void *w, const void *a, const int32_t *ids, float
                          int64_t N, int64_t K, int64_t T, int32_t n_used, int pairs_per_col,
                          hipStream_t stream);
 
+// Rotary positions, the cache's page upkeep and attention (arguments as the
+// entry points', already checked).
+int launch_rope_table(const double *inv_freq, float *table, int64_t n_pos, int n_freq,
+                      double scale, hipStream_t stream);
+int launch_rope(const void *x, int64_t x_token, int64_t x_head, void *y, int64_t y_token,
+                int64_t y_head, const int32_t *positions, const float *table, int64_t T,
+                int n_heads, int head_dim, int64_t n_pos, int n_freq, bool interleaved,
+                bool inverse, int in_dtype, int out_dtype, hipStream_t stream);
+int launch_rope_append(const void *q, const void *k, const void *v, int64_t token_stride,
+                       void *q_out, const bqm_kv_cache *cache, const bqm_kv_batch *batch,
+                       const int32_t *positions, const float *table, int64_t n_pos, int n_freq,
+                       bool interleaved, int n_q_heads, int in_dtype, hipStream_t stream);
+size_t kv_pages_workspace(int64_t n_pages, int64_t n_seqs);
+int launch_kv_extend(const bqm_kv_pages *in, const bqm_kv_pages *out, const int32_t *n_new,
+                     int page_size, int32_t *short_of, void *workspace, hipStream_t stream);
+int launch_kv_fork(const bqm_kv_pages *in, const bqm_kv_pages *out, const int32_t *parents,
+                   const int32_t *children, int n, int page_size, int32_t *moves,
+                   int32_t *short_of, void *workspace, hipStream_t stream);
+int launch_kv_free(const bqm_kv_pages *in, const bqm_kv_pages *out, const int32_t *seqs, int n,
+                   hipStream_t stream);
+int launch_kv_compact(const bqm_kv_pages *in, const bqm_kv_pages *out, int page_size,
+                      int32_t *page_map, int32_t *moves, hipStream_t stream);
+int launch_kv_copy_pages(const bqm_kv_cache *c, const int32_t *moves, int64_t n,
+                         hipStream_t stream);
+size_t attention_workspace(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads);
+int launch_paged_attention(const void *q, int64_t q_token, int64_t q_head, const bqm_kv_cache *c,
+                           const bqm_kv_batch *b, void *out, int n_q_heads, float scale,
+                           bool causal, int window, int out_dtype, void *workspace,
+                           hipStream_t stream);
+
 }  // namespace bqm

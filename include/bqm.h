@@ -1,5 +1,6 @@
 /*
- * bqm.h -- C ABI of the MI355X (gfx950) TQ1_0 x Q8_1 quantized mat-vec library.
+ * bqm.h -- C ABI of the MI355X (gfx950) TQ1_0 x Q8_1 quantized mat-vec library,
+ * with the attention side of a decoder layer (at the end).
  *
  * The operation: ternary weights stored in the TQ1_0 block format (five
  * base-3 trits per byte, 256-element blocks) multiplied against activations
@@ -348,6 +349,191 @@ BQM_API int mmvq_tq2_0(const void *w, const void *a, float *y,
  * (int32 [T][N][K/32]) instead of the outputs. Same shapes and alignment. */
 BQM_API int mmvq_tq2_0_block_isums(const void *w, const void *a, int32_t *isums,
                            int64_t N, int64_t K, int32_t T, void *stream);
+
+/* ---- The attention side of a decoder layer ---------------------------------
+ * Between the q/k/v product and the output product of a layer: rotary
+ * positions, a cache of keys and values kept in pages, attention of new tokens
+ * over that cache, and the upkeep of its pages. None of it is on the pages
+ * cited above; the definitions below are the whole of it.
+ *
+ * A cache holds n_pages pages of page_size tokens. Which pages a sequence
+ * holds, and in which order, stands in its row of a page table: its token i
+ * lies in page table[seq][i / page_size] at place i % page_size. The same
+ * table serves every layer. Page ids outside [0, n_pages) mean "no page":
+ * tokens there are not stored, and read as keys and values of zero.
+ *
+ * Fixed contents the device does not check (results are unspecified, every
+ * access stays inside the buffers described): lengths above max_kv or the
+ * table's width, q_starts that do not ascend from 0 to total_q, a page given
+ * to two writers at once. */
+
+/* A cache (host struct; read during the call only). Strides are in elements;
+ * the head_dim values of one (page, token, head) are contiguous, so both
+ * [page][token][head] and [page][head][token] orders are described. */
+typedef struct bqm_kv_cache {
+    void *k, *v;          /* layer 0, page 0, token 0, head 0; 16-byte aligned  */
+    int64_t layer_stride; /* kv_copy_pages only                                 */
+    int64_t page_stride, token_stride, head_stride;
+    int64_t n_layers;     /* kv_copy_pages copies all; the others use layer 0   */
+    int64_t n_pages;
+    int32_t page_size;    /* 1 .. 65536, any number                             */
+    int32_t n_heads;      /* key/value heads, 1 .. 65535                        */
+    int32_t head_dim;     /* a multiple of 8, 8 .. 256                          */
+    int32_t dtype;        /* BQM_DTYPE_F16 or BQM_DTYPE_BF16                    */
+} bqm_kv_cache;
+/* Strides are multiples of 8 and not negative, and one layer of k spans less
+ * than 2^35 elements (64 GiB). */
+
+/* The new tokens of a step (host struct, device arrays). Sequence b's new
+ * tokens are rows q_starts[b] .. q_starts[b+1]-1 of the token arrays; they
+ * are its last ones: with kv_lens[b] counting them, new token i stands at
+ * position kv_lens[b] - (q_starts[b+1] - q_starts[b]) + i. */
+typedef struct bqm_kv_batch {
+    const int32_t *table;    /* [n_seqs][max_pages], rows table_stride apart     */
+    const int32_t *kv_lens;  /* [n_seqs] tokens in the cache, new ones included  */
+    const int32_t *q_starts; /* [n_seqs + 1], ascending from 0 to total_q        */
+    int64_t table_stride;
+    int64_t total_q;         /* rows of the token arrays, 0 .. 2^23              */
+    int32_t n_seqs;          /* 1 .. 65535                                       */
+    int32_t max_pages;
+    int32_t max_q, max_kv;   /* no sequence has more new tokens / tokens         */
+} bqm_kv_batch;
+
+/* Which sequences hold which pages (device arrays). refs[p] counts the rows
+ * that hold page p; 0 is a free page. Unused row entries are -1. */
+typedef struct bqm_kv_pages {
+    int32_t *table;       /* [n_seqs][max_pages], rows table_stride apart       */
+    int32_t *lens;        /* [n_seqs] tokens                                    */
+    int32_t *refs;        /* [n_pages]                                          */
+    int64_t table_stride;
+    int64_t n_pages;      /* 1 .. 2^30                                          */
+    int32_t n_seqs;       /* 1 .. 65535                                         */
+    int32_t max_pages;    /* 1 .. 2^24                                          */
+} bqm_kv_pages;
+
+/* Rotary angles: table[p][i] = (scale * cos(p * inv_freq[i]),
+ * scale * sin(p * inv_freq[i])), formed in fp64 and stored in fp32, so that
+ * positions in the millions lose nothing. Scaling for long contexts is a
+ * matter of the frequencies (and of scale) the caller gives.
+ *   inv_freq [n_freq] fp64; table [n_pos][n_freq][2] fp32.
+ * Shapes: 1 <= n_pos < 2^31, 1 <= n_freq <= 512. Alignment: 8 bytes. */
+BQM_API int rope_table(const double *inv_freq, float *table, int64_t n_pos, int32_t n_freq,
+                       double scale, void *stream);
+
+/* Rotary positions: pair i < n_freq of each head of token t turns by the
+ * angle of row positions[t] = (c, s) of the table,
+ *   y_a = x_a * c - x_b * s,   y_b = x_b * c + x_a * s   (inverse: s -> -s,
+ * which is the gradient's way back), with (a, b) = (i, i + n_freq), or, if
+ * interleaved, (2i, 2i + 1); values from 2 * n_freq on are copied. The sums
+ * are fp32, rounded once to the output's type.
+ *   x [T][n_heads][head_dim] of in_dtype, y the same of out_dtype (any pair of
+ *   BQM_DTYPE_*), strides in elements, the values of a head contiguous; y may
+ *   be x itself with the same type and strides and must not otherwise overlap.
+ *   positions [T] int32, clamped to [0, n_pos).
+ * Shapes: 0 <= T <= 2^23 (0: nothing is done), head_dim 2 .. 1024,
+ * 1 <= n_freq, 2 * n_freq <= head_dim, 1 <= n_pos < 2^31, n_heads * head_dim at
+ * most 2^23, strides not negative. Alignment: x and y to their elements, table
+ * 8, positions 4 bytes. */
+BQM_API int rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y,
+                 int64_t y_token_stride, int64_t y_head_stride, const int32_t *positions,
+                 const float *table, int64_t T, int32_t n_heads, int32_t head_dim, int64_t n_pos,
+                 int32_t n_freq, int32_t interleaved, int32_t inverse, int32_t in_dtype,
+                 int32_t out_dtype, void *stream);
+
+/* The step between the q/k/v product and attention, in one launch: queries
+ * turned into q_out, keys turned and values copied into the cache's pages at
+ * their tokens' places (layer 0).
+ *   q [total_q][n_q_heads][head_dim], k and v [total_q][n_heads][head_dim] of
+ *   in_dtype (BQM_DTYPE_*), rows token_stride elements apart in all three
+ *   (slices of one product's rows), heads contiguous; q may be NULL (with
+ *   n_q_heads 0: keys and values only), and q_out then is not used.
+ *   q_out [total_q][n_q_heads][head_dim] of the cache's type, contiguous.
+ *   positions [total_q] int32 or NULL: the tokens' places in their sequences
+ *   (a token before a sequence's first place is not stored).
+ * head_dim, page table and lengths are the cache's and the batch's; the rest as
+ * for rope, (n_q_heads + 2 * n_heads) * head_dim at most 2^23. Alignment: q, k, v
+ * to their elements, q_out 16 bytes. */
+BQM_API int rope_kv_append(const void *q, const void *k, const void *v, int64_t token_stride,
+                           void *q_out, const bqm_kv_cache *cache, const bqm_kv_batch *batch,
+                           const int32_t *positions, const float *table, int64_t n_pos,
+                           int32_t n_freq, int32_t interleaved, int32_t n_q_heads,
+                           int32_t in_dtype, void *stream);
+
+/* Attention of the batch's new tokens over the cache (layer 0): for query head
+ * h of the token at position p of its sequence,
+ *   out = sum_j e_j v_j / sum_j e_j,  e_j = exp(scale * (q . k_j) - max),
+ * over the visible tokens j: j < kv_len, j <= p if causal, j > p - window if
+ * window > 0; k_j and v_j of key/value head h / (n_q_heads / n_heads). A row
+ * that sees nothing is zeros; what a row does not see (stale places, later
+ * tokens) does not reach it, NaN and infinities included.
+ * q . k and all sums are fp32; e_j is rounded to the cache's type before it
+ * meets v_j (the sum in the denominator takes the rounded e_j).
+ *   q [total_q][n_q_heads][head_dim] of the cache's type, strides in elements
+ *   (multiples of 8), values contiguous; out [total_q][n_q_heads][head_dim] of
+ *   out_dtype (the cache's type or BQM_DTYPE_F32), contiguous.
+ *   workspace: at least paged_attention_workspace_bytes(...) bytes, 256-byte
+ *   aligned (NULL if that is 0); nothing in it need be kept or cleared, and
+ *   calls that overlap on two streams need one each.
+ * Shapes: n_q_heads a multiple of n_heads, at most 65535, n_q_heads * head_dim
+ * at most 2^23; scale > 0 and finite; window >= 0. Alignment: q and out 16
+ * bytes. */
+BQM_API int paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                            const bqm_kv_cache *cache, const bqm_kv_batch *batch, void *out,
+                            int32_t n_q_heads, float scale, int32_t causal, int32_t window,
+                            int32_t out_dtype, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/* Workspace paged_attention needs for these sizes (of the batch only total_q,
+ * n_seqs, max_q, max_kv and max_pages are read); 0 also for sizes it refuses. */
+BQM_API size_t paged_attention_workspace_bytes(const bqm_kv_cache *cache,
+                                               const bqm_kv_batch *batch, int32_t n_q_heads);
+
+/* Page upkeep. Each call reads `in` and writes `out` (same sizes; each array of
+ * out is the same array of in, in place, or does not overlap it). New pages are
+ * the lowest free ones, in the order of the requests, so results do not depend
+ * on timing. `workspace`: kv_pages_workspace_bytes(pages) bytes, 256-byte
+ * aligned, as for paged_attention. */
+
+/* Room for n_new[s] more tokens in each sequence: lens grow and rows take new
+ * pages. When pages run out, the first sequence that cannot be served and every
+ * later one that needs pages keep their lengths (as does one whose row would
+ * not hold its pages), and short_of[0] counts them (0: all served). */
+BQM_API int kv_extend(const bqm_kv_pages *in, const bqm_kv_pages *out, const int32_t *n_new,
+                      int32_t page_size, int32_t *short_of, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* Forks: child row children[i] (which holds nothing, and is listed once) takes
+ * the tokens of parents[i]: its full pages shared, a partly filled last page
+ * as a new page, for whose tokens moves[i] = (from, to, tokens) is written
+ * (-1, -1, 0 where there is none) for kv_copy_pages. A fork that finds no free
+ * page leaves its child empty and is counted in short_of[0]. Forks whose row
+ * ids lie outside [0, n_seqs) are left out.
+ *   parents, children [n]; moves [n][3]. 0 <= n <= n_seqs. */
+BQM_API int kv_fork(const bqm_kv_pages *in, const bqm_kv_pages *out, const int32_t *parents,
+                    const int32_t *children, int32_t n, int32_t page_size, int32_t *moves,
+                    int32_t *short_of, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The rows seqs[0 .. n-1] end: each gives one count of its pages back and holds
+ * nothing afterwards. A row listed twice is freed once. 0 <= n <= 65535. */
+BQM_API int kv_free(const bqm_kv_pages *in, const bqm_kv_pages *out, const int32_t *seqs,
+                    int32_t n, void *stream);
+
+/* Moves the used pages together: with U pages in use, the k-th used page from U
+ * on goes to the k-th free page before U. page_map[p] is where page p's tokens
+ * are now (p itself if it stays), moves [n_pages / 2][3] lists (from, to,
+ * page_size), then (-1, -1, 0), for kv_copy_pages. */
+BQM_API int kv_compact(const bqm_kv_pages *in, const bqm_kv_pages *out, int32_t page_size,
+                       int32_t *page_map, int32_t *moves, void *stream);
+
+/* Copies tokens between pages in every layer of k and v: for each of the n
+ * moves (from, to, tokens), the first `tokens` tokens of page `from` (at most
+ * page_size) to page `to`; a move with a page outside [0, n_pages) is left out.
+ * No page may be written by two moves, or written by one and read by another. */
+BQM_API int kv_copy_pages(const bqm_kv_cache *cache, const int32_t *moves, int64_t n,
+                          void *stream);
+
+/* Workspace of kv_extend and kv_fork for tables of these sizes. */
+BQM_API size_t kv_pages_workspace_bytes(const bqm_kv_pages *pages);
 
 /* Human-readable text for a status code (static storage). */
 BQM_API const char *bqm_status_string(int status);
