@@ -146,9 +146,8 @@ class KvBatch:
                       _ints(q_starts, "q_starts", n + 1, table.device), table.stride(0))
 
     def struct(self, total_q, page_size):
-        top = 2 ** 31 - 1
-        max_q = min(total_q if self.max_q is None else self.max_q, top)
-        max_kv = min(self.max_pages * page_size if self.max_kv is None else self.max_kv, top)
+        max_q = total_q if self.max_q is None else self.max_q
+        max_kv = min(self.max_pages * page_size, 2 ** 30) if self.max_kv is None else self.max_kv
         return _BatchStruct(*self._args, total_q, self.n_seqs, self.max_pages, max_q, max_kv)
 
 

@@ -1,7 +1,22 @@
 // attention.hip -- attention of new tokens over a paged cache.
 //
 // out = sum_j e_j v_j / sum_j e_j, e_j = exp(scale q.k_j - max): one pass over
-// the keys with the running maximum and sum.
+// the keys with the running maximum and sum of each row.
+//
+// Rows. The query heads of one key/value head see the same keys, so a row is a
+// (token, head of the group) pair: row r of a sequence is token r / group, head
+// r % group, and 32 rows share every key tile a wave reads. A single token with
+// 4 heads fills 4 of 32 rows; the matrix cores have that to spare while the
+// cache streams from memory.
+//
+// Matrix products, transposed so that a row of the softmax lies in one lane
+// pair (l, l + 32): S^T = K Q^T (32 tokens x 32 rows, 32x32x16 products), lane l
+// holding row l % 32 of 16 tokens; then O^T += V^T P^T takes P^T from the same
+// registers: the product's k index may name tokens in any order, and the order
+// in which a lane holds its scores (4 of 8 tokens each half) is also the one in
+// which a transposing LDS read delivers V.
+#include <algorithm>
+
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -9,115 +24,698 @@ namespace bqm {
 
 namespace {
 
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+template <class T>
+struct Operand;
+template <>
+struct Operand<_Float16> {
+    typedef f16x8 type;
+};
+template <>
+struct Operand<__bf16> {
+    typedef bf16x8 type;
+};
+
 struct AttnArgs {
-    const void *q, *k, *v;
+    const void *q;
+    const u32x4 *k, *v;  // 16-byte pieces of 8 values
     void *out;
     const int32_t *pages, *kv_lens, *q_starts;
-    int64_t q_token, q_head, pages_stride;
-    int64_t c_page, c_token, c_head;
-    int64_t total_q, n_pages;
-    int n_seqs, max_pages, page_size, max_q, max_kv;
-    int n_q_heads, group, dim;
-    float scale;
+    float *part;         // [n_splits][total_q][n_q_heads][dim], unscaled sums
+    float2 *part_ml;     // the same rows' maximum (log2) and sum of weights
+    int64_t q_token, q_head, pages_stride, total_q;
+    uint32_t c_page, c_token, c_head;  // strides in pieces
+    int n_pages, n_seqs, max_pages, page_size, max_kv;
+    int n_q_heads, n_heads, group, dim;
+    int tiles, n_splits, chunk;
+    float scale_log2;    // scale * log2(e)
     int causal, window;
 };
 
-// One wave per query head and token: each lane scores one key of 64, then the
-// lanes hold the output's values and the keys go by one at a time.
-template <class T, class O>
-__global__ __launch_bounds__(64) void attention_plain_kernel(AttnArgs a)
+// What invalid pieces (tokens past the range, values past the head) are read
+// from: zeros, so that no stale value, NaN included, meets a product.
+__device__ const u32x4 kZeros = {0, 0, 0, 0};
+
+typedef const __attribute__((address_space(1))) u32x4 *piece_ptr;
+
+// A tile of rows: its sequence, and the tokens that any of its rows sees.
+struct Tile {
+    int seq, tile;      // tile of the sequence
+    int64_t q0;         // the sequence's first token row
+    int q_len, rows;    // its tokens and (token, head) rows
+    int kv_len;
+    int begin, end;     // tokens seen
+};
+
+__device__ __forceinline__ int row_lo(const AttnArgs &a, int pos)
 {
-    __shared__ float qs[256];
-    const int64_t t = blockIdx.x;
-    const int h = blockIdx.y, lane = threadIdx.x;
+    return a.window > 0 ? (int)max((int64_t)0, (int64_t)pos - a.window + 1) : 0;
+}
+
+__device__ __forceinline__ int row_hi(const AttnArgs &a, int kv_len, int pos)
+{
+    return a.causal ? min(kv_len, pos + 1) : kv_len;
+}
+
+__device__ __forceinline__ void load_sequence(const AttnArgs &a, int b, Tile &t)
+{
+    t.seq = b;
+    t.q0 = min(max((int64_t)a.q_starts[b], (int64_t)0), a.total_q);
+    t.q_len = (int)min(max((int64_t)a.q_starts[b + 1] - t.q0, (int64_t)0), a.total_q - t.q0);
+    t.rows = t.q_len * a.group;
+    const int64_t room = min((int64_t)a.max_pages * a.page_size, (int64_t)a.max_kv);
+    t.kv_len = (int)min((int64_t)max(a.kv_lens[b], 0), room);
+}
+
+template <int M>
+__device__ __forceinline__ void load_range(const AttnArgs &a, Tile &t)
+{
+    const int first = t.tile * M / a.group;
+    const int last = min(t.tile * M + M - 1, t.rows - 1) / a.group;
+    const int base = t.kv_len - t.q_len;
+    t.begin = row_lo(a, base + first);
+    t.end = row_hi(a, t.kv_len, base + last);
+}
+
+// How many parts the tile's tokens are cut into.
+__device__ __forceinline__ int parts_of(const AttnArgs &a, const Tile &t)
+{
+    return t.end - t.begin > a.chunk ? (t.end - t.begin + a.chunk - 1) / a.chunk : 1;
+}
+
+// Tile x of the launch. Sequence b's tiles start at floor(q_starts[b] * group /
+// M) + b: never fewer places than it has tiles, some left empty, and found by
+// bisection without a table of sums.
+template <int M>
+__device__ __forceinline__ bool find_tile(const AttnArgs &a, int x, Tile &t)
+{
     int lo = 0, hi = a.n_seqs - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (a.q_starts[mid] <= t)
+        if ((int64_t)a.q_starts[mid] * a.group / M + mid <= x)
             lo = mid;
         else
             hi = mid - 1;
     }
-    const T *q = static_cast<const T *>(a.q) + t * a.q_token + h * a.q_head;
-    for (int d = lane; d < a.dim; d += 64)
-        qs[d] = (float)q[d];
-    __syncthreads();
-    const int most = (int)min((int64_t)a.max_kv, (int64_t)a.max_pages * a.page_size);
-    const int kv_len = min(a.kv_lens[lo], most);
-    const int pos = (int)(kv_len - a.q_starts[lo + 1] + t);
-    int first = 0, end = kv_len;
-    if (a.causal)
-        end = min(end, pos + 1);
-    if (a.window > 0)
-        first = (int)max((int64_t)0, (int64_t)pos - a.window + 1);
-    const T *kc = static_cast<const T *>(a.k) + h / a.group * a.c_head;
-    const T *vc = static_cast<const T *>(a.v) + h / a.group * a.c_head;
-    float top = -INFINITY, sum = 0.0f, acc[4] = {};
-    for (int j0 = first; j0 < end; j0 += 64) {
+    load_sequence(a, lo, t);
+    t.tile = x - (int)((int64_t)a.q_starts[lo] * a.group / M + lo);
+    if (t.tile < 0 || (int64_t)t.tile * M >= t.rows)
+        return false;
+    load_range<M>(a, t);
+    return true;
+}
+
+// Maximum and sum over a lane pair (l, l + 32): the two halves of a softmax row.
+__device__ __forceinline__ float pair_max(float v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+__device__ __forceinline__ float pair_sum(float v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The finite ones of eight values, the others as zeros.
+template <class T>
+__device__ __forceinline__ u32x4 finite_only(u32x4 v)
+{
+    constexpr short e = __is_same(T, _Float16) ? 0x7c00 : 0x7f80;  // the exponent's bits
+    const s16x8 w = __builtin_bit_cast(s16x8, v);
+    return __builtin_bit_cast(u32x4, w & ((w & e) != e));
+}
+
+// Output values d0 .. d0 + dn - 1 (at most 32) of one row, token by token, from
+// those it sees alone; m is the row's maximum (log2). What comes out infinite or
+// NaN is stored: the row sees such a value, and the products left it out.
+template <class T, class Store>
+__device__ __forceinline__ void redo_row(const AttnArgs &a, const int32_t *table, int head,
+                                         const T *q, int lo, int hi, float m, int d0, int dn,
+                                         Store store)
+{
+    const int lane = threadIdx.x & 63;
+    const float base = m == -INFINITY ? 0.0f : m;
+    float o = 0.0f;
+#pragma unroll 1
+    for (int j0 = lo; j0 < hi; j0 += 64) {
         const int j = j0 + lane;
-        float s = -INFINITY;
+        float p = 0.0f;
         int64_t at = -1;
-        if (j < end) {
-            const int page = a.pages[lo * a.pages_stride + j / a.page_size];
-            s = 0.0f;
-            if ((uint64_t)(int64_t)page < (uint64_t)a.n_pages) {
-                at = page * a.c_page + (j % a.page_size) * a.c_token;
+        if (j < hi) {
+            const int page = table[j / a.page_size];
+            float s = 0.0f;
+            if ((uint32_t)page < (uint32_t)a.n_pages) {
+                at = 8 * ((int64_t)page * a.c_page + (int64_t)(j % a.page_size) * a.c_token +
+                          (int64_t)head * a.c_head);
+                const T *k = reinterpret_cast<const T *>(a.k) + at;
+#pragma unroll 1
                 for (int d = 0; d < a.dim; d++)
-                    s += qs[d] * (float)kc[at + d];
+                    s = fmaf((float)q[d], (float)k[d], s);
             }
-            s *= a.scale;
+            p = (float)(T)exp2_fast(fmaf(s, a.scale_log2, -base));
         }
-        float m = s;
-        for (int x = 32; x >= 1; x >>= 1)
-            m = fmaxf(m, __shfl_xor(m, x, 64));
-        m = fmaxf(m, top);
-        const float back = expf(top - m);
-        const float p = (float)(T)expf(s - m);
-        float add = j < end ? p : 0.0f;
-        for (int x = 32; x >= 1; x >>= 1)
-            add += __shfl_xor(add, x, 64);
-        sum = sum * back + add;
-        top = m;
-        for (int c = 0; c < 4; c++)
-            acc[c] *= back;
-        for (int e = 0; e < 64 && j0 + e < end; e++) {
+#pragma unroll 1
+        for (int e = 0; e < 64 && j0 + e < hi; e++) {
             const float pe = __shfl(p, e, 64);
             const int64_t ae = __shfl(at, e, 64);
-            if (ae >= 0)
-                for (int c = 0; c < 4; c++)
-                    if (c * 64 + lane < a.dim)
-                        acc[c] += pe * (float)vc[ae + c * 64 + lane];
+            if (ae < 0)
+                continue;
+            if (lane < dn)
+                o = fmaf(pe, (float)reinterpret_cast<const T *>(a.v)[ae + d0 + lane], o);
         }
     }
-    O *out = static_cast<O *>(a.out) + (t * a.n_q_heads + h) * (int64_t)a.dim;
+    if (lane < dn && !(fabsf(o) < INFINITY))
+        store(d0 + lane, o);
+}
+
+template <class O>
+__device__ __forceinline__ void store4(O *p, f32x4 v)
+{
+    typedef O o4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<o4 *>(p) = __builtin_convertvector(v, o4);
+}
+
+// WM waves share a key tile, 32 rows each; WK such groups take every WK-th tile
+// of 32 * NT tokens and are joined at the end.
+template <int DP, int WM, int WK, int NT>
+struct Shape {
+    static constexpr int M = 32 * WM;
+    static constexpr int kThreads = 64 * WM * WK;
+    static constexpr int TK = 32 * NT;
+    static constexpr int kPieces = DP / 8;                     // of a row
+    static constexpr int kLoads = TK * kPieces / (64 * WM);    // a thread's, of K and of V
+    static constexpr int kRowsPerLoad = 64 * WM / kPieces;
+    // LDS rows are padded: K by 16 bytes (32 lanes read 16 bytes of 32 rows),
+    // V by 32 (16 lanes read 32 bytes of 4 rows): no two of them share banks
+    static constexpr int KS = DP * 2 + 16, VS = DP * 2 + 32;
+    static constexpr int kTile = TK * (KS + VS);
+    static constexpr int kBufs = WM > 1 ? 2 : 1;
+    static constexpr int kStage = kTile * kBufs * WK;
+    static constexpr int kJoin = WK > 1 ? WK * (DP / 32) * 4096 + WK * 256 : 0;
+    static constexpr int kLds = kStage > kJoin ? kStage : kJoin;
+};
+
+template <class T, class O, int DP, int WM, int WK, int NT>
+__global__ __launch_bounds__(64 * WM *WK, DP > 128 ? 1 : 2) void attention_kernel(AttnArgs a)
+{
+    typedef Shape<DP, WM, WK, NT> S;
+    typedef typename Operand<T>::type Op;
+    extern __shared__ char lds[];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = wave % WM, wk = wave / WM;
+    const int half = lane >> 5, col = lane & 31;
+
+    // heads lie next to one another in the grid, so that with eight of them each
+    // XCD's L2 holds one head's keys and values; causal tiles go longest first
+    int x = blockIdx.x;
+    const int head = x % a.n_heads;
+    x /= a.n_heads;
+    const int split = x / a.tiles;
+    x -= split * a.tiles;
+    Tile t;
+    if (!find_tile<S::M>(a, a.tiles - 1 - x, t))
+        return;
+    const int parts = parts_of(a, t);
+    if (split >= parts)
+        return;
+    const int c0 = t.begin + split * a.chunk;
+    const int c1 = parts > 1 ? min(t.end, c0 + a.chunk) : t.end;
+
+    // this lane's row; rows past the end repeat the last and store nothing
+    const int r = t.tile * S::M + wm * 32 + col;
+    const int rc = min(r, t.rows - 1), tok = rc / a.group, g = rc - tok * a.group;
+    const int pos = t.kv_len - t.q_len + tok;
+    const int lo = max(row_lo(a, pos), c0), hi = min(row_hi(a, t.kv_len, pos), c1);
+    // rows ascend with the lanes, and so do lo and hi
+    const int lo_first = __builtin_amdgcn_readlane(lo, 0);
+    const int lo_last = __builtin_amdgcn_readlane(lo, 31);
+    const int hi_first = __builtin_amdgcn_readlane(hi, 0);
+    const int hi_last = __builtin_amdgcn_readlane(hi, 31);
+    const int64_t q_row = t.q0 + tok;
+    const int q_head = head * a.group + g;
+
+    Op qf[DP / 16];
+    {
+        const T *qp = static_cast<const T *>(a.q) + q_row * a.q_token + q_head * a.q_head;
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; kk++) {
+            const int d = 16 * kk + 8 * half;
+            const T *p = d < a.dim ? qp + d : reinterpret_cast<const T *>(&kZeros);
+            qf[kk] = *reinterpret_cast<const Op *>(p);
+        }
+    }
+
+    // ---- staging: this group's tiles are n = 0, 1, ..: tokens t0(n) = c0 + (n WK + wk) TK
+    const int iters = (c1 - c0 + WK * S::TK - 1) / (WK * S::TK);
+    const int gt = wm * 64 + lane;  // thread of the group
+    const int piece = gt % S::kPieces, row0 = gt / S::kPieces;
+    const bool piece_ok = piece * 8 < a.dim;
+    const piece_ptr kp = (piece_ptr)a.k + (uint64_t)head * a.c_head + piece;
+    const piece_ptr vp = (piece_ptr)a.v + (uint64_t)head * a.c_head + piece;
+    const piece_ptr zeros = (piece_ptr)&kZeros;
+    char *buf = lds + wk * S::kTile * S::kBufs;
+    const int32_t *table = a.pages + t.seq * a.pages_stride;
+
+    // lane l looks up token l of the tile to be read next; page and place advance
+    // by a tile at a time without a division
+    const int step_page = WK * S::TK / a.page_size, step_place = WK * S::TK % a.page_size;
+    int ct, cpage, cplace, page_id, place;
+    auto look_up = [&] {
+        page_id = ct < c1 ? table[cpage] : -1;
+        place = cplace;
+        ct += WK * S::TK;
+        cpage += step_page;
+        cplace += step_place;
+        if (cplace >= a.page_size) {
+            cplace -= a.page_size;
+            cpage++;
+        }
+    };
+    u32x4 kr[S::kLoads], vr[S::kLoads];
+    auto load_tile = [&] {
+        const uint32_t mine = (uint32_t)page_id < (uint32_t)a.n_pages
+                                  ? (uint32_t)page_id * a.c_page + (uint32_t)place * a.c_token
+                                  : 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < S::kLoads; i++) {
+            const uint32_t off = __shfl(mine, row0 + i * S::kRowsPerLoad, 64);
+            const bool ok = piece_ok && off != 0xffffffffu;
+            kr[i] = *(ok ? kp + off : zeros);
+            vr[i] = *(ok ? vp + off : zeros);
+        }
+    };
+    bool careful = false;  // keep infinities and NaN of V out of the products
+    auto store_tile = [&](char *b) {
+#pragma unroll
+        for (int i = 0; i < S::kLoads; i++) {
+            const int row = row0 + i * S::kRowsPerLoad;
+            if (careful)
+                vr[i] = finite_only<T>(vr[i]);
+            *reinterpret_cast<u32x4 *>(b + row * S::KS + piece * 16) = kr[i];
+            *reinterpret_cast<u32x4 *>(b + S::TK * S::KS + row * S::VS + piece * 16) = vr[i];
+        }
+    };
+
+    f32x16 acc[DP / 32];
+    float top, sum;  // of this lane's row; sum over its own tokens
+
+    auto compute = [&](const char *b, int t0) {
+        if (t0 >= hi_last || t0 + S::TK <= lo_first)
+            return;  // no row of this wave sees the tile
+        f32x16 s[NT];
+        const char *kb = b + col * S::KS + half * 16;
+#pragma unroll
+        for (int tt = 0; tt < NT; tt++) {
+            s[tt] = f32x16{};
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; kk++)
+                s[tt] = mfma(*reinterpret_cast<const Op *>(kb + tt * 32 * S::KS + kk * 32), qf[kk],
+                             s[tt]);
+        }
+        const bool whole = t0 >= lo_last && t0 + S::TK <= hi_first;
+        if (!whole) {
+#pragma unroll
+            for (int tt = 0; tt < NT; tt++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const int j = t0 + tt * 32 + (i / 4) * 8 + half * 4 + i % 4;
+                    s[tt][i] = j >= lo && j < hi ? s[tt][i] : -INFINITY;
+                }
+        }
+        float m = -INFINITY;
+#pragma unroll
+        for (int tt = 0; tt < NT; tt++)
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                m = fmaxf(m, s[tt][i]);
+        m = fmaxf(pair_max(m) * a.scale_log2, top);
+        const float base = m == -INFINITY ? 0.0f : m;  // a row that has seen nothing yet
+        const float back = exp2_fast(top - base);
+        top = m;
+        sum *= back;
+        Op p[NT][2];
+#pragma unroll
+        for (int tt = 0; tt < NT; tt++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                // rounded to the cache's type: the matrix cores take no wider
+                // operand; the sum takes the rounded weight too
+                const T e = (T)exp2_fast(fmaf(s[tt][i], a.scale_log2, -base));
+                p[tt][i / 8][i % 8] = e;
+                sum += (float)e;
+            }
+#pragma unroll
+        for (int dt = 0; dt < DP / 32; dt++)
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                acc[dt][i] *= back;
+        // 16 lanes read 4 tokens x 16 values; lane l gets value l of the 4
+        const char *vb = b + S::TK * S::KS + (half * 4 + (lane & 15) / 4) * S::VS +
+                         ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+        auto v_frag = [&](int dt, int tt, int c) {
+            typedef __attribute__((address_space(3))) s16x4 *lp;
+            const char *at = vb + (tt * 32 + c * 16) * S::VS + dt * 64;
+            const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at));
+            const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at + 8 * S::VS));
+            return __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+        };
+#pragma unroll
+        for (int dt = 0; dt < DP / 32; dt++)
+#pragma unroll
+            for (int tt = 0; tt < NT; tt++)
+#pragma unroll
+                for (int c = 0; c < 2; c++)
+                    acc[dt] = mfma(__builtin_bit_cast(Op, v_frag(dt, tt, c)), p[tt][c], acc[dt]);
+    };
+
+    const int t00 = c0 + wk * S::TK;
+    for (;;) {
+        ct = t00 + lane % S::TK;
+        cpage = ct / a.page_size;
+        cplace = ct % a.page_size;
+#pragma unroll
+        for (int dt = 0; dt < DP / 32; dt++)
+            acc[dt] = f32x16{};
+        top = -INFINITY;
+        sum = 0.0f;
+        look_up();
+        load_tile();
+        look_up();
+        if constexpr (S::kBufs == 1) {
+            // each wave has its own tile: no barrier, the next tile loads into
+            // registers while this one is used
+            for (int n = 0; n < iters; n++) {
+                store_tile(buf);
+                load_tile();
+                look_up();
+                compute(buf, t00 + n * WK * S::TK);
+            }
+        } else {
+            store_tile(buf);
+            load_tile();
+            look_up();
+            __syncthreads();
+            for (int n = 0; n < iters; n++) {
+                store_tile(buf + ((n + 1) & 1) * S::kTile);
+                load_tile();
+                look_up();
+                compute(buf + (n & 1) * S::kTile, t00 + n * WK * S::TK);
+                __syncthreads();
+            }
+        }
+        // A weight of zero that met an infinity or NaN in a value its row does not
+        // see leaves NaN: then all again with those values as zeros, and rows that
+        // do see them get their due at the end.
+        bool odd = false;
+#pragma unroll
+        for (int dt = 0; dt < DP / 32; dt++)
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                odd |= !(fabsf(acc[dt][i]) < INFINITY);
+        if (careful || !__syncthreads_or(odd))
+            break;
+        careful = true;
+    }
+    sum = pair_sum(sum);
+
+    const bool stores = r < t.rows;
+    const int64_t out_row = q_row * a.n_q_heads + q_head;
+    const int64_t part_row = (int64_t)split * a.total_q * a.n_q_heads;
+    // 32-value tiles first, first + step, .. of the output (o(dt)): final, or this
+    // part's share with its maximum m and sum l
+    auto store_out = [&](auto o, int first, int step, float m, float l) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int dt = first; dt < DP / 32; dt += step) {
+            const f32x16 w = o(dt);
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                const f32x4 v = {w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]};
+                const int d = dt * 32 + c * 8 + half * 4;
+                if (stores && d < a.dim) {
+                    if (parts > 1)
+                        store4(a.part + (part_row + out_row) * a.dim + d, v);
+                    else
+                        store4(static_cast<O *>(a.out) + out_row * a.dim + d, v * inv);
+                }
+            }
+        }
+        if (stores && parts > 1 && first == 0 && half == 0)
+            a.part_ml[part_row + out_row] = make_float2(m, l);
+        if (!careful)
+            return;
+        __threadfence_block();  // the rows' stores above come first
+#pragma unroll 1
+        for (int src = 0; src < min(32, t.rows - t.tile * S::M - wm * 32); src++) {
+            const int64_t at = __shfl(out_row, src, 64);
+            const int64_t tq = at / a.n_q_heads;
+            const T *q = static_cast<const T *>(a.q) + tq * a.q_token +
+                         (at - tq * a.n_q_heads) * a.q_head;
+            const float rm = __shfl(m, src, 64), rinv = __shfl(inv, src, 64);
+            const int rlo = __shfl(lo, src, 64), rhi = __shfl(hi, src, 64);
+#pragma unroll 1
+            for (int dt = first; dt < DP / 32; dt += step)
+                redo_row<T>(a, table, head, q, rlo, rhi, rm, dt * 32, min(32, a.dim - dt * 32),
+                            [&](int d, float v) {
+                                if (parts > 1)
+                                    a.part[(part_row + at) * a.dim + d] = v;
+                                else
+                                    static_cast<O *>(a.out)[at * a.dim + d] = (O)(v * rinv);
+                            });
+        }
+    };
+
+    if constexpr (WK == 1) {
+        store_out([&](int dt) { return acc[dt]; }, 0, 1, top, sum);
+    } else {
+        // join the groups: every wave brings its sums to the common maximum, and
+        // each 32-value tile is added up by one of them
+        float *ml = reinterpret_cast<float *>(lds + WK * WM * (DP / 32) * 4096);
+        float *os = reinterpret_cast<float *>(lds);
+        static_assert(WM == 1, "the join is written for groups of one wave");
+        __syncthreads();
+        if (half == 0)
+            ml[wk * 32 + col] = top;
+        __syncthreads();
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WK; w++)
+            m = fmaxf(m, ml[w * 32 + col]);
+        const float f = top == -INFINITY ? (sum == sum ? 0.0f : 1.0f) : exp2_fast(top - m);
+        float *ls = ml + WK * 32;
+        if (half == 0)
+            ls[wk * 32 + col] = sum * f;
+#pragma unroll
+        for (int dt = 0; dt < DP / 32; dt++)
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                os[((wk * (DP / 32) + dt) * 16 + i) * 64 + lane] = acc[dt][i] * f;
+        __syncthreads();
+        float l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WK; w++)
+            l += ls[w * 32 + col];
+        store_out(
+            [&](int dt) {
+                f32x16 o = {};
+#pragma unroll
+                for (int w = 0; w < WK; w++)
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        o[i] += os[((w * (DP / 32) + dt) * 16 + i) * 64 + lane];
+                return o;
+            },
+            wk, WK, m, l);
+    }
+}
+
+// Joins the parts of rows whose tokens were cut. One wave a row.
+template <class O, int M>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t rows = a.total_q * a.n_q_heads;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= rows)
+        return;
+    const int64_t tq = row / a.n_q_heads;
+    const int h = (int)(row - tq * a.n_q_heads);
+    int lo = 0, hi = a.n_seqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.q_starts[mid] <= tq)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    Tile t;
+    load_sequence(a, lo, t);
+    if (tq < t.q0 || tq >= t.q0 + t.q_len)
+        return;
+    t.tile = (int)((tq - t.q0) * a.group + h % a.group) / M;
+    load_range<M>(a, t);
+    const int parts = parts_of(a, t);
+    if (parts == 1)
+        return;  // written whole
+    float m = -INFINITY;
+    for (int p = 0; p < parts; p++)
+        m = fmaxf(m, a.part_ml[p * rows + row].x);
+    const float base = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f, o[4] = {};
+    for (int p = 0; p < parts; p++) {
+        const float2 ml = a.part_ml[p * rows + row];
+        const float f = ml.x == -INFINITY ? (ml.y == ml.y ? 0.0f : 1.0f) : exp2_fast(ml.x - base);
+        l += ml.y * f;
+#pragma unroll
+        for (int c = 0; c < 4; c++)
+            if (c * 64 + lane < a.dim)
+                o[c] += f * a.part[(p * rows + row) * a.dim + c * 64 + lane];
+    }
+    O *out = static_cast<O *>(a.out) + row * a.dim;
+#pragma unroll
     for (int c = 0; c < 4; c++)
         if (c * 64 + lane < a.dim)
-            out[c * 64 + lane] = (O)(sum == 0.0f ? 0.0f : acc[c] / sum);
+            out[c * 64 + lane] = (O)(l == 0.0f ? 0.0f : o[c] / l);
+}
+
+// How a call is launched: which kernel, and into how many parts the tokens of a
+// tile are cut so that the card is full when there are few rows.
+struct Plan {
+    bool few_rows;      // 32 rows a workgroup, its four waves on tokens
+    int tiles, n_splits, chunk;
+};
+
+constexpr int kFewRows = 32;
+constexpr int64_t kWantedWorkgroups = 1024;  // four a compute unit, of which two run at once
+constexpr int kLeastChunk = 256;
+
+Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads)
+{
+    const int64_t group = n_q_heads / c->n_heads;
+    Plan p;
+    p.few_rows = std::min<int64_t>(b->max_q, b->total_q) * group <= kFewRows;
+    const int m = p.few_rows ? 32 : 128;
+    p.tiles = (int)(b->total_q * group / m + b->n_seqs);
+    const int64_t room = std::min<int64_t>(b->max_kv, (int64_t)b->max_pages * c->page_size);
+    const int64_t workgroups = (int64_t)p.tiles * c->n_heads;
+    const int64_t splits = std::clamp<int64_t>(kWantedWorkgroups / workgroups, 1,
+                                               std::max<int64_t>(1, room / kLeastChunk));
+    const int64_t chunk = (room + splits - 1) / splits;
+    p.chunk = (int)std::max<int64_t>(128, (chunk + 127) / 128 * 128);
+    p.n_splits = (int)std::max<int64_t>(1, (room + p.chunk - 1) / p.chunk);
+    return p;
+}
+
+template <class T, class O, int DP, int WM, int WK, int NT>
+int launch_shape(const AttnArgs &a, hipStream_t stream)
+{
+    typedef Shape<DP, WM, WK, NT> S;
+    auto kernel = attention_kernel<T, O, DP, WM, WK, NT>;
+    allow_dynamic_lds(reinterpret_cast<const void *>(kernel), S::kLds);
+    const int64_t grid = (int64_t)a.tiles * a.n_splits * a.n_heads;
+    if (grid * S::kThreads >= 1ll << 32)
+        return BQM_ERR_SHAPE;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(S::kThreads), S::kLds, stream, a);
+    if (a.n_splits > 1)
+        hipLaunchKernelGGL((attention_join_kernel<O, S::M>),
+                           dim3((unsigned)((a.total_q * a.n_q_heads + 3) / 4)), dim3(256), 0,
+                           stream, a);
+    return check_launch();
+}
+
+template <class T, class O>
+int launch_types(const AttnArgs &a, bool few_rows, hipStream_t stream)
+{
+    if (a.dim <= 64)
+        return few_rows ? launch_shape<T, O, 64, 1, 4, 1>(a, stream)
+                        : launch_shape<T, O, 64, 4, 1, 2>(a, stream);
+    if (a.dim <= 128)
+        return few_rows ? launch_shape<T, O, 128, 1, 4, 1>(a, stream)
+                        : launch_shape<T, O, 128, 4, 1, 2>(a, stream);
+    return few_rows ? launch_shape<T, O, 256, 1, 4, 1>(a, stream)
+                    : launch_shape<T, O, 256, 4, 1, 2>(a, stream);
 }
 
 }  // namespace
 
-size_t attention_workspace(const bqm_kv_cache *, const bqm_kv_batch *, int) { return 0; }
+size_t attention_workspace(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads)
+{
+    if (b->total_q == 0)
+        return 0;
+    const Plan p = plan_of(c, b, n_q_heads);
+    if (p.n_splits == 1)
+        return 0;
+    const size_t rows = (size_t)p.n_splits * b->total_q * n_q_heads;
+    return (rows * (4 * (size_t)c->head_dim + 8) + 255) / 256 * 256;
+}
 
 int launch_paged_attention(const void *q, int64_t q_token, int64_t q_head, const bqm_kv_cache *c,
                            const bqm_kv_batch *b, void *out, int n_q_heads, float scale,
-                           bool causal, int window, int out_dtype, void *, hipStream_t stream)
+                           bool causal, int window, int out_dtype, void *workspace,
+                           hipStream_t stream)
 {
-    const AttnArgs a = {q, c->k, c->v, out, b->table, b->kv_lens, b->q_starts, q_token, q_head,
-                        b->table_stride, c->page_stride, c->token_stride, c->head_stride,
-                        b->total_q, c->n_pages, b->n_seqs, b->max_pages, c->page_size, b->max_q,
-                        b->max_kv, n_q_heads, n_q_heads / c->n_heads, c->head_dim, scale, causal,
-                        window};
-    const dim3 grid((unsigned)b->total_q, (unsigned)n_q_heads);
-    if (c->dtype == BQM_DTYPE_F16 && out_dtype == BQM_DTYPE_F32)
-        hipLaunchKernelGGL((attention_plain_kernel<_Float16, float>), grid, dim3(64), 0, stream, a);
-    else if (c->dtype == BQM_DTYPE_F16)
-        hipLaunchKernelGGL((attention_plain_kernel<_Float16, _Float16>), grid, dim3(64), 0, stream, a);
-    else if (out_dtype == BQM_DTYPE_F32)
-        hipLaunchKernelGGL((attention_plain_kernel<__bf16, float>), grid, dim3(64), 0, stream, a);
-    else
-        hipLaunchKernelGGL((attention_plain_kernel<__bf16, __bf16>), grid, dim3(64), 0, stream, a);
-    return check_launch();
+    const Plan p = plan_of(c, b, n_q_heads);
+    AttnArgs a = {};
+    a.q = q;
+    a.k = static_cast<const u32x4 *>(c->k);
+    a.v = static_cast<const u32x4 *>(c->v);
+    a.out = out;
+    a.pages = b->table;
+    a.kv_lens = b->kv_lens;
+    a.q_starts = b->q_starts;
+    a.q_token = q_token;
+    a.q_head = q_head;
+    a.pages_stride = b->table_stride;
+    a.total_q = b->total_q;
+    a.c_page = (uint32_t)(c->page_stride / 8);
+    a.c_token = (uint32_t)(c->token_stride / 8);
+    a.c_head = (uint32_t)(c->head_stride / 8);
+    a.n_pages = (int)c->n_pages;
+    a.n_seqs = b->n_seqs;
+    a.max_pages = b->max_pages;
+    a.page_size = c->page_size;
+    a.max_kv = b->max_kv;
+    a.n_q_heads = n_q_heads;
+    a.n_heads = c->n_heads;
+    a.group = n_q_heads / c->n_heads;
+    a.dim = c->head_dim;
+    a.tiles = p.tiles;
+    a.n_splits = p.n_splits;
+    a.chunk = p.chunk;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.causal = causal;
+    a.window = window;
+    a.part = static_cast<float *>(workspace);
+    if (p.n_splits > 1)
+        a.part_ml = reinterpret_cast<float2 *>(
+            a.part + (size_t)p.n_splits * b->total_q * n_q_heads * c->head_dim);
+    if (c->dtype == BQM_DTYPE_F16)
+        return out_dtype == BQM_DTYPE_F32
+                   ? launch_types<_Float16, float>(a, p.few_rows, stream)
+                   : launch_types<_Float16, _Float16>(a, p.few_rows, stream);
+    return out_dtype == BQM_DTYPE_F32 ? launch_types<__bf16, float>(a, p.few_rows, stream)
+                                      : launch_types<__bf16, __bf16>(a, p.few_rows, stream);
 }
 
 }  // namespace bqm

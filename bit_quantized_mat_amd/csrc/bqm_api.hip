@@ -388,7 +388,7 @@ static int check_batch(const bqm_kv_batch *b)
         return BQM_ERR_NULL;
     if (b->n_seqs < 1 || b->n_seqs > 65535 || b->max_pages < 1 || b->max_pages > (1 << 24) ||
         b->table_stride < 0 || b->total_q < 0 || b->total_q > (1 << 23) || b->max_q < 0 ||
-        b->max_kv < 0)
+        b->max_kv < 0 || b->max_kv > (1 << 30))
         return BQM_ERR_SHAPE;
     if (!aligned4(b->table) || !aligned4(b->kv_lens) || !aligned4(b->q_starts))
         return BQM_ERR_ALIGN;
@@ -469,9 +469,10 @@ int rope_kv_append(const void *q, const void *k, const void *v, int64_t token_st
                                    n_q_heads, in_dtype, as_stream(stream));
 }
 
-static bool attention_heads_ok(const bqm_kv_cache *c, int32_t n_q_heads)
+static bool attention_heads_ok(const bqm_kv_cache *c, const bqm_kv_batch *b, int32_t n_q_heads)
 {
-    return n_q_heads >= 1 && n_q_heads <= 65535 && n_q_heads % c->n_heads == 0 &&
+    return b->total_q * n_q_heads <= 0x7fffffff &&
+           n_q_heads >= 1 && n_q_heads <= 65535 && n_q_heads % c->n_heads == 0 &&
            (int64_t)n_q_heads * c->head_dim <= (1 << 23);
 }
 
@@ -480,7 +481,8 @@ size_t paged_attention_workspace_bytes(const bqm_kv_cache *cache, const bqm_kv_b
 {
     if (check_cache(cache) || !batch || batch->n_seqs < 1 || batch->n_seqs > 65535 ||
         batch->max_pages < 1 || batch->total_q < 0 || batch->total_q > (1 << 23) ||
-        batch->max_q < 0 || batch->max_kv < 0 || !attention_heads_ok(cache, n_q_heads))
+        batch->max_q < 0 || batch->max_kv < 0 || batch->max_kv > (1 << 30) ||
+        !attention_heads_ok(cache, batch, n_q_heads))
         return 0;
     return bqm::attention_workspace(cache, batch, n_q_heads);
 }
@@ -496,7 +498,7 @@ int paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride
         return rc;
     if (int rc = check_batch(batch))
         return rc;
-    if (!attention_heads_ok(cache, n_q_heads) || !(scale > 0.0f) || !isfinite(scale) ||
+    if (!attention_heads_ok(cache, batch, n_q_heads) || !(scale > 0.0f) || !isfinite(scale) ||
         window < 0 || (out_dtype != cache->dtype && out_dtype != BQM_DTYPE_F32) ||
         q_token_stride < 0 || q_token_stride > (1ll << 38) || q_head_stride < 0 ||
         q_head_stride > (1ll << 38))

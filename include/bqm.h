@@ -396,7 +396,8 @@ typedef struct bqm_kv_batch {
     int64_t total_q;         /* rows of the token arrays, 0 .. 2^23              */
     int32_t n_seqs;          /* 1 .. 65535                                       */
     int32_t max_pages;
-    int32_t max_q, max_kv;   /* no sequence has more new tokens / tokens         */
+    int32_t max_q, max_kv;   /* no sequence has more new tokens / tokens; max_kv
+                                at most 2^30                                     */
 } bqm_kv_batch;
 
 /* Which sequences hold which pages (device arrays). refs[p] counts the rows
@@ -475,7 +476,7 @@ BQM_API int rope_kv_append(const void *q, const void *k, const void *v, int64_t 
  *   aligned (NULL if that is 0); nothing in it need be kept or cleared, and
  *   calls that overlap on two streams need one each.
  * Shapes: n_q_heads a multiple of n_heads, at most 65535, n_q_heads * head_dim
- * at most 2^23; scale > 0 and finite; window >= 0. Alignment: q and out 16
+ * at most 2^23, total_q * n_q_heads below 2^31; scale > 0 and finite; window >= 0. Alignment: q and out 16
  * bytes. */
 BQM_API int paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,
                             const bqm_kv_cache *cache, const bqm_kv_batch *batch, void *out,
