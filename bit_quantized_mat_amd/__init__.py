@@ -90,9 +90,27 @@ def library():
                      "mmvq_tq1_0_add", "mmvq_tq1_0_f32_add", "mmvq_tq1_0_glu",
                      "mmvq_tq1_0_f32_glu", "mmvq_tq1_0_block_isums", "mmvq_id_tq1_0", "mmvq_id_tq1_0_slots",
                      "mmvq_id_tq1_0_noalloc", "tq1_dequantize", "tq2_pack", "mmvq_tq2_0",
-                     "mmvq_tq2_0_block_isums"):
+                     "mmvq_tq2_0_block_isums", "rope_table", "rope", "rope_kv_append",
+                     "paged_attention", "kv_extend", "kv_fork", "kv_free", "kv_compact",
+                     "kv_copy_pages"):
             getattr(L, name).restype = ctypes.c_int
-        _attention_argtypes(L)
+        f, d = ctypes.c_float, ctypes.c_double
+        L.rope_table.argtypes = [_p, _p, _i64, _i32, d, _p]
+        L.rope.argtypes = [_p, _i64, _i64, _p, _i64, _i64, _p, _p, _i64, _i32, _i32, _i64, _i32,
+                           _i32, _i32, _i32, _i32, _p]
+        L.rope_kv_append.argtypes = [_p, _p, _p, _i64, _p, _p, _p, _p, _p, _i64, _i32, _i32, _i32,
+                                     _i32, _p]
+        L.paged_attention.argtypes = [_p, _i64, _i64, _p, _p, _p, _i32, f, _i32, _i32, _i32, _p,
+                                      _sz, _p]
+        L.paged_attention_workspace_bytes.argtypes = [_p, _p, _i32]
+        L.kv_extend.argtypes = [_p, _p, _p, _i32, _p, _p, _sz, _p]
+        L.kv_fork.argtypes = [_p, _p, _p, _p, _i32, _i32, _p, _p, _p, _sz, _p]
+        L.kv_free.argtypes = [_p, _p, _p, _i32, _p]
+        L.kv_compact.argtypes = [_p, _p, _i32, _p, _p, _p]
+        L.kv_copy_pages.argtypes = [_p, _p, _i64, _p]
+        L.kv_pages_workspace_bytes.argtypes = [_p]
+        L.paged_attention_workspace_bytes.restype = _sz
+        L.kv_pages_workspace_bytes.restype = _sz
         _lib = L
     return _lib
 
@@ -390,9 +408,16 @@ def mmvq_id_tq1_0_noalloc(w, a, ids, E, N, K, T, n_used, out=None, stream=None):
     return out
 
 
-# the attention side: its functions use the helpers above
-from .attention import (KvBatch, KvCache, KvPages, kv_compact, kv_copy_pages,  # noqa: E402
-                        kv_extend, kv_fork, kv_free, paged_attention,
-                        paged_attention_workspace_bytes, rope, rope_inv_freq, rope_kv_append,
-                        rope_table)
-from .attention import argtypes as _attention_argtypes  # noqa: E402
+# the attention side imports torch, so it is loaded by the first use of a name
+_ATTENTION = frozenset((
+    "KvCache", "KvBatch", "KvPages", "rope_inv_freq", "rope_table", "rope", "rope_kv_append",
+    "paged_attention", "paged_attention_workspace_bytes", "kv_extend", "kv_fork", "kv_free",
+    "kv_compact", "kv_copy_pages"))
+
+
+def __getattr__(name):
+    if name not in _ATTENTION:
+        raise AttributeError("module %r has no attribute %r" % (__name__, name))
+    from . import attention
+    value = globals()[name] = getattr(attention, name)
+    return value

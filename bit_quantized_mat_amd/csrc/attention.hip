@@ -27,6 +27,7 @@ namespace {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -369,27 +370,37 @@ __global__ __launch_bounds__(64 * WM *WK, DP > 128 ? 1 : 2) void attention_kerne
 #pragma unroll
             for (int i = 0; i < 16; i++)
                 m = fmaxf(m, s[tt][i]);
-        m = fmaxf(pair_max(m) * a.scale_log2, top);
-        const float base = m == -INFINITY ? 0.0f : m;  // a row that has seen nothing yet
-        const float back = exp2_fast(top - base);
-        top = m;
-        sum *= back;
+        m = pair_max(m) * a.scale_log2;
+        // The weights' base follows the maximum only when that has grown by a
+        // factor of 2^8: sums and weights (up to 256, the same relative rounding
+        // in either type) have room for it, and most tiles pass without scaling
+        // the accumulators.
+        if (__any(m > top + 8.0f)) {
+            const float grown = fmaxf(m, top);
+            const float back = top == -INFINITY ? 0.0f : exp2_fast(top - grown);
+            top = grown;
+            sum *= back;
+#pragma unroll
+            for (int dt = 0; dt < DP / 32; dt++)
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    acc[dt][i] *= back;
+        }
+        const float base = top == -INFINITY ? 0.0f : top;  // nothing seen yet
         Op p[NT][2];
 #pragma unroll
         for (int tt = 0; tt < NT; tt++)
 #pragma unroll
-            for (int i = 0; i < 16; i++) {
-                // rounded to the cache's type: the matrix cores take no wider
-                // operand; the sum takes the rounded weight too
-                const T e = (T)exp2_fast(fmaf(s[tt][i], a.scale_log2, -base));
-                p[tt][i / 8][i % 8] = e;
-                sum += (float)e;
+            for (int c = 0; c < 2; c++) {
+                f32x8 e;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    e[i] = exp2_fast(fmaf(s[tt][8 * c + i], a.scale_log2, -base));
+                    sum += e[i];
+                }
+                // rounded to the cache's type: the matrix cores take no wider operand
+                p[tt][c] = __builtin_convertvector(e, Op);
             }
-#pragma unroll
-        for (int dt = 0; dt < DP / 32; dt++)
-#pragma unroll
-            for (int i = 0; i < 16; i++)
-                acc[dt][i] *= back;
         // 16 lanes read 4 tokens x 16 values; lane l gets value l of the 4
         const char *vb = b + S::TK * S::KS + (half * 4 + (lane & 15) / 4) * S::VS +
                          ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
@@ -550,15 +561,17 @@ __global__ __launch_bounds__(64 * WM *WK, DP > 128 ? 1 : 2) void attention_kerne
     }
 }
 
-// Joins the parts of rows whose tokens were cut. One wave a row.
+// Joins the parts of rows whose tokens were cut: one workgroup a row, its four
+// waves on every fourth part, several parts' loads in flight in each.
+constexpr int kMostParts = 1024;
+
 template <class O, int M>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t rows = a.total_q * a.n_q_heads;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= rows)
-        return;
+    __shared__ float weight[kMostParts];
+    __shared__ float share[4][256], sums[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t rows = a.total_q * a.n_q_heads, row = blockIdx.x;
     const int64_t tq = row / a.n_q_heads;
     const int h = (int)(row - tq * a.n_q_heads);
     int lo = 0, hi = a.n_seqs - 1;
@@ -578,25 +591,44 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a)
     const int parts = parts_of(a, t);
     if (parts == 1)
         return;  // written whole
+    // every wave finds the maximum; the parts' weights go to LDS
     float m = -INFINITY;
-    for (int p = 0; p < parts; p++)
+    for (int p = lane; p < parts; p += 64)
         m = fmaxf(m, a.part_ml[p * rows + row].x);
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1)
+        m = fmaxf(m, __shfl_xor(m, d, 64));
     const float base = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, o[4] = {};
-    for (int p = 0; p < parts; p++) {
+    float l = 0.0f;
+    for (int p = threadIdx.x; p < parts; p += 256) {
         const float2 ml = a.part_ml[p * rows + row];
         const float f = ml.x == -INFINITY ? (ml.y == ml.y ? 0.0f : 1.0f) : exp2_fast(ml.x - base);
+        weight[p] = f;
         l += ml.y * f;
-#pragma unroll
-        for (int c = 0; c < 4; c++)
-            if (c * 64 + lane < a.dim)
-                o[c] += f * a.part[(p * rows + row) * a.dim + c * 64 + lane];
     }
-    O *out = static_cast<O *>(a.out) + row * a.dim;
 #pragma unroll
-    for (int c = 0; c < 4; c++)
-        if (c * 64 + lane < a.dim)
-            out[c * 64 + lane] = (O)(l == 0.0f ? 0.0f : o[c] / l);
+    for (int d = 32; d >= 1; d >>= 1)
+        l += __shfl_xor(l, d, 64);
+    if (lane == 0)
+        sums[wave] = l;
+    __syncthreads();
+    l = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    f32x4 o = {};
+    if (lane * 4 < a.dim) {
+        const float *src = a.part + row * a.dim + lane * 4;
+#pragma unroll 4
+        for (int p = wave; p < parts; p += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(src + p * rows * a.dim);
+            o += v * weight[p];
+        }
+    }
+    *reinterpret_cast<f32x4 *>(&share[wave][lane * 4]) = o;
+    __syncthreads();
+    const int d = threadIdx.x;
+    if (d < a.dim) {
+        const float v = (share[0][d] + share[1][d]) + (share[2][d] + share[3][d]);
+        static_cast<O *>(a.out)[row * a.dim + d] = (O)(l == 0.0f ? 0.0f : v / l);
+    }
 }
 
 // How a call is launched: which kernel, and into how many parts the tokens of a
@@ -608,7 +640,8 @@ struct Plan {
 
 constexpr int kFewRows = 32;
 constexpr int64_t kWantedWorkgroups = 1024;  // four a compute unit, of which two run at once
-constexpr int kLeastChunk = 256;
+constexpr int64_t kMostWorkgroups = 8192;    // most of them empty, where lengths differ
+constexpr int kLeastChunk = 256, kRaggedChunk = 1024;
 
 Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads)
 {
@@ -619,10 +652,14 @@ Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads)
     p.tiles = (int)(b->total_q * group / m + b->n_seqs);
     const int64_t room = std::min<int64_t>(b->max_kv, (int64_t)b->max_pages * c->page_size);
     const int64_t workgroups = (int64_t)p.tiles * c->n_heads;
-    const int64_t splits = std::clamp<int64_t>(kWantedWorkgroups / workgroups, 1,
-                                               std::max<int64_t>(1, room / kLeastChunk));
-    const int64_t chunk = (room + splits - 1) / splits;
-    p.chunk = (int)std::max<int64_t>(128, (chunk + 127) / 128 * 128);
+    // parts that fill the card, if every sequence had max_kv tokens
+    int64_t chunk = std::max<int64_t>(kLeastChunk, room * workgroups / kWantedWorkgroups);
+    // with few rows a part costs little: cut long sequences among short ones too
+    if (p.few_rows)
+        chunk = std::min(chunk,
+                         std::max<int64_t>(kRaggedChunk, room * workgroups / kMostWorkgroups));
+    chunk = std::max(chunk, (room + kMostParts - 1) / kMostParts);
+    p.chunk = (int)((chunk + 127) / 128 * 128);
     p.n_splits = (int)std::max<int64_t>(1, (room + p.chunk - 1) / p.chunk);
     return p;
 }
@@ -639,8 +676,7 @@ int launch_shape(const AttnArgs &a, hipStream_t stream)
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(S::kThreads), S::kLds, stream, a);
     if (a.n_splits > 1)
         hipLaunchKernelGGL((attention_join_kernel<O, S::M>),
-                           dim3((unsigned)((a.total_q * a.n_q_heads + 3) / 4)), dim3(256), 0,
-                           stream, a);
+                           dim3((unsigned)(a.total_q * a.n_q_heads)), dim3(256), 0, stream, a);
     return check_launch();
 }
 
