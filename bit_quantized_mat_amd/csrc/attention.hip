@@ -119,22 +119,35 @@ __device__ __forceinline__ int parts_of(const AttnArgs &a, const Tile &t)
     return t.end - t.begin > a.chunk ? (t.end - t.begin + a.chunk - 1) / a.chunk : 1;
 }
 
+// The last sequence b for which first(q_starts[b], b) <= x (first ascends with
+// b, and that of sequence 0 is not above x). All lanes take part: each step
+// narrows the range to a 64th, one load's latency instead of six bisections'.
+template <class First>
+__device__ __forceinline__ int find_sequence(const AttnArgs &a, int64_t x, First first)
+{
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = a.n_seqs;
+    while (n > 1) {
+        const int step = (n + 63) >> 6;
+        const int b = lo + lane * step;
+        const bool in = lane * step < n && first(a.q_starts[min(b, a.n_seqs - 1)], b) <= x;
+        const int k = max(__popcll(__ballot(in)) - 1, 0);
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
 // Tile x of the launch. Sequence b's tiles start at floor(q_starts[b] * group /
-// M) + b: never fewer places than it has tiles, some left empty, and found by
-// bisection without a table of sums.
+// M) + b: never fewer places than it has tiles, some left empty, and found
+// without a table of sums.
 template <int M>
 __device__ __forceinline__ bool find_tile(const AttnArgs &a, int x, Tile &t)
 {
-    int lo = 0, hi = a.n_seqs - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)a.q_starts[mid] * a.group / M + mid <= x)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    load_sequence(a, lo, t);
-    t.tile = x - (int)((int64_t)a.q_starts[lo] * a.group / M + lo);
+    auto first = [&](int start, int b) { return (int64_t)start * a.group / M + b; };
+    const int b = find_sequence(a, x, first);
+    load_sequence(a, b, t);
+    t.tile = x - (int)first(a.q_starts[b], b);
     if (t.tile < 0 || (int64_t)t.tile * M >= t.rows)
         return false;
     load_range<M>(a, t);
@@ -561,73 +574,83 @@ __global__ __launch_bounds__(64 * WM *WK, DP > 128 ? 1 : 2) void attention_kerne
     }
 }
 
-// Joins the parts of rows whose tokens were cut: one workgroup a row, its four
-// waves on every fourth part, several parts' loads in flight in each.
+// Joins the parts of rows whose tokens were cut. WAVES waves share a row and
+// take every WAVES-th part, several parts' loads in flight in each: four for the
+// many parts of a long sequence, one where rows are many and parts few.
 constexpr int kMostParts = 1024;
+constexpr int kFewParts = 16;
 
-template <class O, int M>
+template <class O, int M, int WAVES>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a)
 {
-    __shared__ float weight[kMostParts];
-    __shared__ float share[4][256], sums[4];
+    constexpr int kRows = 4 / WAVES;  // of a workgroup
+    __shared__ float weights[kRows][WAVES == 1 ? kFewParts : kMostParts];
+    __shared__ float shares[4][256], sums[4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t rows = a.total_q * a.n_q_heads, row = blockIdx.x;
-    const int64_t tq = row / a.n_q_heads;
-    const int h = (int)(row - tq * a.n_q_heads);
-    int lo = 0, hi = a.n_seqs - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.q_starts[mid] <= tq)
-            lo = mid;
-        else
-            hi = mid - 1;
+    const int slot = wave / WAVES, part0 = wave % WAVES;
+    const int64_t rows = a.total_q * a.n_q_heads, row = (int64_t)blockIdx.x * kRows + slot;
+    int parts = 1;
+    if (row < rows) {
+        const int64_t tq = row / a.n_q_heads;
+        const int h = (int)(row - tq * a.n_q_heads);
+        Tile t;
+        load_sequence(a, find_sequence(a, tq, [](int start, int) { return (int64_t)start; }), t);
+        if (tq >= t.q0 && tq < t.q0 + t.q_len) {
+            t.tile = (int)((tq - t.q0) * a.group + h % a.group) / M;
+            load_range<M>(a, t);
+            parts = parts_of(a, t);
+        }
     }
-    Tile t;
-    load_sequence(a, lo, t);
-    if (tq < t.q0 || tq >= t.q0 + t.q_len)
-        return;
-    t.tile = (int)((tq - t.q0) * a.group + h % a.group) / M;
-    load_range<M>(a, t);
-    const int parts = parts_of(a, t);
-    if (parts == 1)
-        return;  // written whole
-    // every wave finds the maximum; the parts' weights go to LDS
-    float m = -INFINITY;
-    for (int p = lane; p < parts; p += 64)
-        m = fmaxf(m, a.part_ml[p * rows + row].x);
+    if (WAVES > 1 ? parts == 1 : __syncthreads_and(parts == 1))
+        return;  // written whole; the row is the workgroup's, or none of its rows is cut
+    // every wave finds its row's maximum; the parts' weights go to LDS
+    const float2 *mls = a.part_ml + row;
+    float m = -INFINITY, l = 0.0f;
+    if (parts > 1)
+        for (int p = lane; p < parts; p += 64)
+            m = fmaxf(m, mls[p * rows].x);
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1)
         m = fmaxf(m, __shfl_xor(m, d, 64));
     const float base = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
-    for (int p = threadIdx.x; p < parts; p += 256) {
-        const float2 ml = a.part_ml[p * rows + row];
-        const float f = ml.x == -INFINITY ? (ml.y == ml.y ? 0.0f : 1.0f) : exp2_fast(ml.x - base);
-        weight[p] = f;
-        l += ml.y * f;
-    }
+    float *weight = weights[slot];
+    if (parts > 1)
+        for (int p = part0 * 64 + lane; p < parts; p += 64 * WAVES) {
+            const float2 ml = mls[p * rows];
+            const float f =
+                ml.x == -INFINITY ? (ml.y == ml.y ? 0.0f : 1.0f) : exp2_fast(ml.x - base);
+            weight[p] = f;
+            l += ml.y * f;
+        }
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1)
         l += __shfl_xor(l, d, 64);
     if (lane == 0)
         sums[wave] = l;
     __syncthreads();
-    l = (sums[0] + sums[1]) + (sums[2] + sums[3]);
     f32x4 o = {};
-    if (lane * 4 < a.dim) {
+    if (parts > 1 && lane * 4 < a.dim) {
         const float *src = a.part + row * a.dim + lane * 4;
 #pragma unroll 4
-        for (int p = wave; p < parts; p += 4) {
+        for (int p = part0; p < parts; p += WAVES) {
             const f32x4 v = *reinterpret_cast<const f32x4 *>(src + p * rows * a.dim);
             o += v * weight[p];
         }
     }
-    *reinterpret_cast<f32x4 *>(&share[wave][lane * 4]) = o;
-    __syncthreads();
-    const int d = threadIdx.x;
-    if (d < a.dim) {
-        const float v = (share[0][d] + share[1][d]) + (share[2][d] + share[3][d]);
-        static_cast<O *>(a.out)[row * a.dim + d] = (O)(l == 0.0f ? 0.0f : v / l);
+    if constexpr (WAVES == 1) {
+        if (parts > 1 && lane * 4 < a.dim)
+            store4(static_cast<O *>(a.out) + row * a.dim + lane * 4,
+                   o * (l == 0.0f ? 0.0f : 1.0f / l));
+    } else {
+        static_assert(WAVES == 4, "the workgroup's waves share one row");
+        *reinterpret_cast<f32x4 *>(&shares[wave][lane * 4]) = o;
+        __syncthreads();
+        l = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        const int d = threadIdx.x;
+        if (d < a.dim) {
+            const float v = (shares[0][d] + shares[1][d]) + (shares[2][d] + shares[3][d]);
+            static_cast<O *>(a.out)[row * a.dim + d] = (O)(l == 0.0f ? 0.0f : v / l);
+        }
     }
 }
 
@@ -643,14 +666,17 @@ constexpr int64_t kWantedWorkgroups = 1024;  // four a compute unit, of which tw
 constexpr int64_t kMostWorkgroups = 8192;    // most of them empty, where lengths differ
 constexpr int kLeastChunk = 256, kRaggedChunk = 1024;
 
-Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads)
+Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads, int window)
 {
     const int64_t group = n_q_heads / c->n_heads;
     Plan p;
     p.few_rows = std::min<int64_t>(b->max_q, b->total_q) * group <= kFewRows;
     const int m = p.few_rows ? 32 : 128;
     p.tiles = (int)(b->total_q * group / m + b->n_seqs);
-    const int64_t room = std::min<int64_t>(b->max_kv, (int64_t)b->max_pages * c->page_size);
+    // the most tokens a tile's rows see between them
+    int64_t room = std::min<int64_t>(b->max_kv, (int64_t)b->max_pages * c->page_size);
+    if (window > 0)
+        room = std::min<int64_t>(room, (int64_t)window + m / group + 1);
     const int64_t workgroups = (int64_t)p.tiles * c->n_heads;
     // parts that fill the card, if every sequence had max_kv tokens
     int64_t chunk = std::max<int64_t>(kLeastChunk, room * workgroups / kWantedWorkgroups);
@@ -658,7 +684,10 @@ Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads)
     if (p.few_rows)
         chunk = std::min(chunk,
                          std::max<int64_t>(kRaggedChunk, room * workgroups / kMostWorkgroups));
-    chunk = std::max(chunk, (room + kMostParts - 1) / kMostParts);
+    // no more parts than the workspace holds, whose size does not know the window
+    const int64_t most =
+        window > 0 ? plan_of(c, b, n_q_heads, 0).n_splits : (int64_t)kMostParts;
+    chunk = std::max(chunk, (room + most - 1) / most);
     p.chunk = (int)((chunk + 127) / 128 * 128);
     p.n_splits = (int)std::max<int64_t>(1, (room + p.chunk - 1) / p.chunk);
     return p;
@@ -674,9 +703,13 @@ int launch_shape(const AttnArgs &a, hipStream_t stream)
     if (grid * S::kThreads >= 1ll << 32)
         return BQM_ERR_SHAPE;
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(S::kThreads), S::kLds, stream, a);
-    if (a.n_splits > 1)
-        hipLaunchKernelGGL((attention_join_kernel<O, S::M>),
-                           dim3((unsigned)(a.total_q * a.n_q_heads)), dim3(256), 0, stream, a);
+    const int64_t rows = a.total_q * a.n_q_heads;
+    if (a.n_splits > kFewParts)
+        hipLaunchKernelGGL((attention_join_kernel<O, S::M, 4>), dim3((unsigned)rows), dim3(256), 0,
+                           stream, a);
+    else if (a.n_splits > 1)
+        hipLaunchKernelGGL((attention_join_kernel<O, S::M, 1>), dim3((unsigned)((rows + 3) / 4)),
+                           dim3(256), 0, stream, a);
     return check_launch();
 }
 
@@ -699,7 +732,7 @@ size_t attention_workspace(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q
 {
     if (b->total_q == 0)
         return 0;
-    const Plan p = plan_of(c, b, n_q_heads);
+    const Plan p = plan_of(c, b, n_q_heads, 0);
     if (p.n_splits == 1)
         return 0;
     const size_t rows = (size_t)p.n_splits * b->total_q * n_q_heads;
@@ -711,7 +744,7 @@ int launch_paged_attention(const void *q, int64_t q_token, int64_t q_head, const
                            bool causal, int window, int out_dtype, void *workspace,
                            hipStream_t stream)
 {
-    const Plan p = plan_of(c, b, n_q_heads);
+    const Plan p = plan_of(c, b, n_q_heads, window);
     AttnArgs a = {};
     a.q = q;
     a.k = static_cast<const u32x4 *>(c->k);
