@@ -71,6 +71,111 @@ __device__ __forceinline__ int64_t block_max(int64_t v)
     return v;
 }
 
+struct Pages {
+    const int32_t *table, *lens, *refs;
+    int32_t *table_out, *lens_out, *refs_out;
+    int64_t stride, stride_out;
+    int n_pages, n_seqs, max_pages, page_size;
+};
+
+// Which pages are in use, 64 to a word, with the count of used pages before each
+// word: a page's rank among the used (or free) ones is then a popcount. Words of
+// kSegment pages at a time lie in LDS (tables beyond that are gone through again
+// segment by segment).
+constexpr int kWords = 4096;
+constexpr int64_t kSegment = 64 * kWords;
+
+class UsedPages {
+  public:
+    // All threads. Counts the pages in use.
+    __device__ int64_t count(const Pages &p)
+    {
+        int64_t used = 0;
+        for (int64_t at = 0; at < p.n_pages; at += kSegment)
+            used = load(p, at, used);
+        return used;
+    }
+
+    // All threads, after count(): used pages before `page`, which exists.
+    __device__ int64_t before(const Pages &p, int64_t page)
+    {
+        int64_t used = 0, at = 0;
+        if (p.n_pages > kSegment) {
+            for (; at + kSegment <= page; at += kSegment)
+                used = load(p, at, used);
+            load(p, at, used);
+        }
+        const int i = (int)(page - at);
+        return (int64_t)before_()[i >> 6] +
+               __popcll(masks_()[i >> 6] & ((1ull << (i & 63)) - 1));
+    }
+
+    // All threads, after count(): f(page, its count, used pages before it) of every
+    // page, neighbouring threads on neighbouring pages.
+    template <class F>
+    __device__ void each(const Pages &p, F f)
+    {
+        int64_t used = 0;
+        for (int64_t at = 0; at < p.n_pages; at += kSegment) {
+            if (p.n_pages > kSegment)
+                used = load(p, at, used);
+            const int n = (int)min(kSegment, p.n_pages - at);
+#pragma unroll 4
+            for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+                const uint64_t lower = masks_()[i >> 6] & ((1ull << (i & 63)) - 1);
+                f(at + i, p.refs[at + i], (int64_t)before_()[i >> 6] + __popcll(lower));
+            }
+        }
+    }
+
+  private:
+    __device__ static uint64_t *masks_()
+    {
+        __shared__ uint64_t masks[kWords];
+        return masks;
+    }
+    __device__ static int *before_()
+    {
+        __shared__ int before[kWords];
+        return before;
+    }
+
+    // The segment from page `at` on, `used` pages being in use before it; returns
+    // the count after it.
+    __device__ int64_t load(const Pages &p, int64_t at, int64_t used)
+    {
+        const int n = (int)min(kSegment, p.n_pages - at), words = (n + 63) / 64;
+        __syncthreads();  // the last segment's readers are done
+        constexpr int kAhead = 4;  // loads in flight of a thread
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        for (int w0 = wave; w0 < words; w0 += kWaves * kAhead) {
+            int r[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; k++)
+                r[k] = p.refs[at + min((w0 + k * kWaves) * 64 + lane, n - 1)];
+#pragma unroll
+            for (int k = 0; k < kAhead; k++) {
+                const int w = w0 + k * kWaves;
+                const uint64_t m = __ballot(w * 64 + lane < n && r[k] > 0);
+                if (lane == 0 && w < words)
+                    masks_()[w] = m;
+            }
+        }
+        __syncthreads();
+        constexpr int kPer = kWords / kPlanThreads;
+        int64_t mine = 0, all;
+        for (int w = threadIdx.x * kPer; w < min(words, (int)(threadIdx.x + 1) * kPer); w++)
+            mine += __popcll(masks_()[w]);
+        int64_t first = used + block_scan(mine, &all);
+        for (int w = threadIdx.x * kPer; w < min(words, (int)(threadIdx.x + 1) * kPer); w++) {
+            before_()[w] = (int)first;
+            first += __popcll(masks_()[w]);
+        }
+        __syncthreads();
+        return used + all;
+    }
+};
+
 // This thread's run of n items, in the threads' order.
 __device__ __forceinline__ void run_of(int64_t n, int64_t *lo, int64_t *hi)
 {
@@ -78,13 +183,6 @@ __device__ __forceinline__ void run_of(int64_t n, int64_t *lo, int64_t *hi)
     *lo = threadIdx.x * per < n ? threadIdx.x * per : n;
     *hi = *lo + per < n ? *lo + per : n;
 }
-
-struct Pages {
-    const int32_t *table, *lens, *refs;
-    int32_t *table_out, *lens_out, *refs_out;
-    int64_t stride, stride_out;
-    int n_pages, n_seqs, max_pages, page_size;
-};
 
 struct Extend {
     const int32_t *n_new;
@@ -104,53 +202,47 @@ struct Fork {
 };
 
 struct Wish {
-    int64_t have, need;
-    bool fits;  // the row holds the grown sequence
+    int have, need;  // pages
+    bool fits;       // the row holds the grown sequence
 };
+
+// Pages of n tokens, n below 2^32.
+__device__ __forceinline__ uint32_t pages_for(uint32_t n, int page_size)
+{
+    return n == 0 ? 0u : (n - 1) / (uint32_t)page_size + 1;
+}
 
 __device__ __forceinline__ Wish wish_of(const Pages &p, const Extend &e, int64_t s)
 {
-    const int64_t len = max(p.lens[s], 0), grown = len + max(e.n_new[s], 0);
+    const uint32_t len = max(p.lens[s], 0), grown = len + (uint32_t)max(e.n_new[s], 0);
     Wish w;
-    w.have = (len + p.page_size - 1) / p.page_size;
-    const int64_t want = (grown + p.page_size - 1) / p.page_size;
-    w.fits = grown == len || (want <= p.max_pages && grown <= 0x7fffffff);
-    w.need = w.fits ? want - w.have : 0;
+    w.have = (int)pages_for(len, p.page_size);
+    const uint32_t want = pages_for(grown, p.page_size);
+    w.fits = grown == len || (want <= (uint32_t)p.max_pages && grown <= 0x7fffffffu);
+    w.need = w.fits ? (int)want - w.have : 0;
     return w;
 }
 
-// Gives the free pages of rank below `granted` (each to become held once) and
-// lists them; returns nothing but what it wrote. base: this thread's first rank.
-__device__ __forceinline__ void give_pages(const Pages &p, int32_t *free_list, int64_t base,
+// Gives the free pages of rank below `granted` (each is then held once) and
+// lists them.
+__device__ __forceinline__ void give_pages(const Pages &p, UsedPages &u, int32_t *free_list,
                                            int64_t granted)
 {
-    int64_t lo, hi;
-    run_of(p.n_pages, &lo, &hi);
-    for (int64_t i = lo; i < hi; i++) {
-        int r = p.refs[i];
-        if (r <= 0 && base < granted) {
-            free_list[base] = (int)i;
+    u.each(p, [&](int64_t i, int r, int64_t used_before) {
+        const int64_t rank = i - used_before;
+        if (r <= 0 && rank < granted) {
+            free_list[rank] = (int)i;
             r = 1;
-            base++;
         }
         p.refs_out[i] = r;
-    }
-}
-
-__device__ __forceinline__ int64_t count_free(const Pages &p, int64_t *base)
-{
-    int64_t lo, hi, mine = 0, n_free;
-    run_of(p.n_pages, &lo, &hi);
-    for (int64_t i = lo; i < hi; i++)
-        mine += p.refs[i] <= 0;
-    *base = block_scan(mine, &n_free);
-    return n_free;
+    });
 }
 
 __device__ void extend_plan(const Pages &p, const Extend &e)
 {
-    int64_t page_base, total, lo, hi, mine = 0;
-    const int64_t n_free = count_free(p, &page_base);
+    UsedPages pages;
+    int64_t total, lo, hi, mine = 0;
+    const int64_t n_free = p.n_pages - pages.count(p);
     run_of(p.n_seqs, &lo, &hi);
     for (int64_t s = lo; s < hi; s++)
         mine += wish_of(p, e, s).need;
@@ -164,8 +256,8 @@ __device__ void extend_plan(const Pages &p, const Extend &e)
         if (served && w.need > 0)
             granted = end;
         e.first[s] = served && w.need > 0 ? (int)rank : -1;
-        e.have[s] = (int)w.have;
-        e.need[s] = (int)w.need;
+        e.have[s] = w.have;
+        e.need[s] = w.need;
         p.lens_out[s] = served ? max(p.lens[s], 0) + max(e.n_new[s], 0) : p.lens[s];
         rank = end;
     }
@@ -174,7 +266,7 @@ __device__ void extend_plan(const Pages &p, const Extend &e)
     block_scan(refused, &all);
     if (threadIdx.x == 0)
         e.short_of[0] = (int)all;
-    give_pages(p, e.free_list, page_base, granted);
+    give_pages(p, pages, e.free_list, granted);
 }
 
 // Row s of the table, by one wave.
@@ -200,15 +292,16 @@ __device__ __forceinline__ int fork_length(const Pages &p, const Fork &f, int64_
 
 __device__ void fork_plan(const Pages &p, const Fork &f)
 {
-    int64_t page_base, total, lo, hi, mine = 0;
-    const int64_t n_free = count_free(p, &page_base);
+    UsedPages pages;
+    int64_t total, lo, hi, mine = 0;
+    const int64_t n_free = p.n_pages - pages.count(p);
     run_of(f.n, &lo, &hi);
     for (int64_t i = lo; i < hi; i++) {
         const int len = fork_length(p, f, i);
         mine += len > 0 && len % p.page_size != 0;
     }
     const int64_t rank0 = block_scan(mine, &total);
-    give_pages(p, f.free_list, page_base, total < n_free ? total : n_free);
+    give_pages(p, pages, f.free_list, total < n_free ? total : n_free);
     for (int64_t s = threadIdx.x; s < p.n_seqs; s += kPlanThreads)
         f.fork_of[s] = -1;
     __syncthreads();
@@ -297,31 +390,22 @@ __device__ void copy_refs(const Pages &p, int64_t first, int64_t step)
 
 __device__ void compact_plan(const Pages &p, int32_t *page_map, int32_t *moves)
 {
-    int64_t lo, hi, mine = 0, used;
-    run_of(p.n_pages, &lo, &hi);
-    for (int64_t i = lo; i < hi; i++)
-        mine += p.refs[i] > 0;
-    // used pages before this thread's run; free ones are the rest of them
-    int64_t u = block_scan(mine, &used);
-    int64_t used_before_cut = 0;  // of the pages below `used`
-    for (int64_t i = lo; i < hi && i < used; i++)
-        used_before_cut += p.refs[i] > 0;
-    int64_t low_used;
-    block_scan(used_before_cut, &low_used);
-    for (int64_t i = lo; i < hi; i++) {
-        const int r = p.refs[i];
+    UsedPages pages;
+    const int64_t used = pages.count(p);
+    // used pages below the cut; the rest of them move
+    const int64_t low_used = used < p.n_pages ? pages.before(p, used) : used;
+    const int64_t n = used - low_used;
+    pages.each(p, [&](int64_t i, int r, int64_t u) {
         if (r > 0) {
             if (i >= used)
                 moves[3 * (u - low_used)] = (int)i;
-            u++;
         } else if (i < used) {
             moves[3 * (i - u) + 1] = (int)i;  // i - u free pages lie before i
         }
         page_map[i] = (int)i;
         p.refs_out[i] = r;
-    }
+    });
     __syncthreads();
-    const int64_t n = used - low_used;
     for (int64_t m = threadIdx.x; m < p.n_pages / 2; m += kPlanThreads) {
         if (m < n) {
             const int from = moves[3 * m], to = moves[3 * m + 1];
@@ -428,10 +512,10 @@ Pages pages_of(const bqm_kv_pages *in, const bqm_kv_pages *out, int page_size)
 // ---- copies -----------------------------------------------------------------
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyUnroll = 8;
+constexpr int kCopyUnroll = 4;
 
 struct CopyArgs {
-    uint4 *k, *v;                           // a 16-byte piece is 8 values
+    u32x4 *k, *v;                           // a 16-byte piece is 8 values
     int64_t layer, page, token, head;       // strides in pieces
     const int32_t *moves;
     int64_t n_pages;
@@ -450,15 +534,15 @@ __global__ __launch_bounds__(kCopyThreads) void copy_pages_kernel(CopyArgs a, in
     if (tokens <= 0 || (uint64_t)(int64_t)from >= (uint64_t)a.n_pages ||
         (uint64_t)(int64_t)to >= (uint64_t)a.n_pages || from == to)
         return;
-    uint4 *base = (blockIdx.y & 1 ? a.v : a.k) + (int64_t)(blockIdx.y >> 1) * a.layer;
-    const uint4 *src = base + from * a.page;
-    uint4 *dst = base + to * a.page;
+    u32x4 *base = (blockIdx.y & 1 ? a.v : a.k) + (int64_t)(blockIdx.y >> 1) * a.layer;
+    const u32x4 *src = base + from * a.page;
+    u32x4 *dst = base + to * a.page;
     const int row = a.n_heads * a.pieces;
     const int64_t all = (int64_t)tokens * row;
     const int64_t step = (int64_t)shares * kCopyThreads;
     for (int64_t i0 = (int64_t)share * kCopyThreads + threadIdx.x; i0 < all;
          i0 += step * kCopyUnroll) {
-        uint4 x[kCopyUnroll];
+        u32x4 x[kCopyUnroll];
         int64_t at[kCopyUnroll];
 #pragma unroll
         for (int u = 0; u < kCopyUnroll; u++) {
@@ -472,13 +556,13 @@ __global__ __launch_bounds__(kCopyThreads) void copy_pages_kernel(CopyArgs a, in
                     const int r = (int)(i - t * row), h = r / a.pieces;
                     at[u] = t * a.token + h * a.head + (r - h * a.pieces);
                 }
-                x[u] = src[at[u]];
+                x[u] = __builtin_nontemporal_load(src + at[u]);
             }
         }
 #pragma unroll
         for (int u = 0; u < kCopyUnroll; u++)
             if (at[u] >= 0)
-                dst[at[u]] = x[u];
+                __builtin_nontemporal_store(x[u], dst + at[u]);
     }
 }
 
@@ -533,13 +617,13 @@ int launch_kv_compact(const bqm_kv_pages *in, const bqm_kv_pages *out, int page_
 int launch_kv_copy_pages(const bqm_kv_cache *c, const int32_t *moves, int64_t n,
                          hipStream_t stream)
 {
-    const CopyArgs a = {static_cast<uint4 *>(c->k), static_cast<uint4 *>(c->v),
+    const CopyArgs a = {static_cast<u32x4 *>(c->k), static_cast<u32x4 *>(c->v),
                         c->layer_stride / 8, c->page_stride / 8, c->token_stride / 8,
                         c->head_stride / 8, moves, c->n_pages,
                         c->page_size, c->n_heads, c->head_dim / 8};
     const bool flat = (c->n_heads == 1 || c->head_stride == c->head_dim) &&
                       (c->page_size == 1 || c->token_stride == (int64_t)c->n_heads * c->head_dim);
-    // a share of a page is at least 32 KiB (8 pieces a thread)
+    // a share of a page is at least 16 KiB (4 pieces a thread)
     const int64_t pieces = (int64_t)c->page_size * c->n_heads * a.pieces;
     const int shares =
         (int)std::clamp<int64_t>(pieces / (kCopyThreads * kCopyUnroll), 1, 64);
