@@ -1,6 +1,7 @@
 """Build step for the HIP library: compiles every ``csrc/*.hip`` source for
 gfx950 into ``bit_quantized_mat_amd/libbqm.so`` (in-tree, so the built
-library travels with the source tree)."""
+library travels with the source tree), and the Python binding of its attention
+side, ``binding/attention.cpp``, into ``_attention.so`` beside it."""
 import concurrent.futures
 import glob
 import os
@@ -25,6 +26,11 @@ FLAGS = [
     "-ffp-contract=off",
     "-Wall", "-Wno-unused-function",
 ]
+
+
+BINDING_SRC = os.path.join(HERE, "binding", "attention.cpp")
+BINDING_LIB = os.path.join(HERE, "_attention.so")
+CXX = os.environ.get("CXX", "g++")
 
 
 def sources():
@@ -60,11 +66,44 @@ def _compile(srcs, out, verbose):
                 os.remove(o)
 
 
+def _compile_binding(obj, verbose):
+    """The binding's object: host code against torch's headers."""
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    inc = [root, os.path.join(root, "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    _run([CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
+          "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+          *[a for i in inc for a in ("-isystem", i)], "-c", BINDING_SRC, "-o", obj], verbose)
+
+
+def _link_binding(obj, verbose):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_LIB + ".tmp%d" % os.getpid()
+    _run([CXX, "-shared", obj, "-o", tmp, "-L" + HERE, "-l:" + os.path.basename(LIB), "-L" + lib,
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib],
+         verbose)
+    os.replace(tmp, BINDING_LIB)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile the library and the benchmark's probe library (always
-    recompiles); returns the library path."""
-    _compile(sources(), LIB, verbose)
-    _compile([PROBE_SRC], PROBE_LIB, verbose)
+    """Compile the library, its Python binding and the benchmark's probe
+    library (always recompiles); returns the library path."""
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    obj = os.path.join(OBJ_DIR, "attention_binding.%d.o" % os.getpid())
+    try:
+        with concurrent.futures.ThreadPoolExecutor(1) as ex:
+            binding = ex.submit(_compile_binding, obj, verbose)
+            _compile(sources(), LIB, verbose)
+            _compile([PROBE_SRC], PROBE_LIB, verbose)
+            binding.result()
+        _link_binding(obj, verbose)
+    finally:
+        if os.path.exists(obj):
+            os.remove(obj)
     return LIB
 
 
