@@ -95,12 +95,16 @@ __device__ __forceinline__ int row_hi(const AttnArgs &a, int kv_len, int pos)
 
 __device__ __forceinline__ void load_sequence(const AttnArgs &a, int b, Tile &t)
 {
+    // the same in all lanes: read once, kept in scalar registers
+    const int start = __builtin_amdgcn_readfirstlane(a.q_starts[b]);
+    const int next = __builtin_amdgcn_readfirstlane(a.q_starts[b + 1]);
+    const int len = __builtin_amdgcn_readfirstlane(a.kv_lens[b]);
     t.seq = b;
-    t.q0 = min(max((int64_t)a.q_starts[b], (int64_t)0), a.total_q);
-    t.q_len = (int)min(max((int64_t)a.q_starts[b + 1] - t.q0, (int64_t)0), a.total_q - t.q0);
+    t.q0 = min(max((int64_t)start, (int64_t)0), a.total_q);
+    t.q_len = (int)min(max((int64_t)next - t.q0, (int64_t)0), a.total_q - t.q0);
     t.rows = t.q_len * a.group;
     const int64_t room = min((int64_t)a.max_pages * a.page_size, (int64_t)a.max_kv);
-    t.kv_len = (int)min((int64_t)max(a.kv_lens[b], 0), room);
+    t.kv_len = (int)min((int64_t)max(len, 0), room);
 }
 
 template <int M>
@@ -147,7 +151,7 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &a, int x, Tile &t)
     auto first = [&](int start, int b) { return (int64_t)start * a.group / M + b; };
     const int b = find_sequence(a, x, first);
     load_sequence(a, b, t);
-    t.tile = x - (int)first(a.q_starts[b], b);
+    t.tile = x - (int)first(__builtin_amdgcn_readfirstlane(a.q_starts[b]), b);
     if (t.tile < 0 || (int64_t)t.tile * M >= t.rows)
         return false;
     load_range<M>(a, t);
@@ -230,11 +234,28 @@ __device__ __forceinline__ void store4(O *p, f32x4 v)
     *reinterpret_cast<o4 *>(p) = __builtin_convertvector(v, o4);
 }
 
-// WM waves share a key tile, 32 rows each; WK such groups take every WK-th tile
-// of 32 * NT tokens and are joined at the end.
-template <int DP, int WM, int WK, int NT>
+// The order of instructions the scheduler keeps (it would read each operand
+// right before its product, and wait): operands a few products ahead.
+constexpr int kSchedMatrix = 0x8, kSchedLdsRead = 0x100;
+
+template <int READS, int RT>
+__device__ __forceinline__ void order_scores()
+{
+    constexpr int kAhead = READS < 4 ? READS : 4;
+    __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, kAhead, 0);
+#pragma unroll
+    for (int i = 0; i < READS - kAhead; i++) {
+        __builtin_amdgcn_sched_group_barrier(kSchedMatrix, RT, 0);
+        __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(kSchedMatrix, kAhead * RT, 0);
+}
+
+// WM waves share a key tile, RT tiles of 32 rows each; WK such groups take every
+// WK-th tile of 32 * NT tokens and are joined at the end.
+template <int DP, int WM, int WK, int NT, int RT>
 struct Shape {
-    static constexpr int M = 32 * WM;
+    static constexpr int M = 32 * RT * WM;
     static constexpr int kThreads = 64 * WM * WK;
     static constexpr int TK = 32 * NT;
     static constexpr int kPieces = DP / 8;                     // of a row
@@ -250,13 +271,17 @@ struct Shape {
     static constexpr int kLds = kStage > kJoin ? kStage : kJoin;
 };
 
-template <class T, class O, int DP, int WM, int WK, int NT>
-__global__ __launch_bounds__(64 * WM *WK, DP > 128 ? 1 : 2) void attention_kernel(AttnArgs a)
+// AHEAD: the scores of a tile are formed while the weights of the one before are
+// (matrix and vector units side by side in one wave); WAVES: a SIMD's.
+template <class T, class O, int DP, int WM, int WK, int NT, int RT, bool AHEAD, int WAVES>
+__global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs a)
 {
-    typedef Shape<DP, WM, WK, NT> S;
+    typedef Shape<DP, WM, WK, NT, RT> S;
     typedef typename Operand<T>::type Op;
+    typedef f32x16 Scores[RT][NT];
     extern __shared__ char lds[];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % WM, wk = wave / WM;
     const int half = lane >> 5, col = lane & 31;
 
@@ -276,39 +301,47 @@ __global__ __launch_bounds__(64 * WM *WK, DP > 128 ? 1 : 2) void attention_kerne
     const int c0 = t.begin + split * a.chunk;
     const int c1 = parts > 1 ? min(t.end, c0 + a.chunk) : t.end;
 
-    // this lane's row; rows past the end repeat the last and store nothing
-    const int r = t.tile * S::M + wm * 32 + col;
-    const int rc = min(r, t.rows - 1), tok = rc / a.group, g = rc - tok * a.group;
-    const int pos = t.kv_len - t.q_len + tok;
-    const int lo = max(row_lo(a, pos), c0), hi = min(row_hi(a, t.kv_len, pos), c1);
-    // rows ascend with the lanes, and so do lo and hi
-    const int lo_first = __builtin_amdgcn_readlane(lo, 0);
-    const int lo_last = __builtin_amdgcn_readlane(lo, 31);
-    const int hi_first = __builtin_amdgcn_readlane(hi, 0);
-    const int hi_last = __builtin_amdgcn_readlane(hi, 31);
-    const int64_t q_row = t.q0 + tok;
-    const int q_head = head * a.group + g;
-
-    Op qf[DP / 16];
-    {
+    // this lane's rows; rows past the end repeat the last and store nothing
+    const int row_first = t.tile * S::M + wm * RT * 32;
+    int lo[RT], hi[RT];               // tokens the row sees
+    int lo_last[RT], hi_first[RT];    // of the tile's 32 rows: they ascend with the lanes
+    int64_t out_row[RT];
+    Op qf[RT][DP / 16];
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        const int rc = min(row_first + rt * 32 + col, t.rows - 1);
+        const int tok = rc / a.group, g = rc - tok * a.group;
+        const int pos = t.kv_len - t.q_len + tok;
+        lo[rt] = max(row_lo(a, pos), c0);
+        hi[rt] = min(row_hi(a, t.kv_len, pos), c1);
+        lo_last[rt] = __builtin_amdgcn_readlane(lo[rt], 31);
+        hi_first[rt] = __builtin_amdgcn_readlane(hi[rt], 0);
+        const int64_t q_row = t.q0 + tok;
+        const int q_head = head * a.group + g;
+        out_row[rt] = q_row * a.n_q_heads + q_head;
         const T *qp = static_cast<const T *>(a.q) + q_row * a.q_token + q_head * a.q_head;
 #pragma unroll
         for (int kk = 0; kk < DP / 16; kk++) {
             const int d = 16 * kk + 8 * half;
             const T *p = d < a.dim ? qp + d : reinterpret_cast<const T *>(&kZeros);
-            qf[kk] = *reinterpret_cast<const Op *>(p);
+            qf[rt][kk] = *reinterpret_cast<const Op *>(p);
         }
     }
+    const int lo_first = __builtin_amdgcn_readlane(lo[0], 0);
+    const int hi_last = __builtin_amdgcn_readlane(hi[RT - 1], 31);
 
     // ---- staging: this group's tiles are n = 0, 1, ..: tokens t0(n) = c0 + (n WK + wk) TK
     const int iters = (c1 - c0 + WK * S::TK - 1) / (WK * S::TK);
+    const int t00 = c0 + wk * S::TK;
     const int gt = wm * 64 + lane;  // thread of the group
     const int piece = gt % S::kPieces, row0 = gt / S::kPieces;
     const bool piece_ok = piece * 8 < a.dim;
     const piece_ptr kp = (piece_ptr)a.k + (uint64_t)head * a.c_head + piece;
     const piece_ptr vp = (piece_ptr)a.v + (uint64_t)head * a.c_head + piece;
     const piece_ptr zeros = (piece_ptr)&kZeros;
-    char *buf = lds + wk * S::kTile * S::kBufs;
+    char *const buf = lds + wk * S::kTile * S::kBufs;
+    auto k_of = [&](int n) { return buf + (S::kBufs > 1 ? n & 1 : 0) * S::kTile; };
+    auto v_of = [&](int n) { return k_of(n) + S::TK * S::KS; };
     const int32_t *table = a.pages + t.seq * a.pages_stride;
 
     // lane l looks up token l of the tile to be read next; page and place advance
@@ -326,146 +359,242 @@ __global__ __launch_bounds__(64 * WM *WK, DP > 128 ? 1 : 2) void attention_kerne
             cpage++;
         }
     };
+    auto place_of = [&] {  // of lane l's token, in pieces; ~0: none
+        return (uint32_t)page_id < (uint32_t)a.n_pages
+                   ? (uint32_t)page_id * a.c_page + (uint32_t)place * a.c_token
+                   : 0xffffffffu;
+    };
     u32x4 kr[S::kLoads], vr[S::kLoads];
-    auto load_tile = [&] {
-        const uint32_t mine = (uint32_t)page_id < (uint32_t)a.n_pages
-                                  ? (uint32_t)page_id * a.c_page + (uint32_t)place * a.c_token
-                                  : 0xffffffffu;
+    auto load = [&](u32x4 (&r)[S::kLoads], piece_ptr base, uint32_t mine) {
 #pragma unroll
         for (int i = 0; i < S::kLoads; i++) {
             const uint32_t off = __shfl(mine, row0 + i * S::kRowsPerLoad, 64);
-            const bool ok = piece_ok && off != 0xffffffffu;
-            kr[i] = *(ok ? kp + off : zeros);
-            vr[i] = *(ok ? vp + off : zeros);
+            r[i] = *(piece_ok && off != 0xffffffffu ? base + off : zeros);
         }
+    };
+    auto store_k = [&](char *to) {
+#pragma unroll
+        for (int i = 0; i < S::kLoads; i++)
+            *reinterpret_cast<u32x4 *>(to + (row0 + i * S::kRowsPerLoad) * S::KS + piece * 16) = kr[i];
     };
     bool careful = false;  // keep infinities and NaN of V out of the products
-    auto store_tile = [&](char *b) {
+    auto store_v = [&](char *to) {
 #pragma unroll
         for (int i = 0; i < S::kLoads; i++) {
-            const int row = row0 + i * S::kRowsPerLoad;
             if (careful)
                 vr[i] = finite_only<T>(vr[i]);
-            *reinterpret_cast<u32x4 *>(b + row * S::KS + piece * 16) = kr[i];
-            *reinterpret_cast<u32x4 *>(b + S::TK * S::KS + row * S::VS + piece * 16) = vr[i];
+            *reinterpret_cast<u32x4 *>(to + (row0 + i * S::kRowsPerLoad) * S::VS + piece * 16) = vr[i];
         }
     };
 
-    f32x16 acc[DP / 32];
-    float top, sum;  // of this lane's row; sum over its own tokens
+    f32x16 acc[RT][DP / 32];
+    float top[RT], sum[RT];  // of this lane's rows; sum over its own tokens
 
-    auto compute = [&](const char *b, int t0) {
-        if (t0 >= hi_last || t0 + S::TK <= lo_first)
-            return;  // no row of this wave sees the tile
-        f32x16 s[NT];
-        const char *kb = b + col * S::KS + half * 16;
+    // whether a row of this wave sees the tile at t0
+    auto seen = [&](int t0) { return t0 < hi_last && t0 + S::TK > lo_first; };
+    auto scores = [&](Scores &s, const char *k) {
+        const char *kb = k + col * S::KS + half * 16;
 #pragma unroll
         for (int tt = 0; tt < NT; tt++) {
-            s[tt] = f32x16{};
 #pragma unroll
-            for (int kk = 0; kk < DP / 16; kk++)
-                s[tt] = mfma(*reinterpret_cast<const Op *>(kb + tt * 32 * S::KS + kk * 32), qf[kk],
-                             s[tt]);
+            for (int rt = 0; rt < RT; rt++)
+                s[rt][tt] = f32x16{};
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; kk++) {
+                const Op f = *reinterpret_cast<const Op *>(kb + tt * 32 * S::KS + kk * 32);
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++)
+                    s[rt][tt] = mfma(f, qf[rt][kk], s[rt][tt]);
+            }
         }
-        const bool whole = t0 >= lo_last && t0 + S::TK <= hi_first;
-        if (!whole) {
+        order_scores<NT * DP / 16, RT>();
+    };
+    // the rows' maxima: masks the scores, brings accumulators to a new base
+    auto settle = [&](Scores &s, float (&base)[RT], int t0) {
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+            if (!(t0 >= lo_last[rt] && t0 + S::TK <= hi_first[rt])) {
+#pragma unroll
+                for (int tt = 0; tt < NT; tt++)
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        const int j = t0 + tt * 32 + (i / 4) * 8 + half * 4 + i % 4;
+                        s[rt][tt][i] = j >= lo[rt] && j < hi[rt] ? s[rt][tt][i] : -INFINITY;
+                    }
+            }
+            float m = -INFINITY;
 #pragma unroll
             for (int tt = 0; tt < NT; tt++)
-#pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const int j = t0 + tt * 32 + (i / 4) * 8 + half * 4 + i % 4;
-                    s[tt][i] = j >= lo && j < hi ? s[tt][i] : -INFINITY;
-                }
-        }
-        float m = -INFINITY;
-#pragma unroll
-        for (int tt = 0; tt < NT; tt++)
-#pragma unroll
-            for (int i = 0; i < 16; i++)
-                m = fmaxf(m, s[tt][i]);
-        m = pair_max(m) * a.scale_log2;
-        // The weights' base follows the maximum only when that has grown by a
-        // factor of 2^8: sums and weights (up to 256, the same relative rounding
-        // in either type) have room for it, and most tiles pass without scaling
-        // the accumulators.
-        if (__any(m > top + 8.0f)) {
-            const float grown = fmaxf(m, top);
-            const float back = top == -INFINITY ? 0.0f : exp2_fast(top - grown);
-            top = grown;
-            sum *= back;
-#pragma unroll
-            for (int dt = 0; dt < DP / 32; dt++)
 #pragma unroll
                 for (int i = 0; i < 16; i++)
-                    acc[dt][i] *= back;
-        }
-        const float base = top == -INFINITY ? 0.0f : top;  // nothing seen yet
-        Op p[NT][2];
+                    m = fmaxf(m, s[rt][tt][i]);
+            m = pair_max(m) * a.scale_log2;
+            // The weights' base follows the maximum only when that has grown by a
+            // factor of 2^8: sums and weights (up to 256, the same relative
+            // rounding in either type) have room for it, and most tiles pass
+            // without scaling the accumulators.
+            if (__any(m > top[rt] + 8.0f)) {
+                const float grown = fmaxf(m, top[rt]);
+                const float back = top[rt] == -INFINITY ? 0.0f : exp2_fast(top[rt] - grown);
+                top[rt] = grown;
+                sum[rt] *= back;
 #pragma unroll
-        for (int tt = 0; tt < NT; tt++)
+                for (int dt = 0; dt < DP / 32; dt++)
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-                f32x8 e;
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    e[i] = exp2_fast(fmaf(s[tt][8 * c + i], a.scale_log2, -base));
-                    sum += e[i];
-                }
-                // rounded to the cache's type: the matrix cores take no wider operand
-                p[tt][c] = __builtin_convertvector(e, Op);
+                    for (int i = 0; i < 16; i++)
+                        acc[rt][dt][i] *= back;
             }
+            base[rt] = top[rt] == -INFINITY ? 0.0f : top[rt];  // nothing seen yet
+        }
+    };
+    // Weights and products, 16 tokens at a time. Between the products of 16 tokens
+    // go the exponentials and the operand reads of the next 16, in this order: the
+    // scheduler left alone puts each read right before its product and waits.
+    auto product = [&](const Scores &s, const float (&base)[RT], const char *v) {
+        constexpr int kTiles = DP / 32, kChunks = 2 * NT, kShare = 8 / kTiles;
         // 16 lanes read 4 tokens x 16 values; lane l gets value l of the 4
-        const char *vb = b + S::TK * S::KS + (half * 4 + (lane & 15) / 4) * S::VS +
-                         ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-        auto v_frag = [&](int dt, int tt, int c) {
+        const char *vb = v + (half * 4 + (lane & 15) / 4) * S::VS + ((lane >> 4) & 1) * 32 +
+                         (lane & 3) * 8;
+        auto read = [&](int c, int dt) {
             typedef __attribute__((address_space(3))) s16x4 *lp;
-            const char *at = vb + (tt * 32 + c * 16) * S::VS + dt * 64;
+            const char *at = vb + c * 16 * S::VS + dt * 64;
             const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at));
             const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at + 8 * S::VS));
-            return __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+            return __builtin_bit_cast(Op, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
         };
+        f32x8 e[RT];
+        auto weights = [&](int c, int first, int n) {
 #pragma unroll
-        for (int dt = 0; dt < DP / 32; dt++)
+            for (int rt = 0; rt < RT; rt++)
 #pragma unroll
-            for (int tt = 0; tt < NT; tt++)
+                for (int i = first; i < first + n; i++) {
+                    e[rt][i] = exp2_fast(fmaf(s[rt][c / 2][8 * (c % 2) + i], a.scale_log2, -base[rt]));
+                    sum[rt] += e[rt][i];
+                }
+        };
+        Op f[2][kTiles], p[RT];
 #pragma unroll
-                for (int c = 0; c < 2; c++)
-                    acc[dt] = mfma(__builtin_bit_cast(Op, v_frag(dt, tt, c)), p[tt][c], acc[dt]);
+        for (int dt = 0; dt < kTiles; dt++)
+            f[0][dt] = read(0, dt);
+        __builtin_amdgcn_sched_barrier(0);
+        weights(0, 0, 8);
+#pragma unroll
+        for (int c = 0; c < kChunks; c++) {
+            // rounded to the cache's type: the matrix cores take no wider operand
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++)
+                p[rt] = __builtin_convertvector(e[rt], Op);
+#pragma unroll
+            for (int dt = 0; dt < kTiles; dt++) {
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++)
+                    acc[rt][dt] = mfma(f[c % 2][dt], p[rt], acc[rt][dt]);
+                if (c + 1 < kChunks) {
+                    f[(c + 1) % 2][dt] = read(c + 1, dt);
+                    weights(c + 1, dt * kShare, kShare);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
     };
 
-    const int t00 = c0 + wk * S::TK;
     for (;;) {
         ct = t00 + lane % S::TK;
         cpage = ct / a.page_size;
         cplace = ct % a.page_size;
 #pragma unroll
-        for (int dt = 0; dt < DP / 32; dt++)
-            acc[dt] = f32x16{};
-        top = -INFINITY;
-        sum = 0.0f;
+        for (int rt = 0; rt < RT; rt++) {
+#pragma unroll
+            for (int dt = 0; dt < DP / 32; dt++)
+                acc[rt][dt] = f32x16{};
+            top[rt] = -INFINITY;
+            sum[rt] = 0.0f;
+        }
         look_up();
-        load_tile();
-        look_up();
-        if constexpr (S::kBufs == 1) {
-            // each wave has its own tile: no barrier, the next tile loads into
-            // registers while this one is used
-            for (int n = 0; n < iters; n++) {
-                store_tile(buf);
-                load_tile();
-                look_up();
-                compute(buf, t00 + n * WK * S::TK);
-            }
-        } else {
-            store_tile(buf);
-            load_tile();
+        if constexpr (AHEAD) {
+            // K(n + 2) and V(n + 1) go to LDS while S(n + 1) and the products with
+            // V(n) are formed; the loads behind them run one tile further ahead
+            uint32_t v_place = place_of();
+            load(kr, kp, v_place);
+            look_up();
+            store_k(k_of(0));
+            load(vr, vp, v_place);
+            v_place = place_of();
+            load(kr, kp, v_place);
+            look_up();
+            store_k(k_of(1));
+            store_v(v_of(0));
+            load(vr, vp, v_place);
+            v_place = place_of();
+            load(kr, kp, v_place);
             look_up();
             __syncthreads();
-            for (int n = 0; n < iters; n++) {
-                store_tile(buf + ((n + 1) & 1) * S::kTile);
-                load_tile();
+            Scores s[2];
+            scores(s[0], k_of(0));
+            __syncthreads();
+            auto step = [&](int n, Scores &now, Scores &next) {
+                store_k(k_of(n));
+                store_v(v_of(n + 1));
+                load(vr, vp, v_place);
+                v_place = place_of();
+                load(kr, kp, v_place);
                 look_up();
-                compute(buf + (n & 1) * S::kTile, t00 + n * WK * S::TK);
+                const int t0 = t00 + n * WK * S::TK;
+                if (seen(t0 + WK * S::TK) || seen(t0)) {
+                    float base[RT];
+                    scores(next, k_of(n + 1));
+                    settle(now, base, t0);
+                    product(now, base, v_of(n));
+                }
                 __syncthreads();
+            };
+            int n = 0;
+            for (; n + 1 < iters; n += 2) {
+                step(n, s[0], s[1]);
+                step(n + 1, s[1], s[0]);
+            }
+            if (n < iters)
+                step(n, s[0], s[1]);
+        } else {
+            auto load_both = [&] {
+                const uint32_t mine = place_of();
+                load(kr, kp, mine);
+                load(vr, vp, mine);
+                look_up();
+            };
+            auto store_both = [&](int n) {
+                store_k(k_of(n));
+                store_v(v_of(n));
+            };
+            auto compute = [&](int n) {
+                const int t0 = t00 + n * WK * S::TK;
+                if (!seen(t0))
+                    return;
+                Scores s;
+                float base[RT];
+                scores(s, k_of(n));
+                settle(s, base, t0);
+                product(s, base, v_of(n));
+            };
+            load_both();
+            if constexpr (S::kBufs == 1) {
+                // each wave has its own tile: no barrier, the next tile loads into
+                // registers while this one is used
+                for (int n = 0; n < iters; n++) {
+                    store_both(n);
+                    load_both();
+                    compute(n);
+                }
+            } else {
+                store_both(0);
+                load_both();
+                __syncthreads();
+                for (int n = 0; n < iters; n++) {
+                    store_both(n + 1);
+                    load_both();
+                    compute(n);
+                    __syncthreads();
+                }
             }
         }
         // A weight of zero that met an infinity or NaN in a value its row does not
@@ -473,23 +602,27 @@ __global__ __launch_bounds__(64 * WM *WK, DP > 128 ? 1 : 2) void attention_kerne
         // do see them get their due at the end.
         bool odd = false;
 #pragma unroll
-        for (int dt = 0; dt < DP / 32; dt++)
+        for (int rt = 0; rt < RT; rt++)
 #pragma unroll
-            for (int i = 0; i < 16; i++)
-                odd |= !(fabsf(acc[dt][i]) < INFINITY);
+            for (int dt = 0; dt < DP / 32; dt++)
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    odd |= !(fabsf(acc[rt][dt][i]) < INFINITY);
         if (careful || !__syncthreads_or(odd))
             break;
         careful = true;
     }
-    sum = pair_sum(sum);
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++)
+        sum[rt] = pair_sum(sum[rt]);
 
-    const bool stores = r < t.rows;
-    const int64_t out_row = q_row * a.n_q_heads + q_head;
     const int64_t part_row = (int64_t)split * a.total_q * a.n_q_heads;
-    // 32-value tiles first, first + step, .. of the output (o(dt)): final, or this
-    // part's share with its maximum m and sum l
-    auto store_out = [&](auto o, int first, int step, float m, float l) {
+    // Of row tile rt, the output's 32-value tiles first, first + step, .. (o(dt)):
+    // final, or this part's share with its maximum m and sum l.
+    auto store_out = [&](int rt, auto o, int first, int step, float m, float l) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int n_rows = min(32, t.rows - row_first - rt * 32);  // that exist
+        const bool stores = col < n_rows;
 #pragma unroll
         for (int dt = first; dt < DP / 32; dt += step) {
             const f32x16 w = o(dt);
@@ -499,25 +632,25 @@ __global__ __launch_bounds__(64 * WM *WK, DP > 128 ? 1 : 2) void attention_kerne
                 const int d = dt * 32 + c * 8 + half * 4;
                 if (stores && d < a.dim) {
                     if (parts > 1)
-                        store4(a.part + (part_row + out_row) * a.dim + d, v);
+                        store4(a.part + (part_row + out_row[rt]) * a.dim + d, v);
                     else
-                        store4(static_cast<O *>(a.out) + out_row * a.dim + d, v * inv);
+                        store4(static_cast<O *>(a.out) + out_row[rt] * a.dim + d, v * inv);
                 }
             }
         }
         if (stores && parts > 1 && first == 0 && half == 0)
-            a.part_ml[part_row + out_row] = make_float2(m, l);
+            a.part_ml[part_row + out_row[rt]] = make_float2(m, l);
         if (!careful)
             return;
         __threadfence_block();  // the rows' stores above come first
 #pragma unroll 1
-        for (int src = 0; src < min(32, t.rows - t.tile * S::M - wm * 32); src++) {
-            const int64_t at = __shfl(out_row, src, 64);
+        for (int src = 0; src < n_rows; src++) {
+            const int64_t at = __shfl(out_row[rt], src, 64);
             const int64_t tq = at / a.n_q_heads;
             const T *q = static_cast<const T *>(a.q) + tq * a.q_token +
                          (at - tq * a.n_q_heads) * a.q_head;
             const float rm = __shfl(m, src, 64), rinv = __shfl(inv, src, 64);
-            const int rlo = __shfl(lo, src, 64), rhi = __shfl(hi, src, 64);
+            const int rlo = __shfl(lo[rt], src, 64), rhi = __shfl(hi[rt], src, 64);
 #pragma unroll 1
             for (int dt = first; dt < DP / 32; dt += step)
                 redo_row<T>(a, table, head, q, rlo, rhi, rm, dt * 32, min(32, a.dim - dt * 32),
@@ -531,36 +664,39 @@ __global__ __launch_bounds__(64 * WM *WK, DP > 128 ? 1 : 2) void attention_kerne
     };
 
     if constexpr (WK == 1) {
-        store_out([&](int dt) { return acc[dt]; }, 0, 1, top, sum);
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++)
+            store_out(rt, [&](int dt) { return acc[rt][dt]; }, 0, 1, top[rt], sum[rt]);
     } else {
         // join the groups: every wave brings its sums to the common maximum, and
         // each 32-value tile is added up by one of them
-        float *ml = reinterpret_cast<float *>(lds + WK * WM * (DP / 32) * 4096);
+        static_assert(WM == 1 && RT == 1, "the join is written for groups of one wave");
+        float *ml = reinterpret_cast<float *>(lds + WK * (DP / 32) * 4096);
         float *os = reinterpret_cast<float *>(lds);
-        static_assert(WM == 1, "the join is written for groups of one wave");
         __syncthreads();
         if (half == 0)
-            ml[wk * 32 + col] = top;
+            ml[wk * 32 + col] = top[0];
         __syncthreads();
         float m = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WK; w++)
             m = fmaxf(m, ml[w * 32 + col]);
-        const float f = top == -INFINITY ? (sum == sum ? 0.0f : 1.0f) : exp2_fast(top - m);
+        const float f = top[0] == -INFINITY ? (sum[0] == sum[0] ? 0.0f : 1.0f) : exp2_fast(top[0] - m);
         float *ls = ml + WK * 32;
         if (half == 0)
-            ls[wk * 32 + col] = sum * f;
+            ls[wk * 32 + col] = sum[0] * f;
 #pragma unroll
         for (int dt = 0; dt < DP / 32; dt++)
 #pragma unroll
             for (int i = 0; i < 16; i++)
-                os[((wk * (DP / 32) + dt) * 16 + i) * 64 + lane] = acc[dt][i] * f;
+                os[((wk * (DP / 32) + dt) * 16 + i) * 64 + lane] = acc[0][dt][i] * f;
         __syncthreads();
         float l = 0.0f;
 #pragma unroll
         for (int w = 0; w < WK; w++)
             l += ls[w * 32 + col];
         store_out(
+            0,
             [&](int dt) {
                 f32x16 o = {};
 #pragma unroll
@@ -657,12 +793,14 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a)
 // How a call is launched: which kernel, and into how many parts the tokens of a
 // tile are cut so that the card is full when there are few rows.
 struct Plan {
-    bool few_rows;      // 32 rows a workgroup, its four waves on tokens
+    int m;              // rows a workgroup: 32 (its four waves on tokens), 128 or 256
     int tiles, n_splits, chunk;
 };
 
 constexpr int kFewRows = 32;
 constexpr int64_t kWantedWorkgroups = 1024;  // four a compute unit, of which two run at once
+constexpr int64_t kWantedTiles = 512;        // the same for tiles of 128 rows, whose parts cost more
+constexpr int64_t kManyTiles = 512000;          // of 256 rows: two a compute unit
 constexpr int64_t kMostWorkgroups = 8192;    // most of them empty, where lengths differ
 constexpr int kLeastChunk = 256, kRaggedChunk = 1024;
 
@@ -670,18 +808,23 @@ Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads, int wi
 {
     const int64_t group = n_q_heads / c->n_heads;
     Plan p;
-    p.few_rows = std::min<int64_t>(b->max_q, b->total_q) * group <= kFewRows;
-    const int m = p.few_rows ? 32 : 128;
-    p.tiles = (int)(b->total_q * group / m + b->n_seqs);
+    const int64_t rows = b->total_q * group;
+    const bool few = std::min<int64_t>(b->max_q, b->total_q) * group <= kFewRows;
+    // 256 rows read each key tile once where 128 read it twice, but want enough
+    // of them to give every compute unit its workgroups
+    const bool many = c->head_dim <= 128 && rows / 256 * c->n_heads >= kManyTiles;
+    const int m = p.m = few ? 32 : many ? 256 : 128;
+    p.tiles = (int)(rows / m + b->n_seqs);
     // the most tokens a tile's rows see between them
     int64_t room = std::min<int64_t>(b->max_kv, (int64_t)b->max_pages * c->page_size);
     if (window > 0)
         room = std::min<int64_t>(room, (int64_t)window + m / group + 1);
     const int64_t workgroups = (int64_t)p.tiles * c->n_heads;
     // parts that fill the card, if every sequence had max_kv tokens
-    int64_t chunk = std::max<int64_t>(kLeastChunk, room * workgroups / kWantedWorkgroups);
+    int64_t chunk = std::max<int64_t>(
+        kLeastChunk, room * workgroups / (few ? kWantedWorkgroups : kWantedTiles));
     // with few rows a part costs little: cut long sequences among short ones too
-    if (p.few_rows)
+    if (few)
         chunk = std::min(chunk,
                          std::max<int64_t>(kRaggedChunk, room * workgroups / kMostWorkgroups));
     // no more parts than the workspace holds, whose size does not know the window
@@ -693,11 +836,11 @@ Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads, int wi
     return p;
 }
 
-template <class T, class O, int DP, int WM, int WK, int NT>
+template <class T, class O, int DP, int WM, int WK, int NT, int RT, bool AHEAD, int WAVES>
 int launch_shape(const AttnArgs &a, hipStream_t stream)
 {
-    typedef Shape<DP, WM, WK, NT> S;
-    auto kernel = attention_kernel<T, O, DP, WM, WK, NT>;
+    typedef Shape<DP, WM, WK, NT, RT> S;
+    auto kernel = attention_kernel<T, O, DP, WM, WK, NT, RT, AHEAD, WAVES>;
     allow_dynamic_lds(reinterpret_cast<const void *>(kernel), S::kLds);
     const int64_t grid = (int64_t)a.tiles * a.n_splits * a.n_heads;
     if (grid * S::kThreads >= 1ll << 32)
@@ -713,17 +856,25 @@ int launch_shape(const AttnArgs &a, hipStream_t stream)
     return check_launch();
 }
 
+template <class T, class O, int DP>
+int launch_rows(const AttnArgs &a, int m, hipStream_t stream)
+{
+    if (m == 32)
+        return launch_shape<T, O, DP, 1, 4, 1, 1, false, (DP > 128 ? 1 : 2)>(a, stream);
+    if constexpr (DP <= 128)
+        if (m == 256)
+            return launch_shape<T, O, DP, 4, 1, 2, 2, false, (DP > 64 ? 1 : 2)>(a, stream);
+    return launch_shape<T, O, DP, 4, 1, 2, 1, false, (DP > 128 ? 1 : 2)>(a, stream);
+}
+
 template <class T, class O>
-int launch_types(const AttnArgs &a, bool few_rows, hipStream_t stream)
+int launch_types(const AttnArgs &a, int m, hipStream_t stream)
 {
     if (a.dim <= 64)
-        return few_rows ? launch_shape<T, O, 64, 1, 4, 1>(a, stream)
-                        : launch_shape<T, O, 64, 4, 1, 2>(a, stream);
+        return launch_rows<T, O, 64>(a, m, stream);
     if (a.dim <= 128)
-        return few_rows ? launch_shape<T, O, 128, 1, 4, 1>(a, stream)
-                        : launch_shape<T, O, 128, 4, 1, 2>(a, stream);
-    return few_rows ? launch_shape<T, O, 256, 1, 4, 1>(a, stream)
-                    : launch_shape<T, O, 256, 4, 1, 2>(a, stream);
+        return launch_rows<T, O, 128>(a, m, stream);
+    return launch_rows<T, O, 256>(a, m, stream);
 }
 
 }  // namespace
@@ -781,10 +932,10 @@ int launch_paged_attention(const void *q, int64_t q_token, int64_t q_head, const
             a.part + (size_t)p.n_splits * b->total_q * n_q_heads * c->head_dim);
     if (c->dtype == BQM_DTYPE_F16)
         return out_dtype == BQM_DTYPE_F32
-                   ? launch_types<_Float16, float>(a, p.few_rows, stream)
-                   : launch_types<_Float16, _Float16>(a, p.few_rows, stream);
-    return out_dtype == BQM_DTYPE_F32 ? launch_types<__bf16, float>(a, p.few_rows, stream)
-                                      : launch_types<__bf16, __bf16>(a, p.few_rows, stream);
+                   ? launch_types<_Float16, float>(a, p.m, stream)
+                   : launch_types<_Float16, _Float16>(a, p.m, stream);
+    return out_dtype == BQM_DTYPE_F32 ? launch_types<__bf16, float>(a, p.m, stream)
+                                      : launch_types<__bf16, __bf16>(a, p.m, stream);
 }
 
 }  // namespace bqm
