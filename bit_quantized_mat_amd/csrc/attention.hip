@@ -184,49 +184,6 @@ __device__ __forceinline__ u32x4 finite_only(u32x4 v)
     return __builtin_bit_cast(u32x4, w & ((w & e) != e));
 }
 
-// Output values d0 .. d0 + dn - 1 (at most 32) of one row, token by token, from
-// those it sees alone; m is the row's maximum (log2). What comes out infinite or
-// NaN is stored: the row sees such a value, and the products left it out.
-template <class T, class Store>
-__device__ __forceinline__ void redo_row(const AttnArgs &a, const int32_t *table, int head,
-                                         const T *q, int lo, int hi, float m, int d0, int dn,
-                                         Store store)
-{
-    const int lane = threadIdx.x & 63;
-    const float base = m == -INFINITY ? 0.0f : m;
-    float o = 0.0f;
-#pragma unroll 1
-    for (int j0 = lo; j0 < hi; j0 += 64) {
-        const int j = j0 + lane;
-        float p = 0.0f;
-        int64_t at = -1;
-        if (j < hi) {
-            const int page = table[j / a.page_size];
-            float s = 0.0f;
-            if ((uint32_t)page < (uint32_t)a.n_pages) {
-                at = 8 * ((int64_t)page * a.c_page + (int64_t)(j % a.page_size) * a.c_token +
-                          (int64_t)head * a.c_head);
-                const T *k = reinterpret_cast<const T *>(a.k) + at;
-#pragma unroll 1
-                for (int d = 0; d < a.dim; d++)
-                    s = fmaf((float)q[d], (float)k[d], s);
-            }
-            p = (float)(T)exp2_fast(fmaf(s, a.scale_log2, -base));
-        }
-#pragma unroll 1
-        for (int e = 0; e < 64 && j0 + e < hi; e++) {
-            const float pe = __shfl(p, e, 64);
-            const int64_t ae = __shfl(at, e, 64);
-            if (ae < 0)
-                continue;
-            if (lane < dn)
-                o = fmaf(pe, (float)reinterpret_cast<const T *>(a.v)[ae + d0 + lane], o);
-        }
-    }
-    if (lane < dn && !(fabsf(o) < INFINITY))
-        store(d0 + lane, o);
-}
-
 template <class O>
 __device__ __forceinline__ void store4(O *p, f32x4 v)
 {
@@ -366,11 +323,14 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
     };
     u32x4 kr[S::kLoads], vr[S::kLoads];
     auto load = [&](u32x4 (&r)[S::kLoads], piece_ptr base, uint32_t mine) {
+        uint32_t off[S::kLoads];
 #pragma unroll
-        for (int i = 0; i < S::kLoads; i++) {
-            const uint32_t off = __shfl(mine, row0 + i * S::kRowsPerLoad, 64);
-            r[i] = *(piece_ok && off != 0xffffffffu ? base + off : zeros);
-        }
+        for (int i = 0; i < S::kLoads; i++)
+            off[i] = __shfl(mine, row0 + i * S::kRowsPerLoad, 64);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < S::kLoads; i++)
+            r[i] = *(piece_ok && off[i] != 0xffffffffu ? base + off[i] : zeros);
     };
     auto store_k = [&](char *to) {
 #pragma unroll
@@ -617,12 +577,49 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         sum[rt] = pair_sum(sum[rt]);
 
     const int64_t part_row = (int64_t)split * a.total_q * a.n_q_heads;
+    // What the careful products left out: infinities and NaN that rows of rt see
+    // (their weights are above zero, whatever they round to) are the output in
+    // their places.
+    auto left_out = [&](int rt, bool stores, int first, int step) {
+        auto value_of = [&](int j) -> const T * {  // of token j
+            const int page = j < c1 ? table[j / a.page_size] : -1;
+            if ((uint32_t)page >= (uint32_t)a.n_pages)
+                return nullptr;
+            return reinterpret_cast<const T *>(a.v) +
+                   8 * ((int64_t)page * a.c_page + (int64_t)(j % a.page_size) * a.c_token +
+                        (int64_t)head * a.c_head);
+        };
+        __threadfence_block();  // the rows' stores come first
+#pragma unroll 1
+        for (int d = first * 32 + half; d < a.dim; d += d % 32 < 30 ? 2 : 32 * step - 30) {
+            float o = 0.0f;
+#pragma unroll 1
+            for (int j0 = c0; j0 < c1; j0 += 64) {
+                const T *v = value_of(j0 + lane);
+                const int d_even = d - half;
+                const bool bad = v && !(fabsf((float)v[d_even]) < INFINITY &&
+                                        fabsf((float)v[d_even + 1]) < INFINITY);
+#pragma unroll 1
+                for (uint64_t bads = __ballot(bad); bads; bads &= bads - 1) {
+                    const int j = j0 + __builtin_ctzll(bads);
+                    const float x = (float)value_of(j)[d];
+                    if (j >= lo[rt] && j < hi[rt] && !(fabsf(x) < INFINITY))
+                        o += x;
+                }
+            }
+            if (stores && !(fabsf(o) < INFINITY)) {
+                if (parts > 1)
+                    a.part[(part_row + out_row[rt]) * a.dim + d] = o;
+                else
+                    static_cast<O *>(a.out)[out_row[rt] * a.dim + d] = (O)o;
+            }
+        }
+    };
     // Of row tile rt, the output's 32-value tiles first, first + step, .. (o(dt)):
     // final, or this part's share with its maximum m and sum l.
     auto store_out = [&](int rt, auto o, int first, int step, float m, float l) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int n_rows = min(32, t.rows - row_first - rt * 32);  // that exist
-        const bool stores = col < n_rows;
+        const bool stores = col < t.rows - row_first - rt * 32;
 #pragma unroll
         for (int dt = first; dt < DP / 32; dt += step) {
             const f32x16 w = o(dt);
@@ -640,27 +637,8 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         }
         if (stores && parts > 1 && first == 0 && half == 0)
             a.part_ml[part_row + out_row[rt]] = make_float2(m, l);
-        if (!careful)
-            return;
-        __threadfence_block();  // the rows' stores above come first
-#pragma unroll 1
-        for (int src = 0; src < n_rows; src++) {
-            const int64_t at = __shfl(out_row[rt], src, 64);
-            const int64_t tq = at / a.n_q_heads;
-            const T *q = static_cast<const T *>(a.q) + tq * a.q_token +
-                         (at - tq * a.n_q_heads) * a.q_head;
-            const float rm = __shfl(m, src, 64), rinv = __shfl(inv, src, 64);
-            const int rlo = __shfl(lo[rt], src, 64), rhi = __shfl(hi[rt], src, 64);
-#pragma unroll 1
-            for (int dt = first; dt < DP / 32; dt += step)
-                redo_row<T>(a, table, head, q, rlo, rhi, rm, dt * 32, min(32, a.dim - dt * 32),
-                            [&](int d, float v) {
-                                if (parts > 1)
-                                    a.part[(part_row + at) * a.dim + d] = v;
-                                else
-                                    static_cast<O *>(a.out)[at * a.dim + d] = (O)(v * rinv);
-                            });
-        }
+        if (careful && l == l)  // a sum of NaN has made the whole row so
+            left_out(rt, stores, first, step);
     };
 
     if constexpr (WK == 1) {
