@@ -195,24 +195,25 @@ __device__ __forceinline__ void store4(O *p, f32x4 v)
 // right before its product, and wait): operands a few products ahead.
 constexpr int kSchedMatrix = 0x8, kSchedLdsRead = 0x100;
 
-template <int READS, int RT>
-__device__ __forceinline__ void order_scores()
+// READS operand reads, PER of them a product.
+template <int READS, int PER = 1>
+__device__ __forceinline__ void order_reads()
 {
-    constexpr int kAhead = READS < 4 ? READS : 4;
-    __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, kAhead, 0);
+    constexpr int kProducts = READS / PER, kAhead = kProducts < 4 ? kProducts : 4;
+    __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, kAhead * PER, 0);
 #pragma unroll
-    for (int i = 0; i < READS - kAhead; i++) {
-        __builtin_amdgcn_sched_group_barrier(kSchedMatrix, RT, 0);
-        __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 1, 0);
+    for (int i = 0; i < kProducts - kAhead; i++) {
+        __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, PER, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(kSchedMatrix, kAhead * RT, 0);
+    __builtin_amdgcn_sched_group_barrier(kSchedMatrix, kAhead, 0);
 }
 
-// WM waves share a key tile, RT tiles of 32 rows each; WK such groups take every
-// WK-th tile of 32 * NT tokens and are joined at the end.
-template <int DP, int WM, int WK, int NT, int RT>
+// WM waves share a key tile, 32 rows each; WK such groups take every WK-th tile
+// of 32 * NT tokens and are joined at the end.
+template <int DP, int WM, int WK, int NT>
 struct Shape {
-    static constexpr int M = 32 * RT * WM;
+    static constexpr int M = 32 * WM;
     static constexpr int kThreads = 64 * WM * WK;
     static constexpr int TK = 32 * NT;
     static constexpr int kPieces = DP / 8;                     // of a row
@@ -228,14 +229,16 @@ struct Shape {
     static constexpr int kLds = kStage > kJoin ? kStage : kJoin;
 };
 
-// AHEAD: the scores of a tile are formed while the weights of the one before are
-// (matrix and vector units side by side in one wave); WAVES: a SIMD's.
-template <class T, class O, int DP, int WM, int WK, int NT, int RT, bool AHEAD, int WAVES>
+// WAVES: a SIMD's. With eight waves the workgroup is two halves out of step: while
+// the four waves of one (one a SIMD) are at their matrix products, the others are
+// at their softmax, and a barrier has them change places.
+template <class T, class O, int DP, int WM, int WK, int NT, int WAVES>
 __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs a)
 {
-    typedef Shape<DP, WM, WK, NT, RT> S;
+    typedef Shape<DP, WM, WK, NT> S;
     typedef typename Operand<T>::type Op;
-    typedef f32x16 Scores[RT][NT];
+    typedef f32x16 Scores[NT];
+    constexpr bool kHalves = WM == 8;
     extern __shared__ char lds[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -258,34 +261,30 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
     const int c0 = t.begin + split * a.chunk;
     const int c1 = parts > 1 ? min(t.end, c0 + a.chunk) : t.end;
 
-    // this lane's rows; rows past the end repeat the last and store nothing
-    const int row_first = t.tile * S::M + wm * RT * 32;
-    int lo[RT], hi[RT];               // tokens the row sees
-    int lo_last[RT], hi_first[RT];    // of the tile's 32 rows: they ascend with the lanes
-    int64_t out_row[RT];
-    Op qf[RT][DP / 16];
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++) {
-        const int rc = min(row_first + rt * 32 + col, t.rows - 1);
-        const int tok = rc / a.group, g = rc - tok * a.group;
-        const int pos = t.kv_len - t.q_len + tok;
-        lo[rt] = max(row_lo(a, pos), c0);
-        hi[rt] = min(row_hi(a, t.kv_len, pos), c1);
-        lo_last[rt] = __builtin_amdgcn_readlane(lo[rt], 31);
-        hi_first[rt] = __builtin_amdgcn_readlane(hi[rt], 0);
-        const int64_t q_row = t.q0 + tok;
-        const int q_head = head * a.group + g;
-        out_row[rt] = q_row * a.n_q_heads + q_head;
+    // this lane's row; rows past the end repeat the last and store nothing
+    const int row_first = t.tile * S::M + wm * 32;
+    const int rc = min(row_first + col, t.rows - 1);
+    const int tok = rc / a.group, g = rc - tok * a.group;
+    const int pos = t.kv_len - t.q_len + tok;
+    const int lo = max(row_lo(a, pos), c0), hi = min(row_hi(a, t.kv_len, pos), c1);
+    // rows ascend with the lanes, and so do lo and hi
+    const int lo_first = __builtin_amdgcn_readlane(lo, 0);
+    const int lo_last = __builtin_amdgcn_readlane(lo, 31);
+    const int hi_first = __builtin_amdgcn_readlane(hi, 0);
+    const int hi_last = __builtin_amdgcn_readlane(hi, 31);
+    const int64_t q_row = t.q0 + tok;
+    const int q_head = head * a.group + g;
+    const int64_t out_row = q_row * a.n_q_heads + q_head;
+    Op qf[DP / 16];
+    {
         const T *qp = static_cast<const T *>(a.q) + q_row * a.q_token + q_head * a.q_head;
 #pragma unroll
         for (int kk = 0; kk < DP / 16; kk++) {
             const int d = 16 * kk + 8 * half;
             const T *p = d < a.dim ? qp + d : reinterpret_cast<const T *>(&kZeros);
-            qf[rt][kk] = *reinterpret_cast<const Op *>(p);
+            qf[kk] = *reinterpret_cast<const Op *>(p);
         }
     }
-    const int lo_first = __builtin_amdgcn_readlane(lo[0], 0);
-    const int hi_last = __builtin_amdgcn_readlane(hi[RT - 1], 31);
 
     // ---- staging: this group's tiles are n = 0, 1, ..: tokens t0(n) = c0 + (n WK + wk) TK
     const int iters = (c1 - c0 + WK * S::TK - 1) / (WK * S::TK);
@@ -347,8 +346,8 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         }
     };
 
-    f32x16 acc[RT][DP / 32];
-    float top[RT], sum[RT];  // of this lane's rows; sum over its own tokens
+    f32x16 acc[DP / 32];
+    float top, sum;  // of this lane's row; sum over its own tokens
 
     // whether a row of this wave sees the tile at t0
     auto seen = [&](int t0) { return t0 < hi_last && t0 + S::TK > lo_first; };
@@ -356,102 +355,88 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         const char *kb = k + col * S::KS + half * 16;
 #pragma unroll
         for (int tt = 0; tt < NT; tt++) {
+            s[tt] = f32x16{};
 #pragma unroll
-            for (int rt = 0; rt < RT; rt++)
-                s[rt][tt] = f32x16{};
-#pragma unroll
-            for (int kk = 0; kk < DP / 16; kk++) {
-                const Op f = *reinterpret_cast<const Op *>(kb + tt * 32 * S::KS + kk * 32);
-#pragma unroll
-                for (int rt = 0; rt < RT; rt++)
-                    s[rt][tt] = mfma(f, qf[rt][kk], s[rt][tt]);
-            }
+            for (int kk = 0; kk < DP / 16; kk++)
+                s[tt] = mfma(*reinterpret_cast<const Op *>(kb + tt * 32 * S::KS + kk * 32), qf[kk],
+                             s[tt]);
         }
-        order_scores<NT * DP / 16, RT>();
+        order_reads<NT * DP / 16>();
     };
-    // the rows' maxima: masks the scores, brings accumulators to a new base
-    auto settle = [&](Scores &s, float (&base)[RT], int t0) {
-#pragma unroll
-        for (int rt = 0; rt < RT; rt++) {
-            if (!(t0 >= lo_last[rt] && t0 + S::TK <= hi_first[rt])) {
-#pragma unroll
-                for (int tt = 0; tt < NT; tt++)
-#pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        const int j = t0 + tt * 32 + (i / 4) * 8 + half * 4 + i % 4;
-                        s[rt][tt][i] = j >= lo[rt] && j < hi[rt] ? s[rt][tt][i] : -INFINITY;
-                    }
-            }
-            float m = -INFINITY;
+    // the row's maximum: masks the scores, brings the accumulators to a new base
+    auto settle = [&](Scores &s, int t0) {
+        if (!(t0 >= lo_last && t0 + S::TK <= hi_first)) {
 #pragma unroll
             for (int tt = 0; tt < NT; tt++)
 #pragma unroll
-                for (int i = 0; i < 16; i++)
-                    m = fmaxf(m, s[rt][tt][i]);
-            m = pair_max(m) * a.scale_log2;
-            // The weights' base follows the maximum only when that has grown by a
-            // factor of 2^8: sums and weights (up to 256, the same relative
-            // rounding in either type) have room for it, and most tiles pass
-            // without scaling the accumulators.
-            if (__any(m > top[rt] + 8.0f)) {
-                const float grown = fmaxf(m, top[rt]);
-                const float back = top[rt] == -INFINITY ? 0.0f : exp2_fast(top[rt] - grown);
-                top[rt] = grown;
-                sum[rt] *= back;
-#pragma unroll
-                for (int dt = 0; dt < DP / 32; dt++)
-#pragma unroll
-                    for (int i = 0; i < 16; i++)
-                        acc[rt][dt][i] *= back;
-            }
-            base[rt] = top[rt] == -INFINITY ? 0.0f : top[rt];  // nothing seen yet
+                for (int i = 0; i < 16; i++) {
+                    const int j = t0 + tt * 32 + (i / 4) * 8 + half * 4 + i % 4;
+                    s[tt][i] = j >= lo && j < hi ? s[tt][i] : -INFINITY;
+                }
         }
+        float m = -INFINITY;
+#pragma unroll
+        for (int tt = 0; tt < NT; tt++)
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                m = fmaxf(m, s[tt][i]);
+        m = pair_max(m) * a.scale_log2;
+        // The weights' base follows the maximum only when that has grown by a
+        // factor of 2^8: sums and weights (up to 256, the same relative rounding
+        // in either type) have room for it, and most tiles pass without scaling
+        // the accumulators.
+        if (__any(m > top + 8.0f)) {
+            const float grown = fmaxf(m, top);
+            const float back = top == -INFINITY ? 0.0f : exp2_fast(top - grown);
+            top = grown;
+            sum *= back;
+#pragma unroll
+            for (int dt = 0; dt < DP / 32; dt++)
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    acc[dt][i] *= back;
+        }
+        return top == -INFINITY ? 0.0f : top;  // nothing seen yet
+    };
+    constexpr int kTiles = DP / 32, kChunks = 2 * NT;  // of 32 values, of 16 tokens
+    auto weights = [&](f32x8 &e, const Scores &s, float base, int c, int first, int n) {
+#pragma unroll
+        for (int i = first; i < first + n; i++) {
+            e[i] = exp2_fast(fmaf(s[c / 2][8 * (c % 2) + i], a.scale_log2, -base));
+            sum += e[i];
+        }
+    };
+    // 16 lanes read 4 tokens x 16 values; lane l gets value l of the 4
+    const int v_lane = (half * 4 + (lane & 15) / 4) * S::VS + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+    auto read_v = [&](const char *v, int c, int dt) {
+        typedef __attribute__((address_space(3))) s16x4 *lp;
+        const char *at = v + v_lane + c * 16 * S::VS + dt * 64;
+        const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at));
+        const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at + 8 * S::VS));
+        return __builtin_bit_cast(Op, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
     };
     // Weights and products, 16 tokens at a time. Between the products of 16 tokens
     // go the exponentials and the operand reads of the next 16, in this order: the
     // scheduler left alone puts each read right before its product and waits.
-    auto product = [&](const Scores &s, const float (&base)[RT], const char *v) {
-        constexpr int kTiles = DP / 32, kChunks = 2 * NT, kShare = 8 / kTiles;
-        // 16 lanes read 4 tokens x 16 values; lane l gets value l of the 4
-        const char *vb = v + (half * 4 + (lane & 15) / 4) * S::VS + ((lane >> 4) & 1) * 32 +
-                         (lane & 3) * 8;
-        auto read = [&](int c, int dt) {
-            typedef __attribute__((address_space(3))) s16x4 *lp;
-            const char *at = vb + c * 16 * S::VS + dt * 64;
-            const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at));
-            const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at + 8 * S::VS));
-            return __builtin_bit_cast(Op, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
-        };
-        f32x8 e[RT];
-        auto weights = [&](int c, int first, int n) {
-#pragma unroll
-            for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-                for (int i = first; i < first + n; i++) {
-                    e[rt][i] = exp2_fast(fmaf(s[rt][c / 2][8 * (c % 2) + i], a.scale_log2, -base[rt]));
-                    sum[rt] += e[rt][i];
-                }
-        };
-        Op f[2][kTiles], p[RT];
+    auto weigh_and_multiply = [&](const Scores &s, float base, const char *v) {
+        constexpr int kShare = 8 / kTiles;
+        f32x8 e;
+        Op f[2][kTiles];
 #pragma unroll
         for (int dt = 0; dt < kTiles; dt++)
-            f[0][dt] = read(0, dt);
+            f[0][dt] = read_v(v, 0, dt);
         __builtin_amdgcn_sched_barrier(0);
-        weights(0, 0, 8);
+        weights(e, s, base, 0, 0, 8);
 #pragma unroll
         for (int c = 0; c < kChunks; c++) {
             // rounded to the cache's type: the matrix cores take no wider operand
-#pragma unroll
-            for (int rt = 0; rt < RT; rt++)
-                p[rt] = __builtin_convertvector(e[rt], Op);
+            const Op p = __builtin_convertvector(e, Op);
 #pragma unroll
             for (int dt = 0; dt < kTiles; dt++) {
-#pragma unroll
-                for (int rt = 0; rt < RT; rt++)
-                    acc[rt][dt] = mfma(f[c % 2][dt], p[rt], acc[rt][dt]);
+                acc[dt] = mfma(f[c % 2][dt], p, acc[dt]);
                 if (c + 1 < kChunks) {
-                    f[(c + 1) % 2][dt] = read(c + 1, dt);
-                    weights(c + 1, dt * kShare, kShare);
+                    f[(c + 1) % 2][dt] = read_v(v, c + 1, dt);
+                    weights(e, s, base, c + 1, dt * kShare, kShare);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -463,17 +448,20 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         cpage = ct / a.page_size;
         cplace = ct % a.page_size;
 #pragma unroll
-        for (int rt = 0; rt < RT; rt++) {
-#pragma unroll
-            for (int dt = 0; dt < DP / 32; dt++)
-                acc[rt][dt] = f32x16{};
-            top[rt] = -INFINITY;
-            sum[rt] = 0.0f;
-        }
+        for (int dt = 0; dt < DP / 32; dt++)
+            acc[dt] = f32x16{};
+        top = -INFINITY;
+        sum = 0.0f;
         look_up();
-        if constexpr (AHEAD) {
-            // K(n + 2) and V(n + 1) go to LDS while S(n + 1) and the products with
-            // V(n) are formed; the loads behind them run one tile further ahead
+        if constexpr (kHalves) {
+            // Step n of a half: at its products, S(n + 1) from K(n + 1) and the
+            // sums from V(n) and the weights n; then, while the other half is at
+            // its products, the weights n + 1. The first half is at products n in
+            // phase 2n, the second in phase 2n + 1, so K(n + 2) and V(n + 1) may be
+            // stored in phases 2n (by the second half, between its steps n - 1 and
+            // n) and 2n + 1 (by the first): what they replace was last read in
+            // phase 2n - 1.
+            const bool second = wm >= 4;
             uint32_t v_place = place_of();
             load(kr, kp, v_place);
             look_up();
@@ -484,37 +472,65 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
             look_up();
             store_k(k_of(1));
             store_v(v_of(0));
-            load(vr, vp, v_place);
-            v_place = place_of();
-            load(kr, kp, v_place);
-            look_up();
-            __syncthreads();
-            Scores s[2];
-            scores(s[0], k_of(0));
-            __syncthreads();
-            auto step = [&](int n, Scores &now, Scores &next) {
-                store_k(k_of(n));
-                store_v(v_of(n + 1));
+            auto load_next = [&] {  // K one tile further than V
                 load(vr, vp, v_place);
                 v_place = place_of();
                 load(kr, kp, v_place);
                 look_up();
-                const int t0 = t00 + n * WK * S::TK;
-                if (seen(t0 + WK * S::TK) || seen(t0)) {
-                    float base[RT];
-                    scores(next, k_of(n + 1));
-                    settle(now, base, t0);
-                    product(now, base, v_of(n));
-                }
-                __syncthreads();
             };
-            int n = 0;
-            for (; n + 1 < iters; n += 2) {
-                step(n, s[0], s[1]);
-                step(n + 1, s[1], s[0]);
+            load_next();  // K(2), V(1)
+            __syncthreads();
+            Scores s;
+            Op p[kChunks];
+            auto soften = [&](int n) {  // the weights n
+                const int t0 = t00 + n * S::TK;
+                if (!seen(t0))
+                    return;
+                const float base = settle(s, t0);
+#pragma unroll
+                for (int c = 0; c < kChunks; c++) {
+                    f32x8 e;
+                    weights(e, s, base, c, 0, 8);
+                    // rounded to the cache's type: the matrix cores take no wider operand
+                    p[c] = __builtin_convertvector(e, Op);
+                }
+            };
+            auto stage = [&](int n) {  // K(n + 2), V(n + 1)
+                store_k(k_of(n));
+                store_v(v_of(n + 1));
+                load_next();
+            };
+            scores(s, k_of(0));
+            if (!second)
+                soften(0);
+            __syncthreads();
+            if (second) {
+                stage(0);
+                soften(0);
+                __syncthreads();
             }
-            if (n < iters)
-                step(n, s[0], s[1]);
+            for (int n = 0; n < iters; n++) {
+                __builtin_amdgcn_s_setprio(1);
+                const int t0 = t00 + n * S::TK;
+                if (seen(t0 + S::TK))
+                    scores(s, k_of(n + 1));
+                if (seen(t0)) {
+                    const char *v = v_of(n);
+#pragma unroll
+                    for (int c = 0; c < kChunks; c++)
+#pragma unroll
+                        for (int dt = 0; dt < kTiles; dt++)
+                            acc[dt] = mfma(read_v(v, c, dt), p[c], acc[dt]);
+                    order_reads<2 * kChunks * kTiles, 2>();
+                }
+                __builtin_amdgcn_s_setprio(0);
+                __syncthreads();
+                stage(second ? n + 1 : n);
+                soften(n + 1);
+                __syncthreads();
+            }
+            if (!second)
+                __syncthreads();
         } else {
             auto load_both = [&] {
                 const uint32_t mine = place_of();
@@ -531,10 +547,9 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
                 if (!seen(t0))
                     return;
                 Scores s;
-                float base[RT];
                 scores(s, k_of(n));
-                settle(s, base, t0);
-                product(s, base, v_of(n));
+                const float base = settle(s, t0);
+                weigh_and_multiply(s, base, v_of(n));
             };
             load_both();
             if constexpr (S::kBufs == 1) {
@@ -562,25 +577,21 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         // do see them get their due at the end.
         bool odd = false;
 #pragma unroll
-        for (int rt = 0; rt < RT; rt++)
+        for (int dt = 0; dt < DP / 32; dt++)
 #pragma unroll
-            for (int dt = 0; dt < DP / 32; dt++)
-#pragma unroll
-                for (int i = 0; i < 16; i++)
-                    odd |= !(fabsf(acc[rt][dt][i]) < INFINITY);
+            for (int i = 0; i < 16; i++)
+                odd |= !(fabsf(acc[dt][i]) < INFINITY);
         if (careful || !__syncthreads_or(odd))
             break;
         careful = true;
     }
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++)
-        sum[rt] = pair_sum(sum[rt]);
+    sum = pair_sum(sum);
 
     const int64_t part_row = (int64_t)split * a.total_q * a.n_q_heads;
-    // What the careful products left out: infinities and NaN that rows of rt see
+    // What the careful products left out: infinities and NaN that the rows see
     // (their weights are above zero, whatever they round to) are the output in
     // their places.
-    auto left_out = [&](int rt, bool stores, int first, int step) {
+    auto left_out = [&](bool stores, int first, int step) {
         auto value_of = [&](int j) -> const T * {  // of token j
             const int page = j < c1 ? table[j / a.page_size] : -1;
             if ((uint32_t)page >= (uint32_t)a.n_pages)
@@ -603,23 +614,23 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
                 for (uint64_t bads = __ballot(bad); bads; bads &= bads - 1) {
                     const int j = j0 + __builtin_ctzll(bads);
                     const float x = (float)value_of(j)[d];
-                    if (j >= lo[rt] && j < hi[rt] && !(fabsf(x) < INFINITY))
+                    if (j >= lo && j < hi && !(fabsf(x) < INFINITY))
                         o += x;
                 }
             }
             if (stores && !(fabsf(o) < INFINITY)) {
                 if (parts > 1)
-                    a.part[(part_row + out_row[rt]) * a.dim + d] = o;
+                    a.part[(part_row + out_row) * a.dim + d] = o;
                 else
-                    static_cast<O *>(a.out)[out_row[rt] * a.dim + d] = (O)o;
+                    static_cast<O *>(a.out)[out_row * a.dim + d] = (O)o;
             }
         }
     };
-    // Of row tile rt, the output's 32-value tiles first, first + step, .. (o(dt)):
+    // The output's 32-value tiles first, first + step, .. (o(dt)):
     // final, or this part's share with its maximum m and sum l.
-    auto store_out = [&](int rt, auto o, int first, int step, float m, float l) {
+    auto store_out = [&](auto o, int first, int step, float m, float l) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const bool stores = col < t.rows - row_first - rt * 32;
+        const bool stores = col < t.rows - row_first;
 #pragma unroll
         for (int dt = first; dt < DP / 32; dt += step) {
             const f32x16 w = o(dt);
@@ -629,52 +640,49 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
                 const int d = dt * 32 + c * 8 + half * 4;
                 if (stores && d < a.dim) {
                     if (parts > 1)
-                        store4(a.part + (part_row + out_row[rt]) * a.dim + d, v);
+                        store4(a.part + (part_row + out_row) * a.dim + d, v);
                     else
-                        store4(static_cast<O *>(a.out) + out_row[rt] * a.dim + d, v * inv);
+                        store4(static_cast<O *>(a.out) + out_row * a.dim + d, v * inv);
                 }
             }
         }
         if (stores && parts > 1 && first == 0 && half == 0)
-            a.part_ml[part_row + out_row[rt]] = make_float2(m, l);
+            a.part_ml[part_row + out_row] = make_float2(m, l);
         if (careful && l == l)  // a sum of NaN has made the whole row so
-            left_out(rt, stores, first, step);
+            left_out(stores, first, step);
     };
 
     if constexpr (WK == 1) {
-#pragma unroll
-        for (int rt = 0; rt < RT; rt++)
-            store_out(rt, [&](int dt) { return acc[rt][dt]; }, 0, 1, top[rt], sum[rt]);
+        store_out([&](int dt) { return acc[dt]; }, 0, 1, top, sum);
     } else {
         // join the groups: every wave brings its sums to the common maximum, and
         // each 32-value tile is added up by one of them
-        static_assert(WM == 1 && RT == 1, "the join is written for groups of one wave");
+        static_assert(WM == 1, "the join is written for groups of one wave");
         float *ml = reinterpret_cast<float *>(lds + WK * (DP / 32) * 4096);
         float *os = reinterpret_cast<float *>(lds);
         __syncthreads();
         if (half == 0)
-            ml[wk * 32 + col] = top[0];
+            ml[wk * 32 + col] = top;
         __syncthreads();
         float m = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WK; w++)
             m = fmaxf(m, ml[w * 32 + col]);
-        const float f = top[0] == -INFINITY ? (sum[0] == sum[0] ? 0.0f : 1.0f) : exp2_fast(top[0] - m);
+        const float f = top == -INFINITY ? (sum == sum ? 0.0f : 1.0f) : exp2_fast(top - m);
         float *ls = ml + WK * 32;
         if (half == 0)
-            ls[wk * 32 + col] = sum[0] * f;
+            ls[wk * 32 + col] = sum * f;
 #pragma unroll
         for (int dt = 0; dt < DP / 32; dt++)
 #pragma unroll
             for (int i = 0; i < 16; i++)
-                os[((wk * (DP / 32) + dt) * 16 + i) * 64 + lane] = acc[0][dt][i] * f;
+                os[((wk * (DP / 32) + dt) * 16 + i) * 64 + lane] = acc[dt][i] * f;
         __syncthreads();
         float l = 0.0f;
 #pragma unroll
         for (int w = 0; w < WK; w++)
             l += ls[w * 32 + col];
         store_out(
-            0,
             [&](int dt) {
                 f32x16 o = {};
 #pragma unroll
@@ -778,7 +786,7 @@ struct Plan {
 constexpr int kFewRows = 32;
 constexpr int64_t kWantedWorkgroups = 1024;  // four a compute unit, of which two run at once
 constexpr int64_t kWantedTiles = 512;        // the same for tiles of 128 rows, whose parts cost more
-constexpr int64_t kManyTiles = 512000;          // of 256 rows: two a compute unit
+constexpr int64_t kManyTiles = 512;          // of 256 rows: two a compute unit
 constexpr int64_t kMostWorkgroups = 8192;    // most of them empty, where lengths differ
 constexpr int kLeastChunk = 256, kRaggedChunk = 1024;
 
@@ -814,11 +822,11 @@ Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads, int wi
     return p;
 }
 
-template <class T, class O, int DP, int WM, int WK, int NT, int RT, bool AHEAD, int WAVES>
+template <class T, class O, int DP, int WM, int WK, int NT, int WAVES>
 int launch_shape(const AttnArgs &a, hipStream_t stream)
 {
-    typedef Shape<DP, WM, WK, NT, RT> S;
-    auto kernel = attention_kernel<T, O, DP, WM, WK, NT, RT, AHEAD, WAVES>;
+    typedef Shape<DP, WM, WK, NT> S;
+    auto kernel = attention_kernel<T, O, DP, WM, WK, NT, WAVES>;
     allow_dynamic_lds(reinterpret_cast<const void *>(kernel), S::kLds);
     const int64_t grid = (int64_t)a.tiles * a.n_splits * a.n_heads;
     if (grid * S::kThreads >= 1ll << 32)
@@ -838,11 +846,11 @@ template <class T, class O, int DP>
 int launch_rows(const AttnArgs &a, int m, hipStream_t stream)
 {
     if (m == 32)
-        return launch_shape<T, O, DP, 1, 4, 1, 1, false, (DP > 128 ? 1 : 2)>(a, stream);
+        return launch_shape<T, O, DP, 1, 4, 1, (DP > 128 ? 1 : 2)>(a, stream);
     if constexpr (DP <= 128)
         if (m == 256)
-            return launch_shape<T, O, DP, 4, 1, 2, 2, false, (DP > 64 ? 1 : 2)>(a, stream);
-    return launch_shape<T, O, DP, 4, 1, 2, 1, false, (DP > 128 ? 1 : 2)>(a, stream);
+            return launch_shape<T, O, DP, 8, 1, 2, 2>(a, stream);
+    return launch_shape<T, O, DP, 4, 1, 2, (DP > 128 ? 1 : 2)>(a, stream);
 }
 
 template <class T, class O>

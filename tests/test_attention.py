@@ -736,3 +736,65 @@ def test_binding_refuses(bqm):
         bqm.kv_extend(p, _ints([1]), 0)
     with pytest.raises(ValueError):
         bqm.kv_copy_pages(cache, _ints([[1, 2]]))
+
+
+# Calls of many rows, whose tiles are the widest: every fourth row or so against the
+# definition in 64 bits (on the GPU: the same formulas, torch's float64).
+
+def _rows64(s, b, rows, h, scale, causal, window):
+    k, v = (x[b][:, h // (s.n_q // s.H)].double() for x in (s.ks, s.vs))
+    n = s.lens[b]
+    q = s.q[s.starts[b] + rows, h].double()
+    x = scale * (q @ k.T.contiguous())
+    j, pos = torch.arange(n, device="cuda")[None], (n - s.q_lens[b] + rows)[:, None]
+    hide = torch.zeros_like(x, dtype=torch.bool)
+    if causal:
+        hide |= j > pos
+    if window:
+        hide |= j <= pos - window
+    p = torch.softmax(x.masked_fill(hide, float("-inf")), -1)
+    spread = scale * (q.abs() @ k.abs().T.contiguous()).amax(-1)
+    return p @ v, p @ v.abs(), (~hide).sum(-1), spread
+
+
+@pytest.mark.parametrize("lens,q_lens,H,Hq,D,ps,causal,window,dt", [
+    ([4133], [4133], 8, 32, 128, 16, True, 0, "bf16"),
+    ([2500, 1900, 700], [2477, 1900, 31], 8, 32, 64, 24, True, 0, "f16"),
+    ([3000, 2111], [2600, 2111], 8, 32, 128, 64, True, 700, "f16"),
+    ([2300, 65, 2000], [2300, 65, 2000], 8, 56, 80, 16, True, 0, "bf16"),
+    ([600, 64], [4100, 300], 8, 32, 128, 16, False, 0, "bf16"),
+])
+def test_attention_many_rows(bqm, lens, q_lens, H, Hq, D, ps, causal, window, dt):
+    _say("attention many rows", lens, q_lens, H, Hq, D, ps, causal, window, dt)
+    s = Setup(lens, q_lens, H, D, ps, dt, seed=D, n_q=Hq)
+    scale = D ** -0.5
+    out = torch.full(s.q.shape, float("nan"), dtype=DT[dt], device="cuda")
+    y = bqm.paged_attention(s.q, bqm.KvCache(s.k, s.v), s.batch(bqm), causal=causal, window=window, out=out)
+    assert torch.isfinite(y.float()).all()
+    u, vmax = UNIT[dt], max(float(v.abs().max()) for v in s.vs)
+    for b in range(len(lens)):
+        rows = torch.unique(torch.cat((torch.arange(0, q_lens[b], 3), torch.tensor([q_lens[b] - 1])))).cuda()
+        for h in range(0, Hq, 5):
+            want, mean, seen, spread = _rows64(s, b, rows, h, scale, causal, window)
+            rel = 2.0 * u + 2.0 * ((D + 16) * 2.0 ** -23 * spread + 2.0 ** -20) + seen * 2.0 ** -23
+            bound = rel[:, None] * mean * 1.02 + u * want.abs() * 1.02
+            bound += (2.0 * seen * TINY[dt] * vmax + TINY[dt])[:, None]
+            err = (y[s.starts[b] + rows, h].double() - want).abs()
+            assert (err <= bound).all(), (b, h, float((err - bound).max()))
+
+
+def test_attention_many_rows_infinities_and_nan(bqm):
+    # one infinite value and one NaN, in one head: only rows that see them change,
+    # and those get them
+    s = Setup([4200], [4200], 8, 128, 16, "bf16", seed=77, n_q=32)
+    cache = bqm.KvCache(s.k, s.v)
+    clean = bqm.paged_attention(s.q, cache, s.batch(bqm))
+    for token, head, d, x in ((1000, 2, 5, float("inf")), (1700, 2, 99, float("nan"))):
+        s.v[int(s.table[0, token // 16]), token % 16, head, d] = x
+    y = bqm.paged_attention(s.q, cache, s.batch(bqm))
+    mask = torch.zeros(y.shape, dtype=torch.bool, device="cuda")
+    mask[1000:, 8:12, 5] = True
+    mask[1700:, 8:12, 99] = True
+    assert torch.equal(y[~mask], clean[~mask])
+    assert torch.isposinf(y[1000:, 8:12, 5].float()).all()
+    assert torch.isnan(y[1700:, 8:12, 99].float()).all()
