@@ -61,6 +61,7 @@ struct AttnArgs {
     float2 *part_ml;     // the same rows' maximum (log2) and sum of weights
     int64_t q_token, q_head, pages_stride, total_q;
     uint32_t c_page, c_token, c_head;  // strides in pieces
+    uint32_t span;       // bytes of one head's pieces, first to last; 0: 4 GiB or more
     int n_pages, n_seqs, max_pages, page_size, max_kv;
     int n_q_heads, n_heads, group, dim;
     int tiles, n_splits, chunk;
@@ -73,6 +74,9 @@ struct AttnArgs {
 __device__ const u32x4 kZeros = {0, 0, 0, 0};
 
 typedef const __attribute__((address_space(1))) u32x4 *piece_ptr;
+
+// In the place of a token that there is none of: behind every span below 4 GiB.
+constexpr uint32_t kNoPlace = 0xffffffffu;
 
 // A tile of rows: its sequence, and the tokens that any of its rows sees.
 struct Tile {
@@ -191,24 +195,6 @@ __device__ __forceinline__ void store4(O *p, f32x4 v)
     *reinterpret_cast<o4 *>(p) = __builtin_convertvector(v, o4);
 }
 
-// The order of instructions the scheduler keeps (it would read each operand
-// right before its product, and wait): operands a few products ahead.
-constexpr int kSchedMatrix = 0x8, kSchedLdsRead = 0x100;
-
-// READS operand reads, PER of them a product.
-template <int READS, int PER = 1>
-__device__ __forceinline__ void order_reads()
-{
-    constexpr int kProducts = READS / PER, kAhead = kProducts < 4 ? kProducts : 4;
-    __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, kAhead * PER, 0);
-#pragma unroll
-    for (int i = 0; i < kProducts - kAhead; i++) {
-        __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, PER, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(kSchedMatrix, kAhead, 0);
-}
-
 // WM waves share a key tile, 32 rows each; WK such groups take every WK-th tile
 // of 32 * NT tokens and are joined at the end.
 template <int DP, int WM, int WK, int NT>
@@ -292,9 +278,12 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
     const int gt = wm * 64 + lane;  // thread of the group
     const int piece = gt % S::kPieces, row0 = gt / S::kPieces;
     const bool piece_ok = piece * 8 < a.dim;
-    const piece_ptr kp = (piece_ptr)a.k + (uint64_t)head * a.c_head + piece;
-    const piece_ptr vp = (piece_ptr)a.v + (uint64_t)head * a.c_head + piece;
-    const piece_ptr zeros = (piece_ptr)&kZeros;
+    // Pieces are read through buffer resources of the head's span: a place behind
+    // its end reads as zeros without a branch. Caches of 4 GiB and more a layer,
+    // beyond a resource's offsets, are read through pointers.
+    const u32x4 *const kh = a.k + (uint64_t)head * a.c_head, *const vh = a.v + (uint64_t)head * a.c_head;
+    const __amdgpu_buffer_rsrc_t kb_rsrc = make_rsrc(kh, a.span), vb_rsrc = make_rsrc(vh, a.span);
+    const uint32_t piece_none = piece_ok ? 0u : kNoPlace;
     char *const buf = lds + wk * S::kTile * S::kBufs;
     auto k_of = [&](int n) { return buf + (S::kBufs > 1 ? n & 1 : 0) * S::kTile; };
     auto v_of = [&](int n) { return k_of(n) + S::TK * S::KS; };
@@ -315,22 +304,34 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
             cpage++;
         }
     };
-    auto place_of = [&] {  // of lane l's token, in pieces; ~0: none
+    // of lane l's token, in pieces; kNoPlace: none
+    auto place_of = [&] {
         return (uint32_t)page_id < (uint32_t)a.n_pages
                    ? (uint32_t)page_id * a.c_page + (uint32_t)place * a.c_token
-                   : 0xffffffffu;
+                   : kNoPlace;
+    };
+    // this thread's rows' places
+    typedef uint32_t Places[S::kLoads];
+    auto spread = [&](Places &of, uint32_t mine) {
+#pragma unroll
+        for (int i = 0; i < S::kLoads; i++)
+            of[i] = __shfl(mine, row0 + i * S::kRowsPerLoad, 64) | piece_none;
     };
     u32x4 kr[S::kLoads], vr[S::kLoads];
-    auto load = [&](u32x4 (&r)[S::kLoads], piece_ptr base, uint32_t mine) {
-        uint32_t off[S::kLoads];
+    auto load = [&](u32x4 (&r)[S::kLoads], const u32x4 *base, __amdgpu_buffer_rsrc_t rsrc,
+                    const Places &of) {
+        if (a.span != 0) {
 #pragma unroll
-        for (int i = 0; i < S::kLoads; i++)
-            off[i] = __shfl(mine, row0 + i * S::kRowsPerLoad, 64);
-        __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < S::kLoads; i++)
+                r[i] = ld_b128(rsrc, of[i] == kNoPlace ? kNoPlace : (of[i] + piece) * 16u);
+        } else {
 #pragma unroll
-        for (int i = 0; i < S::kLoads; i++)
-            r[i] = *(piece_ok && off[i] != 0xffffffffu ? base + off[i] : zeros);
+            for (int i = 0; i < S::kLoads; i++)
+                r[i] = *(of[i] == kNoPlace ? (piece_ptr)&kZeros : (piece_ptr)base + of[i] + piece);
+        }
     };
+    auto load_k = [&](const Places &of) { load(kr, kh, kb_rsrc, of); };
+    auto load_v = [&](const Places &of) { load(vr, vh, vb_rsrc, of); };
     auto store_k = [&](char *to) {
 #pragma unroll
         for (int i = 0; i < S::kLoads; i++)
@@ -351,17 +352,29 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
 
     // whether a row of this wave sees the tile at t0
     auto seen = [&](int t0) { return t0 < hi_last && t0 + S::TK > lo_first; };
-    auto scores = [&](Scores &s, const char *k) {
+    // The scheduler left alone puts each operand read right before its product and
+    // waits; these keep kAhead reads in flight.
+    constexpr int kAhead = 4;
+    auto read_k = [&](const char *k, int i) {
         const char *kb = k + col * S::KS + half * 16;
+        return *reinterpret_cast<const Op *>(kb + i / (DP / 16) * 32 * S::KS + i % (DP / 16) * 32);
+    };
+    auto scores = [&](Scores &s, const char *k) {
+        Op f[kAhead];
 #pragma unroll
-        for (int tt = 0; tt < NT; tt++) {
+        for (int i = 0; i < kAhead; i++)
+            f[i] = read_k(k, i);
+#pragma unroll
+        for (int tt = 0; tt < NT; tt++)
             s[tt] = f32x16{};
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int kk = 0; kk < DP / 16; kk++)
-                s[tt] = mfma(*reinterpret_cast<const Op *>(kb + tt * 32 * S::KS + kk * 32), qf[kk],
-                             s[tt]);
+        for (int i = 0; i < NT * DP / 16; i++) {
+            s[i / (DP / 16)] = mfma(f[i % kAhead], qf[i % (DP / 16)], s[i / (DP / 16)]);
+            if (i + kAhead < NT * DP / 16)
+                f[i % kAhead] = read_k(k, i + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        order_reads<NT * DP / 16>();
     };
     // the row's maximum: masks the scores, brings the accumulators to a new base
     auto settle = [&](Scores &s, int t0) {
@@ -416,8 +429,7 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         return __builtin_bit_cast(Op, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
     };
     // Weights and products, 16 tokens at a time. Between the products of 16 tokens
-    // go the exponentials and the operand reads of the next 16, in this order: the
-    // scheduler left alone puts each read right before its product and waits.
+    // go the exponentials and the operand reads of the next 16, in this order.
     auto weigh_and_multiply = [&](const Scores &s, float base, const char *v) {
         constexpr int kShare = 8 / kTiles;
         f32x8 e;
@@ -462,30 +474,38 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
             // n) and 2n + 1 (by the first): what they replace was last read in
             // phase 2n - 1.
             const bool second = wm >= 4;
-            uint32_t v_place = place_of();
-            load(kr, kp, v_place);
-            look_up();
-            store_k(k_of(0));
-            load(vr, vp, v_place);
-            v_place = place_of();
-            load(kr, kp, v_place);
-            look_up();
-            store_k(k_of(1));
-            store_v(v_of(0));
-            auto load_next = [&] {  // K one tile further than V
-                load(vr, vp, v_place);
-                v_place = place_of();
-                load(kr, kp, v_place);
+            Places of_k, of_v;
+            auto next_places = [&] {  // K one tile further than V
+#pragma unroll
+                for (int i = 0; i < S::kLoads; i++)
+                    of_v[i] = of_k[i];
+                spread(of_k, place_of());
                 look_up();
             };
-            load_next();  // K(2), V(1)
+            spread(of_k, place_of());
+            look_up();
+            load_k(of_k);
+            store_k(k_of(0));
+            next_places();
+            load_v(of_v);
+            load_k(of_k);
+            store_k(k_of(1));
+            store_v(v_of(0));
+            next_places();
+            load_v(of_v);  // V(1), K(2)
+            load_k(of_k);
+            next_places();
             __syncthreads();
             Scores s;
             Op p[kChunks];
             auto soften = [&](int n) {  // the weights n
                 const int t0 = t00 + n * S::TK;
-                if (!seen(t0))
+                if (!seen(t0)) {
+#pragma unroll
+                    for (int c = 0; c < kChunks; c++)
+                        p[c] = Op{};
                     return;
+                }
                 const float base = settle(s, t0);
 #pragma unroll
                 for (int c = 0; c < kChunks; c++) {
@@ -495,10 +515,14 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
                     p[c] = __builtin_convertvector(e, Op);
                 }
             };
-            auto stage = [&](int n) {  // K(n + 2), V(n + 1)
+            // K(n + 2) and V(n + 1) to LDS, the loads of the next ones, and where
+            // those after them are
+            auto stage = [&](int n) {
                 store_k(k_of(n));
                 store_v(v_of(n + 1));
-                load_next();
+                load_v(of_v);
+                load_k(of_k);
+                next_places();
             };
             scores(s, k_of(0));
             if (!second)
@@ -512,16 +536,35 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
             for (int n = 0; n < iters; n++) {
                 __builtin_amdgcn_s_setprio(1);
                 const int t0 = t00 + n * S::TK;
-                if (seen(t0 + S::TK))
-                    scores(s, k_of(n + 1));
-                if (seen(t0)) {
-                    const char *v = v_of(n);
+                if (seen(t0) || seen(t0 + S::TK)) {
+                    // S(n + 1), then the products with V(n), reads kAhead of them
+                    constexpr int kScores = NT * DP / 16, kAll = kScores + kChunks * kTiles;
+                    const char *k = k_of(n + 1), *v = v_of(n);
+                    auto read = [&](int i) {
+                        return i < kScores ? read_k(k, i)
+                                           : read_v(v, (i - kScores) / kTiles, (i - kScores) % kTiles);
+                    };
+                    Op f[kAhead];
 #pragma unroll
-                    for (int c = 0; c < kChunks; c++)
+                    for (int i = 0; i < kAhead; i++)
+                        f[i] = read(i);
 #pragma unroll
-                        for (int dt = 0; dt < kTiles; dt++)
-                            acc[dt] = mfma(read_v(v, c, dt), p[c], acc[dt]);
-                    order_reads<2 * kChunks * kTiles, 2>();
+                    for (int tt = 0; tt < NT; tt++)
+                        s[tt] = f32x16{};
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < kAll; i++) {
+                        if (i < kScores) {
+                            f32x16 &t = s[i / (DP / 16)];
+                            t = mfma(f[i % kAhead], qf[i % (DP / 16)], t);
+                        } else {
+                            const int c = (i - kScores) / kTiles, dt = (i - kScores) % kTiles;
+                            acc[dt] = mfma(f[i % kAhead], p[c], acc[dt]);
+                        }
+                        if (i + kAhead < kAll)
+                            f[i % kAhead] = read(i + kAhead);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 }
                 __builtin_amdgcn_s_setprio(0);
                 __syncthreads();
@@ -533,9 +576,10 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
                 __syncthreads();
         } else {
             auto load_both = [&] {
-                const uint32_t mine = place_of();
-                load(kr, kp, mine);
-                load(vr, vp, mine);
+                Places of;
+                spread(of, place_of());
+                load_k(of);
+                load_v(of);
                 look_up();
             };
             auto store_both = [&](int n) {
@@ -897,6 +941,9 @@ int launch_paged_attention(const void *q, int64_t q_token, int64_t q_head, const
     a.c_page = (uint32_t)(c->page_stride / 8);
     a.c_token = (uint32_t)(c->token_stride / 8);
     a.c_head = (uint32_t)(c->head_stride / 8);
+    const uint64_t span = ((uint64_t)(c->n_pages - 1) * a.c_page +
+                           (uint64_t)(c->page_size - 1) * a.c_token + c->head_dim / 8) * 16;
+    a.span = span < 0xfffff000ull ? (uint32_t)span : 0;
     a.n_pages = (int)c->n_pages;
     a.n_seqs = b->n_seqs;
     a.max_pages = b->max_pages;
