@@ -290,7 +290,8 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
     const int32_t *table = a.pages + t.seq * a.pages_stride;
 
     // lane l looks up token l of the tile to be read next; page and place advance
-    // by a tile at a time without a division
+    // by a tile at a time without a division. (The look-up goes out before a tile's
+    // loads: loads are waited for in order, so one behind them would take their time.)
     const int step_page = WK * S::TK / a.page_size, step_place = WK * S::TK % a.page_size;
     int ct, cpage, cplace, page_id, place;
     auto look_up = [&] {
@@ -475,26 +476,23 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
             // phase 2n - 1.
             const bool second = wm >= 4;
             Places of_k, of_v;
-            auto next_places = [&] {  // K one tile further than V
+            auto load_next = [&] {  // K one tile further than V
 #pragma unroll
                 for (int i = 0; i < S::kLoads; i++)
                     of_v[i] = of_k[i];
                 spread(of_k, place_of());
                 look_up();
+                load_v(of_v);
+                load_k(of_k);
             };
             spread(of_k, place_of());
             look_up();
             load_k(of_k);
             store_k(k_of(0));
-            next_places();
-            load_v(of_v);
-            load_k(of_k);
+            load_next();  // V(0), K(1)
             store_k(k_of(1));
             store_v(v_of(0));
-            next_places();
-            load_v(of_v);  // V(1), K(2)
-            load_k(of_k);
-            next_places();
+            load_next();  // V(1), K(2)
             __syncthreads();
             Scores s;
             Op p[kChunks];
@@ -515,14 +513,11 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
                     p[c] = __builtin_convertvector(e, Op);
                 }
             };
-            // K(n + 2) and V(n + 1) to LDS, the loads of the next ones, and where
-            // those after them are
+            // K(n + 2) and V(n + 1) to LDS, and the loads of the next ones
             auto stage = [&](int n) {
                 store_k(k_of(n));
                 store_v(v_of(n + 1));
-                load_v(of_v);
-                load_k(of_k);
-                next_places();
+                load_next();
             };
             scores(s, k_of(0));
             if (!second)
@@ -578,9 +573,9 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
             auto load_both = [&] {
                 Places of;
                 spread(of, place_of());
+                look_up();
                 load_k(of);
                 load_v(of);
-                look_up();
             };
             auto store_both = [&](int n) {
                 store_k(k_of(n));
