@@ -78,6 +78,10 @@ typedef const __attribute__((address_space(1))) u32x4 *piece_ptr;
 // In the place of a token that there is none of: behind every span below 4 GiB.
 constexpr uint32_t kNoPlace = 0xffffffffu;
 
+// The kernel's steps are lambdas called from several places; left to itself the
+// compiler makes calls of some, with the registers they share in memory.
+#define BQM_INLINE __attribute__((always_inline))
+
 // A tile of rows: its sequence, and the tokens that any of its rows sees.
 struct Tile {
     int seq, tile;      // tile of the sequence
@@ -205,9 +209,10 @@ struct Shape {
     static constexpr int kPieces = DP / 8;                     // of a row
     static constexpr int kLoads = TK * kPieces / (64 * WM);    // a thread's, of K and of V
     static constexpr int kRowsPerLoad = 64 * WM / kPieces;
-    // LDS rows are padded: K by 16 bytes (32 lanes read 16 bytes of 32 rows),
-    // V by 32 (16 lanes read 32 bytes of 4 rows): no two of them share banks
-    static constexpr int KS = DP * 2 + 16, VS = DP * 2 + 32;
+    // LDS rows are padded: K by 16 bytes (neighbouring lanes read 16 bytes of
+    // neighbouring rows), V by 64 (32 lanes read 64 bytes of 4 rows), so that no two
+    // of them share one of the 64 banks: no conflicts counted
+    static constexpr int KS = DP * 2 + 16, VS = DP * 2 + 64;
     static constexpr int kTile = TK * (KS + VS);
     static constexpr int kBufs = WM > 1 ? 2 : 1;
     static constexpr int kStage = kTile * kBufs * WK;
@@ -294,52 +299,54 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
     // loads: loads are waited for in order, so one behind them would take their time.)
     const int step_page = WK * S::TK / a.page_size, step_place = WK * S::TK % a.page_size;
     int ct, cpage, cplace, page_id, place;
-    auto look_up = [&] {
-        page_id = ct < c1 ? table[cpage] : -1;
-        place = cplace;
+    const int last_page = max(c1 - 1, 0) / a.page_size;
+    auto look_up = [&]() BQM_INLINE {
+        page_id = table[min(cpage, last_page)];
+        place = ct < c1 ? cplace : -1;
         ct += WK * S::TK;
         cpage += step_page;
         cplace += step_place;
-        if (cplace >= a.page_size) {
-            cplace -= a.page_size;
-            cpage++;
-        }
+        const bool over = cplace >= a.page_size;
+        cplace -= over ? a.page_size : 0;
+        cpage += over;
     };
     // of lane l's token, in pieces; kNoPlace: none
-    auto place_of = [&] {
-        return (uint32_t)page_id < (uint32_t)a.n_pages
-                   ? (uint32_t)page_id * a.c_page + (uint32_t)place * a.c_token
-                   : kNoPlace;
+    auto place_of = [&]() BQM_INLINE {
+        const uint32_t at = (uint32_t)page_id * a.c_page + (uint32_t)place * a.c_token;
+        return place >= 0 && (uint32_t)page_id < (uint32_t)a.n_pages ? at : kNoPlace;
     };
     // this thread's rows' places
     typedef uint32_t Places[S::kLoads];
-    auto spread = [&](Places &of, uint32_t mine) {
+    auto spread = [&](Places &of, uint32_t mine) BQM_INLINE {
 #pragma unroll
         for (int i = 0; i < S::kLoads; i++)
-            of[i] = __shfl(mine, row0 + i * S::kRowsPerLoad, 64) | piece_none;
+            of[i] = __shfl(mine, row0 + i * S::kRowsPerLoad, 64);
     };
     u32x4 kr[S::kLoads], vr[S::kLoads];
-    auto load = [&](u32x4 (&r)[S::kLoads], const u32x4 *base, __amdgpu_buffer_rsrc_t rsrc,
-                    const Places &of) {
-        if (a.span != 0) {
-#pragma unroll
-            for (int i = 0; i < S::kLoads; i++)
-                r[i] = ld_b128(rsrc, of[i] == kNoPlace ? kNoPlace : (of[i] + piece) * 16u);
-        } else {
-#pragma unroll
-            for (int i = 0; i < S::kLoads; i++)
-                r[i] = *(of[i] == kNoPlace ? (piece_ptr)&kZeros : (piece_ptr)base + of[i] + piece);
-        }
+    // piece i of the thread's; none of a head's values beyond its own
+    auto load = [&](const u32x4 *base, __amdgpu_buffer_rsrc_t rsrc, uint32_t of) BQM_INLINE -> u32x4 {
+        of |= piece_none;
+        if (a.span != 0)
+            return ld_b128(rsrc, of == kNoPlace ? kNoPlace : (of + piece) * 16u);
+        return *(of == kNoPlace ? (piece_ptr)&kZeros : (piece_ptr)base + of + piece);
     };
-    auto load_k = [&](const Places &of) { load(kr, kh, kb_rsrc, of); };
-    auto load_v = [&](const Places &of) { load(vr, vh, vb_rsrc, of); };
-    auto store_k = [&](char *to) {
+    auto load_k = [&](u32x4 (&r)[S::kLoads], const Places &of) BQM_INLINE {
 #pragma unroll
         for (int i = 0; i < S::kLoads; i++)
-            *reinterpret_cast<u32x4 *>(to + (row0 + i * S::kRowsPerLoad) * S::KS + piece * 16) = kr[i];
+            r[i] = load(kh, kb_rsrc, of[i]);
+    };
+    auto load_v = [&](const Places &of) BQM_INLINE {
+#pragma unroll
+        for (int i = 0; i < S::kLoads; i++)
+            vr[i] = load(vh, vb_rsrc, of[i]);
+    };
+    auto store_k = [&](const u32x4 (&r)[S::kLoads], char *to) BQM_INLINE {
+#pragma unroll
+        for (int i = 0; i < S::kLoads; i++)
+            *reinterpret_cast<u32x4 *>(to + (row0 + i * S::kRowsPerLoad) * S::KS + piece * 16) = r[i];
     };
     bool careful = false;  // keep infinities and NaN of V out of the products
-    auto store_v = [&](char *to) {
+    auto store_v = [&](char *to) BQM_INLINE {
 #pragma unroll
         for (int i = 0; i < S::kLoads; i++) {
             if (careful)
@@ -356,11 +363,13 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
     // The scheduler left alone puts each operand read right before its product and
     // waits; these keep kAhead reads in flight.
     constexpr int kAhead = 4;
-    auto read_k = [&](const char *k, int i) {
+    // operand i of the scores: the tiles of 32 tokens in turn, so that no product
+    // waits for the sum of the one before it
+    auto read_k = [&](const char *k, int i) BQM_INLINE {
         const char *kb = k + col * S::KS + half * 16;
-        return *reinterpret_cast<const Op *>(kb + i / (DP / 16) * 32 * S::KS + i % (DP / 16) * 32);
+        return *reinterpret_cast<const Op *>(kb + i % NT * 32 * S::KS + i / NT * 32);
     };
-    auto scores = [&](Scores &s, const char *k) {
+    auto scores = [&](Scores &s, const char *k) BQM_INLINE {
         Op f[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; i++)
@@ -371,14 +380,14 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < NT * DP / 16; i++) {
-            s[i / (DP / 16)] = mfma(f[i % kAhead], qf[i % (DP / 16)], s[i / (DP / 16)]);
+            s[i % NT] = mfma(f[i % kAhead], qf[i / NT], s[i % NT]);
             if (i + kAhead < NT * DP / 16)
                 f[i % kAhead] = read_k(k, i + kAhead);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
     // the row's maximum: masks the scores, brings the accumulators to a new base
-    auto settle = [&](Scores &s, int t0) {
+    auto settle = [&](Scores &s, int t0) BQM_INLINE {
         if (!(t0 >= lo_last && t0 + S::TK <= hi_first)) {
 #pragma unroll
             for (int tt = 0; tt < NT; tt++)
@@ -388,13 +397,14 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
                     s[tt][i] = j >= lo && j < hi ? s[tt][i] : -INFINITY;
                 }
         }
-        float m = -INFINITY;
+        float ms[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains, not one
 #pragma unroll
         for (int tt = 0; tt < NT; tt++)
 #pragma unroll
-            for (int i = 0; i < 16; i++)
-                m = fmaxf(m, s[tt][i]);
-        m = pair_max(m) * a.scale_log2;
+            for (int i = 0; i < 16; i += 2)
+                ms[i / 4] = fmaxf(fmaxf(ms[i / 4], s[tt][i]), s[tt][i + 1]);
+        const float m =
+            pair_max(fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]))) * a.scale_log2;
         // The weights' base follows the maximum only when that has grown by a
         // factor of 2^8: sums and weights (up to 256, the same relative rounding
         // in either type) have room for it, and most tiles pass without scaling
@@ -413,7 +423,7 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         return top == -INFINITY ? 0.0f : top;  // nothing seen yet
     };
     constexpr int kTiles = DP / 32, kChunks = 2 * NT;  // of 32 values, of 16 tokens
-    auto weights = [&](f32x8 &e, const Scores &s, float base, int c, int first, int n) {
+    auto weights = [&](f32x8 &e, const Scores &s, float base, int c, int first, int n) BQM_INLINE {
 #pragma unroll
         for (int i = first; i < first + n; i++) {
             e[i] = exp2_fast(fmaf(s[c / 2][8 * (c % 2) + i], a.scale_log2, -base));
@@ -422,7 +432,7 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
     };
     // 16 lanes read 4 tokens x 16 values; lane l gets value l of the 4
     const int v_lane = (half * 4 + (lane & 15) / 4) * S::VS + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-    auto read_v = [&](const char *v, int c, int dt) {
+    auto read_v = [&](const char *v, int c, int dt) BQM_INLINE {
         typedef __attribute__((address_space(3))) s16x4 *lp;
         const char *at = v + v_lane + c * 16 * S::VS + dt * 64;
         const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at));
@@ -431,7 +441,7 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
     };
     // Weights and products, 16 tokens at a time. Between the products of 16 tokens
     // go the exponentials and the operand reads of the next 16, in this order.
-    auto weigh_and_multiply = [&](const Scores &s, float base, const char *v) {
+    auto weigh_and_multiply = [&](const Scores &s, float base, const char *v) BQM_INLINE {
         constexpr int kShare = 8 / kTiles;
         f32x8 e;
         Op f[2][kTiles];
@@ -469,34 +479,43 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         if constexpr (kHalves) {
             // Step n of a half: at its products, S(n + 1) from K(n + 1) and the
             // sums from V(n) and the weights n; then, while the other half is at
-            // its products, the weights n + 1. The first half is at products n in
-            // phase 2n, the second in phase 2n + 1, so K(n + 2) and V(n + 1) may be
-            // stored in phases 2n (by the second half, between its steps n - 1 and
-            // n) and 2n + 1 (by the first): what they replace was last read in
-            // phase 2n - 1.
+            // its products, the weights n + 1 and its share of the next tiles to
+            // LDS. The first half is at products n in phase 2n, the second in phase
+            // 2n + 1, so K(n + 2) and V(n + 1) may be stored in phases 2n (by the
+            // second half, between its steps n - 1 and n) and 2n + 1 (by the first):
+            // what they replace was last read in phase 2n - 1.
             const bool second = wm >= 4;
             Places of_k, of_v;
-            auto load_next = [&] {  // K one tile further than V
-#pragma unroll
-                for (int i = 0; i < S::kLoads; i++)
-                    of_v[i] = of_k[i];
-                spread(of_k, place_of());
+            {  // K(0), K(1) and V(0) in one round of loads
+                const int page0 = page_id, place0 = place;
                 look_up();
-                load_v(of_v);
-                load_k(of_k);
-            };
+                const int page1 = page_id, place1 = place;
+                look_up();
+                const int page2 = page_id, place2 = place;
+                page_id = page0, place = place0;
+                spread(of_v, place_of());
+                page_id = page1, place = place1;
+                spread(of_k, place_of());
+                page_id = page2, place = place2;
+            }
+            u32x4 k0[S::kLoads];
+            load_k(k0, of_v);
+            load_k(kr, of_k);
+            load_v(of_v);
+            store_k(k0, k_of(0));
+            store_k(kr, k_of(1));
+            store_v(v_of(0));
+#pragma unroll
+            for (int i = 0; i < S::kLoads; i++)
+                of_v[i] = of_k[i];
             spread(of_k, place_of());
             look_up();
-            load_k(of_k);
-            store_k(k_of(0));
-            load_next();  // V(0), K(1)
-            store_k(k_of(1));
-            store_v(v_of(0));
-            load_next();  // V(1), K(2)
+            load_v(of_v);  // V(1), K(2)
+            load_k(kr, of_k);
             __syncthreads();
             Scores s;
             Op p[kChunks];
-            auto soften = [&](int n) {  // the weights n
+            auto soften = [&](int n) BQM_INLINE {  // the weights n
                 const int t0 = t00 + n * S::TK;
                 if (!seen(t0)) {
 #pragma unroll
@@ -513,23 +532,29 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
                     p[c] = __builtin_convertvector(e, Op);
                 }
             };
-            // K(n + 2) and V(n + 1) to LDS, and the loads of the next ones
-            auto stage = [&](int n) {
-                store_k(k_of(n));
+            // K(n + 2) and V(n + 1) to LDS, the loads of the tiles after them, and
+            // the weights m
+            auto stage_and_soften = [&](int n, int m) BQM_INLINE {
+                store_k(kr, k_of(n));
                 store_v(v_of(n + 1));
-                load_next();
+#pragma unroll
+                for (int i = 0; i < S::kLoads; i++)
+                    of_v[i] = of_k[i];
+                spread(of_k, place_of());
+                look_up();
+                load_v(of_v);
+                load_k(kr, of_k);
+                soften(m);
             };
             scores(s, k_of(0));
             if (!second)
                 soften(0);
             __syncthreads();
             if (second) {
-                stage(0);
-                soften(0);
+                stage_and_soften(0, 0);
                 __syncthreads();
             }
             for (int n = 0; n < iters; n++) {
-                __builtin_amdgcn_s_setprio(1);
                 const int t0 = t00 + n * S::TK;
                 if (seen(t0) || seen(t0 + S::TK)) {
                     // S(n + 1), then the products with V(n), reads kAhead of them
@@ -550,8 +575,7 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
 #pragma unroll
                     for (int i = 0; i < kAll; i++) {
                         if (i < kScores) {
-                            f32x16 &t = s[i / (DP / 16)];
-                            t = mfma(f[i % kAhead], qf[i % (DP / 16)], t);
+                            s[i % NT] = mfma(f[i % kAhead], qf[i / NT], s[i % NT]);
                         } else {
                             const int c = (i - kScores) / kTiles, dt = (i - kScores) % kTiles;
                             acc[dt] = mfma(f[i % kAhead], p[c], acc[dt]);
@@ -561,27 +585,25 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
-                __builtin_amdgcn_s_setprio(0);
                 __syncthreads();
-                stage(second ? n + 1 : n);
-                soften(n + 1);
+                stage_and_soften(second ? n + 1 : n, n + 1);
                 __syncthreads();
             }
             if (!second)
                 __syncthreads();
         } else {
-            auto load_both = [&] {
+            auto load_both = [&]() BQM_INLINE {
                 Places of;
                 spread(of, place_of());
                 look_up();
-                load_k(of);
+                load_k(kr, of);
                 load_v(of);
             };
-            auto store_both = [&](int n) {
-                store_k(k_of(n));
+            auto store_both = [&](int n) BQM_INLINE {
+                store_k(kr, k_of(n));
                 store_v(v_of(n));
             };
-            auto compute = [&](int n) {
+            auto compute = [&](int n) BQM_INLINE {
                 const int t0 = t00 + n * WK * S::TK;
                 if (!seen(t0))
                     return;
@@ -884,12 +906,13 @@ int launch_shape(const AttnArgs &a, hipStream_t stream)
 template <class T, class O, int DP>
 int launch_rows(const AttnArgs &a, int m, hipStream_t stream)
 {
+    constexpr int kWaves = DP > 128 ? 1 : DP > 64 ? 2 : 3;  // a SIMD's, by the registers
     if (m == 32)
-        return launch_shape<T, O, DP, 1, 4, 1, (DP > 128 ? 1 : 2)>(a, stream);
+        return launch_shape<T, O, DP, 1, 4, 1, kWaves>(a, stream);
     if constexpr (DP <= 128)
         if (m == 256)
             return launch_shape<T, O, DP, 8, 1, 2, 2>(a, stream);
-    return launch_shape<T, O, DP, 4, 1, 2, (DP > 128 ? 1 : 2)>(a, stream);
+    return launch_shape<T, O, DP, 4, 1, 2, kWaves>(a, stream);
 }
 
 template <class T, class O>
