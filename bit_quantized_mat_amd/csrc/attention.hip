@@ -101,18 +101,23 @@ __device__ __forceinline__ int row_hi(const AttnArgs &a, int kv_len, int pos)
     return a.causal ? min(kv_len, pos + 1) : kv_len;
 }
 
-__device__ __forceinline__ void load_sequence(const AttnArgs &a, int b, Tile &t)
+__device__ __forceinline__ void sequence_of(const AttnArgs &a, int b, int start, int next,
+                                            int len, Tile &t)
 {
-    // the same in all lanes: read once, kept in scalar registers
-    const int start = __builtin_amdgcn_readfirstlane(a.q_starts[b]);
-    const int next = __builtin_amdgcn_readfirstlane(a.q_starts[b + 1]);
-    const int len = __builtin_amdgcn_readfirstlane(a.kv_lens[b]);
     t.seq = b;
     t.q0 = min(max((int64_t)start, (int64_t)0), a.total_q);
     t.q_len = (int)min(max((int64_t)next - t.q0, (int64_t)0), a.total_q - t.q0);
     t.rows = t.q_len * a.group;
     const int64_t room = min((int64_t)a.max_pages * a.page_size, (int64_t)a.max_kv);
     t.kv_len = (int)min((int64_t)max(len, 0), room);
+}
+
+__device__ __forceinline__ void load_sequence(const AttnArgs &a, int b, Tile &t)
+{
+    // the same in all lanes: kept in scalar registers
+    sequence_of(a, b, __builtin_amdgcn_readfirstlane(a.q_starts[b]),
+                __builtin_amdgcn_readfirstlane(a.q_starts[b + 1]),
+                __builtin_amdgcn_readfirstlane(a.kv_lens[b]), t);
 }
 
 template <int M>
@@ -164,6 +169,68 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &a, int x, Tile &t)
         return false;
     load_range<M>(a, t);
     return true;
+}
+
+// Piece x of a launch of few rows: (tile, part) pairs that exist come first, whole
+// chunks before what they leave over, so that sequences of very different lengths
+// fill the card evenly and the places of pieces that do not exist come when all
+// others are under way. A lane counts a sequence's pieces, in groups of 64.
+constexpr int kCountedSeqs = 128;
+
+__device__ __forceinline__ int wave_scan(int v)
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(v, d, 64);
+        v += lane >= d ? u : 0;
+    }
+    return v;
+}
+
+template <int M>
+__device__ __forceinline__ bool find_piece(const AttnArgs &a, int x, Tile &t, int &part)
+{
+    constexpr int kGroups = kCountedSeqs / 64;
+    const int lane = threadIdx.x & 63;
+    int tiles[kGroups], whole[kGroups], tiles_upto[kGroups], whole_upto[kGroups];
+    int n_whole = 0;
+#pragma unroll
+    for (int g = 0; g < kGroups; g++) {
+        const int b = g * 64 + lane, bc = min(b, a.n_seqs - 1);
+        Tile s;
+        sequence_of(a, bc, a.q_starts[bc], a.q_starts[bc + 1], a.kv_lens[bc], s);
+        tiles[g] = b < a.n_seqs ? (s.rows + M - 1) / M : 0;
+        // by the widest any tile could be: a part too many is found empty later
+        const int base = s.kv_len - s.q_len;
+        const int seen = row_hi(a, s.kv_len, s.kv_len - 1) - row_lo(a, base);
+        whole[g] = seen > a.chunk ? tiles[g] * ((seen + a.chunk - 1) / a.chunk - 1) : 0;
+        tiles_upto[g] = wave_scan(tiles[g]);
+        whole_upto[g] = n_whole + wave_scan(whole[g]);
+        n_whole = __builtin_amdgcn_readlane(whole_upto[g], 63);
+    }
+    const bool left_over = x >= n_whole;
+    if (left_over)
+        x -= n_whole;
+    int before = 0;
+#pragma unroll
+    for (int g = 0; g < kGroups; g++) {
+        const int n = left_over ? tiles[g] : whole[g];
+        const int upto = left_over ? before + tiles_upto[g] : whole_upto[g];
+        const int all = __builtin_amdgcn_readlane(upto, 63);
+        if (x < all) {
+            const int k = __popcll(__ballot(upto <= x));
+            load_sequence(a, g * 64 + k, t);
+            const int i = x - (__builtin_amdgcn_readlane(upto, k) - __builtin_amdgcn_readlane(n, k));
+            const int n_tiles = __builtin_amdgcn_readlane(tiles[g], k);
+            t.tile = i % n_tiles;
+            part = left_over ? 0 : 1 + i / n_tiles;
+            load_range<M>(a, t);
+            return true;
+        }
+        before = all;
+    }
+    return false;
 }
 
 // Maximum and sum over a lane pair (l, l + 32): the two halves of a softmax row.
@@ -241,16 +308,23 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
     int x = blockIdx.x;
     const int head = x % a.n_heads;
     x /= a.n_heads;
-    const int split = x / a.tiles;
-    x -= split * a.tiles;
     Tile t;
-    if (!find_tile<S::M>(a, a.tiles - 1 - x, t))
-        return;
+    int split;
+    if (WK > 1 && a.n_splits > 1 && a.n_seqs <= kCountedSeqs) {
+        if (!find_piece<S::M>(a, x, t, split))
+            return;
+    } else {
+        split = a.n_splits - 1 - x / a.tiles;
+        if (!find_tile<S::M>(a, a.tiles - 1 - x % a.tiles, t))
+            return;
+    }
     const int parts = parts_of(a, t);
     if (split >= parts)
         return;
-    const int c0 = t.begin + split * a.chunk;
-    const int c1 = parts > 1 ? min(t.end, c0 + a.chunk) : t.end;
+    // part 0 is what whole chunks leave over; it goes last, and fills the gaps that
+    // the whole ones leave on the card
+    const int c1 = t.end - (parts - 1 - split) * a.chunk;
+    const int c0 = split == 0 ? t.begin : c1 - a.chunk;
 
     // this lane's row; rows past the end repeat the last and store nothing
     const int row_first = t.tile * S::M + wm * 32;
@@ -870,8 +944,10 @@ Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads, int wi
     // parts that fill the card, if every sequence had max_kv tokens
     int64_t chunk = std::max<int64_t>(
         kLeastChunk, room * workgroups / (few ? kWantedWorkgroups : kWantedTiles));
-    // with few rows a part costs little: cut long sequences among short ones too
-    if (few)
+    // Many sequences of few rows: cut the long among the short ones too (64 of 33 to
+    // 8192 tokens: 104 us at 1024 tokens a part, 110 at 512, 107 at 2048). Few
+    // sequences are cut enough already (2 of 131071: 188 us at 2048, 197 at 1024).
+    if (few && workgroups >= kWantedWorkgroups / 4)
         chunk = std::min(chunk,
                          std::max<int64_t>(kRaggedChunk, room * workgroups / kMostWorkgroups));
     // no more parts than the workspace holds, whose size does not know the window
