@@ -242,10 +242,10 @@ __device__ void extend_plan(const Pages &p, const Extend &e)
 {
     UsedPages pages;
     int64_t total, lo, hi, mine = 0;
-    const int64_t n_free = p.n_pages - pages.count(p);
     run_of(p.n_seqs, &lo, &hi);
     for (int64_t s = lo; s < hi; s++)
         mine += wish_of(p, e, s).need;
+    const int64_t n_free = p.n_pages - pages.count(p);
     int64_t rank = block_scan(mine, &total);
     int64_t granted = 0, refused = 0;
     for (int64_t s = lo; s < hi; s++) {
@@ -294,12 +294,12 @@ __device__ void fork_plan(const Pages &p, const Fork &f)
 {
     UsedPages pages;
     int64_t total, lo, hi, mine = 0;
-    const int64_t n_free = p.n_pages - pages.count(p);
     run_of(f.n, &lo, &hi);
     for (int64_t i = lo; i < hi; i++) {
         const int len = fork_length(p, f, i);
         mine += len > 0 && len % p.page_size != 0;
     }
+    const int64_t n_free = p.n_pages - pages.count(p);
     const int64_t rank0 = block_scan(mine, &total);
     give_pages(p, pages, f.free_list, total < n_free ? total : n_free);
     for (int64_t s = threadIdx.x; s < p.n_seqs; s += kPlanThreads)
