@@ -130,10 +130,13 @@ __device__ __forceinline__ void load_range(const AttnArgs &a, Tile &t)
     t.end = row_hi(a, t.kv_len, base + last);
 }
 
-// How many parts the tile's tokens are cut into.
+// How many parts the tile's tokens are cut into: at most n_splits, since n_splits
+// chunks hold the most tokens that a tile's rows can see.
 __device__ __forceinline__ int parts_of(const AttnArgs &a, const Tile &t)
 {
-    return t.end - t.begin > a.chunk ? (t.end - t.begin + a.chunk - 1) / a.chunk : 1;
+    return a.n_splits > 1 && t.end - t.begin > a.chunk
+               ? (t.end - t.begin + a.chunk - 1) / a.chunk
+               : 1;
 }
 
 // The last sequence b for which first(q_starts[b], b) <= x (first ascends with
@@ -200,7 +203,7 @@ __device__ __forceinline__ bool find_piece(const AttnArgs &a, int x, Tile &t, in
         const int b = g * 64 + lane, bc = min(b, a.n_seqs - 1);
         Tile s;
         sequence_of(a, bc, a.q_starts[bc], a.q_starts[bc + 1], a.kv_lens[bc], s);
-        tiles[g] = b < a.n_seqs ? (s.rows + M - 1) / M : 0;
+        tiles[g] = b < a.n_seqs && s.rows > 0 ? (s.rows - 1) / M + 1 : 0;
         // by the widest any tile could be: a part too many is found empty later
         const int base = s.kv_len - s.q_len;
         const int seen = row_hi(a, s.kv_len, s.kv_len - 1) - row_lo(a, base);
@@ -925,6 +928,8 @@ constexpr int64_t kManyTiles = 512;          // of 256 rows: two a compute unit
 constexpr int64_t kMostWorkgroups = 8192;    // most of them empty, where lengths differ
 constexpr int kLeastChunk = 256, kRaggedChunk = 1024;
 
+// window: 0 if none bounds what a tile's rows see between them (rows that see later
+// tokens reach to the sequence's end)
 Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads, int window)
 {
     const int64_t group = n_q_heads / c->n_heads;
@@ -1019,7 +1024,7 @@ int launch_paged_attention(const void *q, int64_t q_token, int64_t q_head, const
                            bool causal, int window, int out_dtype, void *workspace,
                            hipStream_t stream)
 {
-    const Plan p = plan_of(c, b, n_q_heads, window);
+    const Plan p = plan_of(c, b, n_q_heads, causal ? window : 0);
     AttnArgs a = {};
     a.q = q;
     a.k = static_cast<const u32x4 *>(c->k);

@@ -258,6 +258,9 @@ ATTN = [
     ([90, 1, 0], [7, 30, 2], 2, 4, 64, 16, False, 0),
     ([260], [70], 1, 2, 128, 16, False, 0),
     ([100], [40], 1, 2, 64, 16, False, 20),
+    ([1700, 900], [1500, 12], 1, 2, 64, 16, False, 300),
+    ([2000], [8], 1, 4, 64, 16, False, 100),
+    ([2100, 700], [3, 5], 1, 2, 64, 16, True, 900),
     # one sequence far along a long axis, and rows that fill several tiles
     ([5000], [1], 1, 4, 128, 16, True, 0),
     ([3001], [3], 2, 4, 64, 16, True, 0),
@@ -763,6 +766,7 @@ def _rows64(s, b, rows, h, scale, causal, window):
     ([3000, 2111], [2600, 2111], 8, 32, 128, 64, True, 700, "f16"),
     ([2300, 65, 2000], [2300, 65, 2000], 8, 56, 80, 16, True, 0, "bf16"),
     ([600, 64], [4100, 300], 8, 32, 128, 16, False, 0, "bf16"),
+    ([4200, 900], [4100, 700], 8, 32, 64, 16, False, 500, "bf16"),
 ])
 def test_attention_many_rows(bqm, lens, q_lens, H, Hq, D, ps, causal, window, dt):
     _say("attention many rows", lens, q_lens, H, Hq, D, ps, causal, window, dt)
