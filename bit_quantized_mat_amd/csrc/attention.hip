@@ -925,6 +925,7 @@ constexpr int kFewRows = 32;
 constexpr int64_t kWantedWorkgroups = 1024;  // four a compute unit, of which two run at once
 constexpr int64_t kWantedTiles = 512;        // the same for tiles of 128 rows, whose parts cost more
 constexpr int64_t kManyTiles = 512;          // of 256 rows: two a compute unit
+constexpr int64_t kManyTokens = 2048;
 constexpr int64_t kMostWorkgroups = 8192;    // most of them empty, where lengths differ
 constexpr int kLeastChunk = 256, kRaggedChunk = 1024;
 
@@ -936,9 +937,16 @@ Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads, int wi
     Plan p;
     const int64_t rows = b->total_q * group;
     const bool few = std::min<int64_t>(b->max_q, b->total_q) * group <= kFewRows;
-    // 256 rows read each key tile once where 128 read it twice, but want enough
-    // of them to give every compute unit its workgroups
-    const bool many = c->head_dim <= 128 && rows / 256 * c->n_heads >= kManyTiles;
+    int64_t seen = std::min<int64_t>(b->max_kv, (int64_t)b->max_pages * c->page_size);
+    if (window > 0)
+        seen = std::min<int64_t>(seen, window);
+    // 256 rows in two halves: heads of 65 to 128 values, enough tiles for two a
+    // compute unit, and enough tokens for a workgroup's start and end, which nothing
+    // covers, to be small (32 heads of 128, prompts of 4096 and 8192 tokens: 157 and
+    // 564 us, with 128 rows 170 and 583; of 2048, half the tiles: 83 and 61; four of
+    // 2048 with a window of 512: 118 and 111; heads of 64, 8192 tokens: 399 and 336).
+    const bool many = c->head_dim > 64 && c->head_dim <= 128 &&
+                      rows / 256 * c->n_heads >= kManyTiles && seen >= kManyTokens;
     const int m = p.m = few ? 32 : many ? 256 : 128;
     p.tiles = (int)(rows / m + b->n_seqs);
     // the most tokens a tile's rows see between them
@@ -990,7 +998,7 @@ int launch_rows(const AttnArgs &a, int m, hipStream_t stream)
     constexpr int kWaves = DP > 128 ? 1 : DP > 64 ? 2 : 3;  // a SIMD's, by the registers
     if (m == 32)
         return launch_shape<T, O, DP, 1, 4, 1, kWaves>(a, stream);
-    if constexpr (DP <= 128)
+    if constexpr (DP == 128)
         if (m == 256)
             return launch_shape<T, O, DP, 8, 1, 2, 2>(a, stream);
     return launch_shape<T, O, DP, 4, 1, 2, kWaves>(a, stream);
