@@ -20,7 +20,7 @@
 //   one token a sequence: memory. 64 sequences of 4096 tokens 203 us (5.3 TB/s; a
 //     large copy reaches 5.0), of 16384 771 us (5.6 TB/s); 64 of 33 to 8192 tokens
 //     104 us (4.2 TB/s), 2 of about 120000 182 us (5.3 TB/s).
-//   a prompt of 8192: issue and the workgroups' ends. 558 us, 986 TFLOP/s where a
+//   a prompt of 8192: issue and the workgroups' ends. 541 us, 1016 TFLOP/s where a
 //     large matrix product of the library reaches 1380; matrix units 43% busy, the
 //     vector unit's softmax beside them, 61 us of start and end of 1024 workgroups.
 //   one token over 37: latency, 8 us of which an empty launch is 4.
@@ -84,8 +84,9 @@ __device__ const u32x4 kZeros = {0, 0, 0, 0};
 
 typedef const __attribute__((address_space(1))) u32x4 *piece_ptr;
 
-// In the place of a token that there is none of: behind every span below 4 GiB.
-constexpr uint32_t kNoPlace = 0xffffffffu;
+// In the place of a token that there is none of, in pieces: behind every span below
+// 4 GiB, with any piece of a head added; and where places need all 32 bits.
+constexpr uint32_t kNoPlace = 0x0fffff00u, kNoWidePlace = 0xffffffffu;
 
 // The kernel's steps are lambdas called from several places; left to itself the
 // compiler makes calls of some, with the registers they share in memory.
@@ -301,7 +302,7 @@ struct Shape {
 
 // WAVES: a SIMD's. With eight waves the workgroup is two halves out of step: while
 // the four waves of one (one a SIMD) are at their matrix products, the others are
-// at their softmax, and a barrier has them change places (prompt of 8192: 558 us;
+// at their softmax, and a barrier has them change places (prompt of 8192: 558 us then;
 // two workgroups of four waves a compute unit, left to fall out of step by
 // themselves, 574 to 583). A wave with 64 rows would read half as much from LDS, but
 // its scores then come to lie in accumulator registers and are moved one by one:
@@ -378,7 +379,7 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
     // beyond a resource's offsets, are read through pointers.
     const u32x4 *const kh = a.k + (uint64_t)head * a.c_head, *const vh = a.v + (uint64_t)head * a.c_head;
     const __amdgpu_buffer_rsrc_t kb_rsrc = make_rsrc(kh, a.span), vb_rsrc = make_rsrc(vh, a.span);
-    const uint32_t piece_none = piece_ok ? 0u : kNoPlace;
+    const uint32_t none = a.span != 0 ? kNoPlace : kNoWidePlace;
     char *const buf = lds + wk * S::kTile * S::kBufs;
     auto k_of = [&](int n) { return buf + (S::kBufs > 1 ? n & 1 : 0) * S::kTile; };
     auto v_of = [&](int n) { return k_of(n) + S::TK * S::KS; };
@@ -400,10 +401,10 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         cplace -= over ? a.page_size : 0;
         cpage += over;
     };
-    // of lane l's token, in pieces; kNoPlace: none
+    // of lane l's token, in pieces
     auto place_of = [&]() BQM_INLINE {
         const uint32_t at = (uint32_t)page_id * a.c_page + (uint32_t)place * a.c_token;
-        return place >= 0 && (uint32_t)page_id < (uint32_t)a.n_pages ? at : kNoPlace;
+        return place >= 0 && (uint32_t)page_id < (uint32_t)a.n_pages ? at : none;
     };
     // this thread's rows' places
     typedef uint32_t Places[S::kLoads];
@@ -415,10 +416,10 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
     u32x4 kr[S::kLoads], vr[S::kLoads];
     // piece i of the thread's; none of a head's values beyond its own
     auto load = [&](const u32x4 *base, __amdgpu_buffer_rsrc_t rsrc, uint32_t of) BQM_INLINE -> u32x4 {
-        of |= piece_none;
+        of = piece_ok ? of : none;
         if (a.span != 0)
-            return ld_b128(rsrc, of == kNoPlace ? kNoPlace : (of + piece) * 16u);
-        return *(of == kNoPlace ? (piece_ptr)&kZeros : (piece_ptr)base + of + piece);
+            return ld_b128(rsrc, (of + piece) * 16u);
+        return *(of == kNoWidePlace ? (piece_ptr)&kZeros : (piece_ptr)base + of + piece);
     };
     auto load_k = [&](u32x4 (&r)[S::kLoads], const Places &of) BQM_INLINE {
 #pragma unroll
@@ -1065,7 +1066,7 @@ int launch_paged_attention(const void *q, int64_t q_token, int64_t q_head, const
     a.c_head = (uint32_t)(c->head_stride / 8);
     const uint64_t span = ((uint64_t)(c->n_pages - 1) * a.c_page +
                            (uint64_t)(c->page_size - 1) * a.c_token + c->head_dim / 8) * 16;
-    a.span = span < 0xfffff000ull ? (uint32_t)span : 0;
+    a.span = span <= 16ull * kNoPlace ? (uint32_t)span : 0;
     a.n_pages = (int)c->n_pages;
     a.n_seqs = b->n_seqs;
     a.max_pages = b->max_pages;
