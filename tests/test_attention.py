@@ -383,6 +383,40 @@ def test_attention_far_pages(bqm):
                        bqm.paged_attention(s.q, bqm.KvCache(s.k, s.v), s.batch(bqm)))
 
 
+def test_attention_pages_just_below_4_gib(bqm):
+    # the last places that 32-bit offsets of bytes reach, and heads shorter than a tile
+    D, H, ps = 80, 2, 64
+    P = 0xfffff000 // (ps * H * D * 2)
+    s = Setup([100, 300], [1, 20], H, D, ps, "f16", seed=13, n_q=4)
+    n = int(s.table.max()) + 1
+    k, v = (torch.empty(P, ps, H, D, dtype=DT["f16"], device="cuda") for _ in range(2))
+    k[P - n:], v[P - n:] = s.k[:n], s.v[:n]
+    b = bqm.KvBatch(_ints(np.where(s.table >= 0, s.table + P - n, -1)), _ints(s.lens), _ints(s.starts))
+    assert torch.equal(bqm.paged_attention(s.q, bqm.KvCache(k, v), b),
+                       bqm.paged_attention(s.q, bqm.KvCache(s.k, s.v), s.batch(bqm)))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,q_lens,H,Hq,D,ps,causal,window", [
+    # rows that fill tiles, their tokens cut into parts, uneven ones and one of a few tokens
+    ([2900], [40], 1, 4, 40, 16, True, 0),
+    ([1500, 0, 700, 2111], [50, 0, 3, 33], 2, 4, 64, 24, True, 0),
+    ([2500, 900], [130, 60], 1, 3, 64, 16, True, 1700),
+    ([1801, 40], [33, 40], 1, 4, 128, 16, True, 0),
+    ([1400], [200], 2, 2, 96, 7, False, 0),
+    ([1290], [35], 1, 2, 136, 16, True, 0),
+])
+def test_attention_parts_of_many_rows(bqm, lens, q_lens, H, Hq, D, ps, causal, window, dt):
+    _say("attention parts", lens, q_lens, H, Hq, D, ps, causal, window, dt)
+    s = Setup(lens, q_lens, H, D, ps, dt, seed=D + len(lens), n_q=Hq)
+    y = bqm.paged_attention(s.q, bqm.KvCache(s.k, s.v), s.batch(bqm), causal=causal, window=window)
+    _close_attention(_f64(y), s, D ** -0.5, causal, window)
+    b = s.batch(bqm, max_q=max(q_lens), max_kv=max(lens))
+    y = bqm.paged_attention(s.q, bqm.KvCache(s.k, s.v), b, causal=causal, window=window,
+                            out_dtype=torch.float32)
+    _close_attention(_f64(y), s, D ** -0.5, causal, window, "f32")
+
+
 def test_attention_is_repeatable(bqm):
     s = Setup([4000, 900, 33], [1, 17, 33], 2, 128, 16, "bf16", seed=12, n_q=8)
     cache, b = bqm.KvCache(s.k, s.v), s.batch(bqm)
