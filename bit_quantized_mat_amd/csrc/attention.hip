@@ -20,7 +20,7 @@
 //   one token a sequence: memory. 64 sequences of 4096 tokens 203 us (5.3 TB/s; a
 //     large copy reaches 5.0), of 16384 771 us (5.6 TB/s); 64 of 33 to 8192 tokens
 //     104 us (4.2 TB/s), 2 of about 120000 182 us (5.3 TB/s).
-//   a prompt of 8192: issue and the workgroups' ends. 541 us, 1016 TFLOP/s where a
+//   a prompt of 8192: issue and the workgroups' ends. 553 us, 995 TFLOP/s where a
 //     large matrix product of the library reaches 1380; matrix units 43% busy, the
 //     vector unit's softmax beside them, 61 us of start and end of 1024 workgroups.
 //   one token over 37: latency, 8 us of which an empty launch is 4.
@@ -302,9 +302,9 @@ struct Shape {
 
 // WAVES: a SIMD's. With eight waves the workgroup is two halves out of step: while
 // the four waves of one (one a SIMD) are at their matrix products, the others are
-// at their softmax, and a barrier has them change places (prompt of 8192: 558 us then;
+// at their softmax, and a barrier has them change places (prompt of 8192: 571 us;
 // two workgroups of four waves a compute unit, left to fall out of step by
-// themselves, 574 to 583). A wave with 64 rows would read half as much from LDS, but
+// themselves, 608). A wave with 64 rows would read half as much from LDS, but
 // its scores then come to lie in accumulator registers and are moved one by one:
 // 1040 us.
 template <class T, class O, int DP, int WM, int WK, int NT, int WAVES>
@@ -979,9 +979,9 @@ Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads, int wi
         seen = std::min<int64_t>(seen, window);
     // 256 rows in two halves: heads of 65 to 128 values, enough tiles for two a
     // compute unit, and enough tokens for a workgroup's start and end, which nothing
-    // covers, to be small (32 heads of 128, prompts of 4096 and 8192 tokens: 157 and
-    // 564 us, with 128 rows 170 and 583; of 2048, half the tiles: 83 and 61; four of
-    // 2048 with a window of 512: 118 and 111; heads of 64, 8192 tokens: 399 and 336).
+    // covers, to be small (32 heads of 128, prompts of 4096 and 8192 tokens: 156 and
+    // 571 us, with 128 rows 176 and 608; of 2048, half the tiles: 86 and 62; four of
+    // 2048 with a window of 512: 118 and 113; heads of 64, 8192 tokens: 399 and 336).
     const bool many = c->head_dim > 64 && c->head_dim <= 128 &&
                       rows / 256 * c->n_heads >= kManyTiles && seen >= kManyTokens;
     const int m = p.m = few ? 32 : many ? 256 : 128;
