@@ -5,10 +5,11 @@
 // The bookkeeping is ranks: request r of a call (counted in the requests' order)
 // takes the r-th lowest free page, so the result is a function of the inputs alone.
 // Ranks are two exclusive scans, over the requests and over the free pages; one
-// workgroup of 16 waves does both, and a second launch of one wave per row rewrites
-// the table. Tables of at most kOneLaunch entries take one launch for both. Latency
-// bounds these launches (scans and loads that follow each other): 2 to 7 us for 8
-// sequences, 7.3 us and 4.6 us for 480 sequences over 3115 pages.
+// workgroup of 16 waves does both at once (6.3 us for 4 forks, one after the other
+// 7.1), and a second launch of one wave per row rewrites the table. Tables of at most
+// kOneLaunch entries take one launch for both. Latency bounds these launches (scans and
+// loads that follow each other): 2 to 6 us for 8 sequences, 6.6 us and 4.6 us for 480
+// sequences over 3115 pages.
 #include <algorithm>
 
 #include "common.hpp"
@@ -27,48 +28,69 @@ constexpr uint32_t kMany = (1u << 30) + 1;
 
 __device__ __forceinline__ uint32_t add_up(uint32_t a, uint32_t b) { return min(a + b, kMany); }
 
-// Exclusive scan over the plan workgroup's threads (v at most kMany); *total is
-// everybody's.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *total)
+// Exclusive scans over the plan workgroup's threads, N at once (values at most kMany);
+// total is everybody's.
+template <int N>
+__device__ __forceinline__ void block_scan(uint32_t (&v)[N], uint32_t (&total)[N])
 {
-    __shared__ uint32_t sums[kWaves];
+    __shared__ uint32_t sums[N][kWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t upto = v;
+    uint32_t upto[N], before[N];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t u = __shfl_up(upto, d, 64);
-        upto = lane >= d ? add_up(upto, u) : upto;
+    for (int k = 0; k < N; k++)
+        upto[k] = v[k];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+            const uint32_t u = __shfl_up(upto[k], d, 64);
+            upto[k] = lane >= d ? add_up(upto[k], u) : upto[k];
+        }
+#pragma unroll
+    for (int k = 0; k < N; k++) {
+        before[k] = __shfl_up(upto[k], 1, 64);
+        before[k] = lane == 0 ? 0 : before[k];
     }
-    uint32_t before = __shfl_up(upto, 1, 64);
-    before = lane == 0 ? 0 : before;
     __syncthreads();  // the last call's readers are done
     if (lane == 63)
-        sums[wave] = upto;
-    __syncthreads();
-    uint32_t all = 0, waves_before = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; w++) {
-        waves_before = w == wave ? all : waves_before;
-        all = add_up(all, sums[w]);
+        for (int k = 0; k < N; k++)
+            sums[k][wave] = upto[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; k++) {
+        uint32_t all = 0, waves_before = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) {
+            waves_before = w == wave ? all : waves_before;
+            all = add_up(all, sums[k][w]);
+        }
+        total[k] = all;
+        v[k] = add_up(waves_before, before[k]);
     }
-    *total = all;
-    return add_up(waves_before, before);
 }
 
-__device__ __forceinline__ uint32_t block_max(uint32_t v)
+// The threads' greatest v, and the sum of their counts n (at most kMany).
+__device__ __forceinline__ void block_max_and_sum(uint32_t &v, uint32_t &n)
 {
-    __shared__ uint32_t tops[kWaves];
+    __shared__ uint32_t tops[kWaves], sums[kWaves];
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
+    for (int d = 32; d >= 1; d >>= 1) {
         v = max(v, (uint32_t)__shfl_xor(v, d, 64));
+        n = add_up(n, (uint32_t)__shfl_xor(n, d, 64));
+    }
     __syncthreads();
-    if ((threadIdx.x & 63) == 0)
+    if ((threadIdx.x & 63) == 0) {
         tops[threadIdx.x >> 6] = v;
+        sums[threadIdx.x >> 6] = n;
+    }
     __syncthreads();
+    n = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; w++)
+    for (int w = 0; w < kWaves; w++) {
         v = max(v, tops[w]);
-    return v;
+        n = add_up(n, sums[w]);
+    }
 }
 
 struct Pages {
@@ -87,11 +109,22 @@ constexpr int64_t kSegment = 64 * kWords;
 
 class UsedPages {
   public:
-    // All threads. Counts the pages in use.
-    __device__ int64_t count(const Pages &p)
+    // All threads. Sends out the first loads of count(), for what the caller reads
+    // meanwhile.
+    __device__ void start(const Pages &p) { read(p, 0, threadIdx.x >> 6, ahead_); }
+
+    // All threads, after start(). Counts the pages in use; beside that scan, the
+    // caller's: before is the sum of the threads' before this one, total of all.
+    __device__ int64_t count(const Pages &p, uint32_t mine = 0, uint32_t *before = nullptr,
+                             uint32_t *total = nullptr)
     {
-        int64_t used = 0;
-        for (int64_t at = 0; at < p.n_pages; at += kSegment)
+        uint32_t v[2] = {0, mine}, all[2];
+        int64_t used = load(p, 0, 0, v, all, true);
+        if (before) {
+            *before = v[1];
+            *total = all[1];
+        }
+        for (int64_t at = kSegment; at < p.n_pages; at += kSegment)
             used = load(p, at, used);
         return used;
     }
@@ -140,19 +173,41 @@ class UsedPages {
         return before;
     }
 
-    // The segment from page `at` on, `used` pages being in use before it; returns
-    // the count after it.
+    static constexpr int kAhead = 4;  // loads in flight of a thread
+    int ahead_[kAhead];
+
+    // Counts of word w's pages and of those a workgroup's stride of words apart
+    __device__ static void read(const Pages &p, int64_t at, int w, int (&r)[kAhead])
+    {
+        const int n = (int)min(kSegment, p.n_pages - at);
+#pragma unroll
+        for (int k = 0; k < kAhead; k++)
+            r[k] = p.refs[at + min((w + k * kWaves) * 64 + (int)(threadIdx.x & 63), n - 1)];
+    }
+
     __device__ int64_t load(const Pages &p, int64_t at, int64_t used)
+    {
+        uint32_t v[1] = {0}, all[1];
+        return load(p, at, used, v, all, false);
+    }
+
+    // The segment from page `at` on, `used` pages being in use before it; returns
+    // the count after it. v, total: block_scan's, the first place for this one's use.
+    template <int N>
+    __device__ int64_t load(const Pages &p, int64_t at, int64_t used, uint32_t (&v)[N],
+                            uint32_t (&total)[N], bool started)
     {
         const int n = (int)min(kSegment, p.n_pages - at), words = (n + 63) / 64;
         __syncthreads();  // the last segment's readers are done
-        constexpr int kAhead = 4;  // loads in flight of a thread
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
         for (int w0 = wave; w0 < words; w0 += kWaves * kAhead) {
             int r[kAhead];
+            if (started && w0 == wave)
 #pragma unroll
-            for (int k = 0; k < kAhead; k++)
-                r[k] = p.refs[at + min((w0 + k * kWaves) * 64 + lane, n - 1)];
+                for (int k = 0; k < kAhead; k++)
+                    r[k] = ahead_[k];
+            else
+                read(p, at, w0, r);
 #pragma unroll
             for (int k = 0; k < kAhead; k++) {
                 const int w = w0 + k * kWaves;
@@ -163,16 +218,17 @@ class UsedPages {
         }
         __syncthreads();
         constexpr int kPer = kWords / kPlanThreads;
-        uint32_t mine = 0, all;
+        v[0] = 0;
         for (int w = threadIdx.x * kPer; w < min(words, (int)(threadIdx.x + 1) * kPer); w++)
-            mine += __popcll(masks_()[w]);
-        int64_t first = used + block_scan(mine, &all);
+            v[0] += __popcll(masks_()[w]);
+        block_scan(v, total);
+        int64_t first = used + v[0];
         for (int w = threadIdx.x * kPer; w < min(words, (int)(threadIdx.x + 1) * kPer); w++) {
             before_()[w] = (int)first;
             first += __popcll(masks_()[w]);
         }
         __syncthreads();
-        return used + all;
+        return used + total[0];
     }
 };
 
@@ -242,12 +298,12 @@ __device__ void extend_plan(const Pages &p, const Extend &e)
 {
     UsedPages pages;
     int64_t lo, hi;
-    uint32_t total, mine = 0;
+    uint32_t rank, total, mine = 0;
+    pages.start(p);
     run_of(p.n_seqs, &lo, &hi);
     for (int64_t s = lo; s < hi; s++)
         mine = add_up(mine, wish_of(p, e, s).need);
-    const uint32_t n_free = (uint32_t)(p.n_pages - pages.count(p));
-    uint32_t rank = block_scan(mine, &total);
+    const uint32_t n_free = (uint32_t)(p.n_pages - pages.count(p, mine, &rank, &total));
     uint32_t granted = 0, refused = 0;
     for (int64_t s = lo; s < hi; s++) {
         const Wish w = wish_of(p, e, s);
@@ -262,11 +318,9 @@ __device__ void extend_plan(const Pages &p, const Extend &e)
         p.lens_out[s] = served ? max(p.lens[s], 0) + max(e.n_new[s], 0) : p.lens[s];
         rank = end;
     }
-    granted = block_max(granted);
-    uint32_t all;
-    block_scan(refused, &all);
+    block_max_and_sum(granted, refused);
     if (threadIdx.x == 0)
-        e.short_of[0] = (int)all;
+        e.short_of[0] = (int)refused;
     give_pages(p, pages, e.free_list, granted);
 }
 
@@ -295,19 +349,18 @@ __device__ void fork_plan(const Pages &p, const Fork &f)
 {
     UsedPages pages;
     int64_t lo, hi;
-    uint32_t total, mine = 0;
+    uint32_t rank, total, mine = 0;
+    pages.start(p);
     run_of(f.n, &lo, &hi);
     for (int64_t i = lo; i < hi; i++) {
         const int len = fork_length(p, f, i);
         mine += len > 0 && len % p.page_size != 0;
     }
-    const uint32_t n_free = (uint32_t)(p.n_pages - pages.count(p));
-    const uint32_t rank0 = block_scan(mine, &total);
+    const uint32_t n_free = (uint32_t)(p.n_pages - pages.count(p, mine, &rank, &total));
     give_pages(p, pages, f.free_list, min(total, n_free));
     for (int64_t s = threadIdx.x; s < p.n_seqs; s += kPlanThreads)
         f.fork_of[s] = -1;
     __syncthreads();
-    uint32_t rank = rank0, refused = 0;
     for (int64_t i = lo; i < hi; i++) {
         const int len = fork_length(p, f, i);
         int from = -1, to = -1, tail = 0;
@@ -317,8 +370,6 @@ __device__ void fork_plan(const Pages &p, const Fork &f)
                 if (rank < n_free) {
                     from = p.table[f.parents[i] * p.stride + len / p.page_size];
                     to = f.free_list[rank];
-                } else {
-                    refused++;
                 }
                 rank++;
             }
@@ -328,10 +379,8 @@ __device__ void fork_plan(const Pages &p, const Fork &f)
         f.moves[3 * i + 1] = to;
         f.moves[3 * i + 2] = to < 0 ? 0 : tail;
     }
-    uint32_t all;
-    block_scan(refused, &all);
     if (threadIdx.x == 0)
-        f.short_of[0] = (int)all;
+        f.short_of[0] = (int)(total - min(total, n_free));
 }
 
 __device__ void fork_row(const Pages &p, const Fork &f, int s)
@@ -393,6 +442,7 @@ __device__ void copy_refs(const Pages &p, int64_t first, int64_t step)
 __device__ void compact_plan(const Pages &p, int32_t *page_map, int32_t *moves)
 {
     UsedPages pages;
+    pages.start(p);
     const int64_t used = pages.count(p);
     // used pages below the cut; the rest of them move
     const int64_t low_used = used < p.n_pages ? pages.before(p, used) : used;
