@@ -938,16 +938,20 @@ struct Plan {
 };
 
 constexpr int kFewRows = 32;
-constexpr int64_t kWantedWorkgroups = 1024;  // four a compute unit, of which two run at once
-constexpr int64_t kLeastSaved = 512, kLeastSavedOf64 = 832;
+constexpr int64_t kLeastSaved = 512, kLeastSavedOf64 = 832, kLeastSavedFew = 256;
+constexpr int64_t kRaggedWorkgroups = 128;   // 16 of 100 to 8000 tokens: 30 us, uncut by this 37
 constexpr int64_t kManyTiles = 512;          // of 256 rows: two a compute unit
 constexpr int64_t kManyTokens = 2048;
 constexpr int64_t kMostWorkgroups = 8192;    // most of them empty, where lengths differ
 constexpr int kLeastChunk = 256, kRaggedChunk = 1024;
 
-// Tiles of 128 rows, parts counted, that a launch is cut into. The nearest number of
-// parts is taken, and one where several would spare a workgroup no more than
-// kLeastSaved tokens: writing, reading and joining the shares costs as much (28 heads
+// Workgroups, parts counted, that a launch is cut into.
+// Of 32 rows: no more than run at once, two a compute unit, since what does not takes
+// another round (24 tokens over 1126, heads of 128, 192 tiles: 33 us in two parts, 40
+// in three; 12 over 3000: 41 us in five, 45 in nine), and one part where several would
+// spare no more than kLeastSavedFew tokens (64 over 300: 22 us in one, 33 in two).
+// Of 128 rows: the nearest number of parts is taken, and one where several would spare
+// a workgroup no more than kLeastSaved tokens: their shares' way costs as much (28 heads
 // of 64 over 4, 17 x 72 tokens with a window of 1024: 49 us in two parts, 32 in one;
 // a prompt of 1024, heads of 128: 41 and 33). Heads of 64 run three workgroups a
 // compute unit (17 x 36 tokens over 4096: 70 us in one part, 55 in three; 17 x 108,
@@ -957,8 +961,10 @@ constexpr int kLeastChunk = 256, kRaggedChunk = 1024;
 // over 4096: 153 in one, 186 in two), but not where many share them (512 tokens over
 // 8192: 98 us in four parts, 113 in three). Of 256, one, in rounds (4 x 128 tokens over
 // 4096: 103 us in seven parts, 110 in six, 127 in eight).
-int64_t wanted_tiles(int head_dim, int64_t of_one)
+int64_t wanted_tiles(int head_dim, int64_t of_one, bool few)
 {
+    if (few)
+        return 512;
     if (head_dim <= 64)
         return 576;
     if (head_dim > 128)
@@ -992,22 +998,20 @@ Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads, int wi
         room = std::min<int64_t>(room, (int64_t)window + m / group + 1);
     const int64_t workgroups = (int64_t)p.tiles * c->n_heads;
     // parts that fill the card, if every sequence had max_q rows and max_kv tokens
-    int64_t chunk = room * workgroups / kWantedWorkgroups;
-    if (!few) {
-        // tiles of one sequence, and of all
-        const int64_t of_one = (std::min<int64_t>(b->max_q, b->total_q) * group + m - 1) / m;
-        const int64_t most_tiles = std::min<int64_t>(p.tiles, b->n_seqs * of_one) * c->n_heads;
-        const int64_t wanted = wanted_tiles(c->head_dim, of_one);
-        const int64_t parts = std::max<int64_t>(1, (wanted + most_tiles / 2) / most_tiles);
-        chunk = (room + parts - 1) / parts;
-        if (room - chunk <= (c->head_dim <= 64 ? kLeastSavedOf64 : kLeastSaved))
-            chunk = room;
-    }
+    // tiles of one sequence, and of all
+    const int64_t of_one = std::max<int64_t>(
+        1, (std::min<int64_t>(b->max_q, b->total_q) * group + m - 1) / m);
+    const int64_t most_tiles = std::min<int64_t>(p.tiles, b->n_seqs * of_one) * c->n_heads;
+    const int64_t wanted = wanted_tiles(c->head_dim, of_one, few);
+    const int64_t parts = std::max<int64_t>(1, (wanted + (few ? 0 : most_tiles / 2)) / most_tiles);
+    int64_t chunk = (room + parts - 1) / parts;
+    if (room - chunk <= (few ? kLeastSavedFew : c->head_dim <= 64 ? kLeastSavedOf64 : kLeastSaved))
+        chunk = room;
     chunk = std::max<int64_t>(kLeastChunk, chunk);
     // Many sequences of few rows: cut the long among the short ones too (64 of 33 to
     // 8192 tokens: 104 us at 1024 tokens a part, 110 at 512, 107 at 2048). Few
-    // sequences are cut enough already (2 of 131071: 188 us at 2048, 197 at 1024).
-    if (few && workgroups >= kWantedWorkgroups / 4)
+    // sequences are cut enough already (2 of 131071: 184 us at 4096, 188 at 2048, 197 at 1024).
+    if (few && workgroups >= kRaggedWorkgroups)
         chunk = std::min(chunk,
                          std::max<int64_t>(kRaggedChunk, room * workgroups / kMostWorkgroups));
     // no more parts than the workspace holds, whose size does not know the window
