@@ -19,7 +19,7 @@
 // What bounds it, measured on one MI355X (bf16, heads of 128, 32 over 8):
 //   one token a sequence: memory. 64 sequences of 4096 tokens 203 us (5.3 TB/s; a
 //     large copy reaches 5.0), of 16384 771 us (5.6 TB/s); 64 of 33 to 8192 tokens
-//     104 us (4.2 TB/s), 2 of about 120000 182 us (5.3 TB/s).
+//     104 us (4.2 TB/s), 2 of about 120000 176 us (5.4 TB/s).
 //   a prompt of 8192: issue and the workgroups' ends. 553 us, 995 TFLOP/s where a
 //     large matrix product of the library reaches 1380; matrix units 43% busy, the
 //     vector unit's softmax beside them, 61 us of start and end of 1024 workgroups.
@@ -850,8 +850,8 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
 
 // Joins the parts of rows whose tokens were cut. WAVES waves share a row and
 // take every WAVES-th part, several parts' loads in flight in each: four for the
-// many parts of a long sequence (64 rows of 62 parts 7.8 us; one wave a row took
-// 89), one where rows are many and parts few (2048 rows of up to 8: 5.6 us; a
+// many parts of a long sequence (64 rows of 62 parts 7.8 us, of 32 parts 5.6; one
+// wave a row took 89 for 62), one where rows are many and parts few (2048 rows of up to 8: 5.6 us; a
 // workgroup each 7.3). Latency bounds both: three loads that follow each other.
 constexpr int kMostParts = 1024;
 constexpr int kFewParts = 16;
