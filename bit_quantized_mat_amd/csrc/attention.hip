@@ -800,8 +800,10 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         }
         if (stores && parts > 1 && first == 0 && half == 0)
             a.part_ml[part_row + out_row] = make_float2(m, l);
-        if (careful && l == l)  // a sum of NaN has made the whole row so
-            left_out(stores, first, step);
+        // the lanes share out the tokens, so all of them take part, those too whose row
+        // a sum of NaN has made NaN already
+        if (careful)
+            left_out(stores && l == l, first, step);
     };
 
     if constexpr (WK == 1) {

@@ -1,0 +1,61 @@
+"""Attention where values, keys or queries are infinite or NaN: each row gets what
+it sees, and nothing of what it does not."""
+import sys
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_attention import Setup  # noqa: E402
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def bqm():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import bit_quantized_mat_amd as m
+    m.library()
+    return m
+
+
+def _diagonal_infinities(s, first):
+    """Value i of token first + i becomes infinite, for every value i of a head: one
+    token at each place of a wave's 64."""
+    for i in range(s.D):
+        j = first + i
+        s.v[int(s.table[0, j // s.ps]), j % s.ps, :, i] = INF
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("n,nan_at", [(64, 40), (128, 100), (130, 90)])
+def test_infinities_beside_rows_of_a_nan_key(bqm, n, nan_at, dt):
+    # rows from nan_at on see a NaN key; the rows before them in the same tile do
+    # not, and get every infinity they see
+    print("nan key", n, nan_at, dt, file=sys.stderr, flush=True)
+    s = Setup([n], [n], 1, 64, 16, dt, seed=40)
+    cache = bqm.KvCache(s.k, s.v)
+    clean = bqm.paged_attention(s.q, cache, s.batch(bqm))
+    _diagonal_infinities(s, 0)
+    s.k[int(s.table[0, nan_at // 16]), nan_at % 16] = NAN
+    y = bqm.paged_attention(s.q, cache, s.batch(bqm))[:, 0]
+    row, col = torch.arange(n, device="cuda")[:, None], torch.arange(64, device="cuda")[None]
+    assert torch.isnan(y[nan_at:]).all()
+    sees = (col <= row)[:nan_at]
+    assert torch.isposinf(y[:nan_at][sees]).all()
+    assert torch.equal(y[:nan_at][~sees], clean[:nan_at, 0][~sees])
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("n,first", [(64, 0), (150, 70), (6000, 0), (6000, 3333), (6000, 5936)])
+def test_infinities_beside_a_nan_query(bqm, n, first, dt):
+    # one token, four heads over one: the last one's query is NaN
+    print("nan query", n, first, dt, file=sys.stderr, flush=True)
+    s = Setup([n], [1], 1, 64, 16, dt, seed=41, n_q=4)
+    _diagonal_infinities(s, first)
+    s.q[0, 3] = NAN
+    y = bqm.paged_attention(s.q, bqm.KvCache(s.k, s.v), s.batch(bqm))
+    assert torch.isposinf(y[0, :3]).all()
+    assert torch.isnan(y[0, 3]).all()
