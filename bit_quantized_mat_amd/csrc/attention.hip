@@ -912,7 +912,10 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a)
 #pragma unroll 4
         for (int p = part0; p < parts; p += WAVES) {
             const f32x4 v = *reinterpret_cast<const f32x4 *>(src + p * rows * a.dim);
-            o += v * weight[p];
+            // an infinity stays one where its part's weight has come out as zero
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                o[i] += fabsf(v[i]) < INFINITY ? v[i] * weight[p] : v[i];
         }
     }
     if constexpr (WAVES == 1) {

@@ -59,3 +59,24 @@ def test_infinities_beside_a_nan_query(bqm, n, first, dt):
     y = bqm.paged_attention(s.q, bqm.KvCache(s.k, s.v), s.batch(bqm))
     assert torch.isposinf(y[0, :3]).all()
     assert torch.isnan(y[0, 3]).all()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("n,q_len,group", [(90, 1, 4), (6000, 1, 4), (6000, 8, 4), (3000, 40, 1)])
+def test_infinities_of_weights_near_zero(bqm, n, q_len, group, dt):
+    # the last tokens' scores are 200 above the others': their weights are e^-200,
+    # which is above zero, and an infinite value times that is infinite
+    s = Setup([n], [q_len], 1, 64, 16, dt, seed=42, n_q=group)
+    s.q.zero_()
+    s.q[..., 0] = 16.0
+    for j in range(n):
+        s.k[int(s.table[0, j // 16]), j % 16, 0, 0] = 12.5 if j >= n - q_len - 3 else 0.0
+    for j, d in ((5, 7), (n // 2, 20), (n // 2 + 1, 21)):
+        s.v[int(s.table[0, j // 16]), j % 16, 0, d] = INF
+    s.v[int(s.table[0, 9 // 16]), 9 % 16, 0, 30] = NAN
+    y = bqm.paged_attention(s.q, bqm.KvCache(s.k, s.v), s.batch(bqm), scale=1.0).float()
+    for d in (7, 20, 21):
+        assert torch.isposinf(y[..., d]).all(), d
+    assert torch.isnan(y[..., 30]).all()
+    rest = [d for d in range(64) if d not in (7, 20, 21, 30)]
+    assert torch.isfinite(y[..., rest]).all()
