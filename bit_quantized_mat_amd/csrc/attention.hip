@@ -436,7 +436,9 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         for (int i = 0; i < S::kLoads; i++)
             *reinterpret_cast<u32x4 *>(to + (row0 + i * S::kRowsPerLoad) * S::KS + piece * 16) = r[i];
     };
-    bool careful = false;  // keep infinities and NaN of V out of the products
+    // a tile's last resorts, each gone through again from the start: keep infinities
+    // and NaN of V out of the products; and weigh less, so that no sum overflows
+    bool careful = false, light = false;
     auto store_v = [&](char *to) BQM_INLINE {
 #pragma unroll
         for (int i = 0; i < S::kLoads; i++) {
@@ -448,6 +450,7 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
 
     f32x16 acc[DP / 32];
     float top, sum;  // of this lane's row; sum over its own tokens
+    float lift = 0.0f;  // log2 of what a weight at top comes to
 
     // whether a row of this wave sees the tile at t0
     auto seen = [&](int t0) { return t0 < hi_last && t0 + S::TK > lo_first; };
@@ -511,7 +514,7 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
                 for (int i = 0; i < 16; i++)
                     acc[dt][i] *= back;
         }
-        return top == -INFINITY ? 0.0f : top;  // nothing seen yet
+        return (top == -INFINITY ? 0.0f : top) - lift;  // the former: nothing seen yet
     };
     constexpr int kTiles = DP / 32, kChunks = 2 * NT;  // of 32 values, of 16 tokens
     auto weights = [&](f32x8 &e, const Scores &s, float base, int c, int first, int n) BQM_INLINE {
@@ -726,18 +729,30 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         }
         // A weight of zero that met an infinity or NaN in a value its row does not
         // see leaves NaN: then all again with those values as zeros, and rows that
-        // do see them get their due at the end.
+        // do see them get their due at the end. Sums of finite values above 2^120
+        // are taken again too, with weights so low that all of them together come to
+        // less than one: neither they nor the sum of four waves or many parts can
+        // then overflow, as sums of values near bfloat16's largest, 2^128, would at
+        // weights of up to 2^8. (Lower weights are lost below 2^-126, which is why
+        // they are not taken so from the start.) Rows of NaN sums are NaN throughout.
+        const float all = pair_sum(sum);
         bool odd = false;
 #pragma unroll
         for (int dt = 0; dt < DP / 32; dt++)
 #pragma unroll
             for (int i = 0; i < 16; i++)
-                odd |= !(fabsf(acc[dt][i]) < INFINITY);
-        if (careful || !__syncthreads_or(odd))
+                odd |= !(fabsf(acc[dt][i]) < 0x1p120f);
+        if (light || !__syncthreads_or(odd && all == all)) {
+            sum = all;
             break;
+        }
+        light = careful;
         careful = true;
+        if (light) {  // tokens < 2^(32 - clz), weights <= 2^(8 + lift)
+            const float low = (float)(__builtin_clz(max(c1 - c0, 1)) - 40);
+            lift = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(low)));
+        }
     }
-    sum = pair_sum(sum);
 
     const int64_t part_row = (int64_t)split * a.total_q * a.n_q_heads;
     // What the careful products left out: infinities and NaN that the rows see
@@ -799,7 +814,7 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
             }
         }
         if (stores && parts > 1 && first == 0 && half == 0)
-            a.part_ml[part_row + out_row] = make_float2(m, l);
+            a.part_ml[part_row + out_row] = make_float2(m - lift, l);
         // the lanes share out the tokens, so all of them take part, those too whose row
         // a sum of NaN has made NaN already
         if (careful)
@@ -906,6 +921,9 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a)
     if (lane == 0)
         sums[wave] = l;
     __syncthreads();
+    if constexpr (WAVES > 1)
+        l = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     f32x4 o = {};
     if (parts > 1 && lane * 4 < a.dim) {
         const float *src = a.part + row * a.dim + lane * 4;
@@ -913,24 +931,23 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a)
         for (int p = part0; p < parts; p += WAVES) {
             const f32x4 v = *reinterpret_cast<const f32x4 *>(src + p * rows * a.dim);
             // an infinity stays one where its part's weight has come out as zero
+            const float w = weight[p] * inv;  // before the sum: shares of a mean cannot overflow
 #pragma unroll
             for (int i = 0; i < 4; i++)
-                o[i] += fabsf(v[i]) < INFINITY ? v[i] * weight[p] : v[i];
+                o[i] += fabsf(v[i]) < INFINITY ? v[i] * w : v[i];
         }
     }
     if constexpr (WAVES == 1) {
         if (parts > 1 && lane * 4 < a.dim)
-            store4(static_cast<O *>(a.out) + row * a.dim + lane * 4,
-                   o * (l == 0.0f ? 0.0f : 1.0f / l));
+            store4(static_cast<O *>(a.out) + row * a.dim + lane * 4, o);
     } else {
         static_assert(WAVES == 4, "the workgroup's waves share one row");
         *reinterpret_cast<f32x4 *>(&shares[wave][lane * 4]) = o;
         __syncthreads();
-        l = (sums[0] + sums[1]) + (sums[2] + sums[3]);
         const int d = threadIdx.x;
         if (d < a.dim) {
             const float v = (shares[0][d] + shares[1][d]) + (shares[2][d] + shares[3][d]);
-            static_cast<O *>(a.out)[row * a.dim + d] = (O)(l == 0.0f ? 0.0f : v / l);
+            static_cast<O *>(a.out)[row * a.dim + d] = (O)v;
         }
     }
 }

@@ -1,5 +1,5 @@
-"""Attention where values, keys or queries are infinite or NaN: each row gets what
-it sees, and nothing of what it does not."""
+"""Attention where values, keys or queries are infinite, NaN or as large as their
+type holds: each row gets what it sees, and nothing of what it does not."""
 import sys
 
 import pytest
@@ -7,7 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_attention import Setup  # noqa: E402
+from test_attention import DT, Setup, UNIT, _close_attention, _f64  # noqa: E402
 
 INF, NAN = float("inf"), float("nan")
 
@@ -80,3 +80,33 @@ def test_infinities_of_weights_near_zero(bqm, n, q_len, group, dt):
     assert torch.isnan(y[..., 30]).all()
     rest = [d for d in range(64) if d not in (7, 20, 21, 30)]
     assert torch.isfinite(y[..., rest]).all()
+
+
+@pytest.mark.parametrize("out_dt", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,q_lens,H,Hq,D", [
+    ([50], [1], 1, 4, 64), ([3000], [1], 2, 8, 128), ([90], [90], 1, 2, 64), ([2900], [40], 1, 4, 40),
+    ([700, 0, 33], [400, 1, 1], 1, 2, 128), ([300], [8], 1, 2, 256), ([2300], [2300], 8, 64, 128),
+])
+def test_values_near_the_largest_of_the_type(bqm, lens, q_lens, H, Hq, D, out_dt):
+    # values up to 2^127 of either sign, sums of many of them above what 32 bits hold:
+    # the weighted means are not
+    print("large values", lens, q_lens, H, Hq, D, out_dt, file=sys.stderr, flush=True)
+    s = Setup(lens, q_lens, H, D, 16, "bf16", seed=43, n_q=Hq)
+    for b in range(len(lens)):
+        # of one sign, so that sums of many go as high as they can
+        s.vs[b] = (s.vs[b].abs().clamp(max=3.5) * 2.0 ** 125).to(DT["bf16"])
+        s.store(s.v, b, s.vs[b])
+    y = bqm.paged_attention(s.q, bqm.KvCache(s.k, s.v), s.batch(bqm), out_dtype=DT[out_dt])
+    assert torch.isfinite(y.float()).all()
+    if sum(q_lens) > 1000:  # rows 0, 97, 194, .. alone, the 64-bit form being slow
+        keep = torch.arange(0, q_lens[0], 97, device="cuda")
+        k, v = s.ks[0].double(), s.vs[0].double()
+        for h in (0, 37, 63):
+            x = (s.q[keep, h].double() @ k[:, h // 8].T.contiguous()) * D ** -0.5
+            x.masked_fill_(torch.arange(lens[0], device="cuda")[None] > keep[:, None], -INF)
+            want = torch.softmax(x, -1) @ v[:, h // 8].contiguous()
+            err = (y[keep, h].double() - want).abs() / want
+            # a weight's rounding to 8 bits above and one store; scores' rounding is far below
+            assert float(err.max()) <= 3.0 * UNIT["bf16"]
+    else:
+        _close_attention(_f64(y), s, D ** -0.5, True, 0, out_dt)
