@@ -450,7 +450,11 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
 
     f32x16 acc[DP / 32];
     float top, sum;  // of this lane's row; sum over its own tokens
-    float lift = 0.0f;  // log2 of what a weight at top comes to
+    // log2 of what a weight at top comes to. Half precision has only 2^-25 below 1
+    // (less comes out as zero) but 2^16 above: weights of up to 2^15 keep what is above
+    // 2^-32 of the row's largest; a million tokens below that come to less than an
+    // output's own rounding.
+    float lift = __is_same(T, _Float16) ? 7.0f : 0.0f;
 
     // whether a row of this wave sees the tile at t0
     auto seen = [&](int t0) { return t0 < hi_last && t0 + S::TK > lo_first; };

@@ -1,5 +1,7 @@
 """Attention where values, keys or queries are infinite, NaN or as large as their
-type holds: each row gets what it sees, and nothing of what it does not."""
+type holds, and where weights are far below the largest: each row gets what it
+sees, and nothing of what it does not."""
+import math
 import sys
 
 import pytest
@@ -7,7 +9,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_attention import DT, Setup, UNIT, _close_attention, _f64  # noqa: E402
+from test_attention import DT, Setup, UNIT, _close_attention, _f64, _ints  # noqa: E402
 
 INF, NAN = float("inf"), float("nan")
 
@@ -110,3 +112,33 @@ def test_values_near_the_largest_of_the_type(bqm, lens, q_lens, H, Hq, D, out_dt
             assert float(err.max()) <= 3.0 * UNIT["bf16"]
     else:
         _close_attention(_f64(y), s, D ** -0.5, True, 0, out_dt)
+
+
+@pytest.mark.parametrize("n,at,q_len,group,n_seqs,H", [
+    (20000, 6000, 1, 4, 1, 1), (120000, 0, 1, 8, 1, 1), (20000, 9, 40, 1, 1, 1), (9000, 8000, 4, 2, 1, 1),
+    (40000, 0, 40, 1, 64, 8), (20000, 100, 40, 4, 64, 2)])
+def test_small_weights_of_many_tokens_in_16_bits(bqm, n, at, q_len, group, n_seqs, H):
+    # one token whose value is 0 outweighs each of the others by e^18 (2^26): the
+    # others' mean, times their share of the sum, is the output. (The sequences
+    # share their pages; 64 of them fill the card without their tokens being cut.)
+    print("small weights", n, at, q_len, group, n_seqs, H, file=sys.stderr, flush=True)
+    s = Setup([n], [q_len], H, 64, 16, "f16", seed=44, n_q=group * H)
+    for x in (s.k, s.v):
+        x.zero_()
+    q = torch.zeros(q_len * n_seqs, group * H, 64, dtype=DT["f16"], device="cuda")
+    q[..., 0] = 4.0
+    pages = torch.tensor(s.table[0, :-(-n // 16)]).cuda()
+    s.v[pages] = 1000.0
+    page, place = int(s.table[0, at // 16]), at % 16
+    s.k[page, place, :, 0] = 4.5
+    s.v[page, place] = 0.0
+    batch = bqm.KvBatch(_ints(s.table.repeat(n_seqs, 0)), _ints([n] * n_seqs),
+                        _ints([i * q_len for i in range(n_seqs + 1)]), max_q=q_len)
+    y = bqm.paged_attention(q, bqm.KvCache(s.k, s.v), batch, scale=1.0, causal=False, out_dtype=torch.float32)
+    e = math.exp(-18.0)
+    want = 1000.0 * (n - 1) * e / (1.0 + (n - 1) * e)
+    # a weight is kept to 2^-12 of itself or to 2^-32 of the row's largest; fp32 sums of
+    # n terms and the exponential beside that
+    bound = want * (2.0 ** -11 + n * 2.0 ** -24 + 2.0 ** -18) + 1000.0 * (n - 1) * 2.0 ** -32
+    err = float((y.double() - want).abs().max())
+    assert err <= bound, (err, want, bound)
