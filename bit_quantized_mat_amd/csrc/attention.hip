@@ -541,6 +541,12 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
     // go the exponentials and the operand reads of the next 16, in this order.
     auto weigh_and_multiply = [&](const Scores &s, float base, const char *v) BQM_INLINE {
         constexpr int kShare = 8 / kTiles;
+        // With few rows, where memory bounds the kernel and the matrix units are 7%
+        // busy, what a weight's rounding leaves over is multiplied too: weights of twice
+        // the bits (64 sequences of 300 tokens 20.8 -> 21.3 us, 2 of about 120000 171.3 ->
+        // 171.5). With many rows the products are what the kernel does, and that would be
+        // three for every two.
+        constexpr bool kRest = WM == 1;
         f32x8 e;
         Op f[2][kTiles];
 #pragma unroll
@@ -552,9 +558,14 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         for (int c = 0; c < kChunks; c++) {
             // rounded to the cache's type: the matrix cores take no wider operand
             const Op p = __builtin_convertvector(e, Op);
+            Op rest;
+            if constexpr (kRest)
+                rest = __builtin_convertvector(e - __builtin_convertvector(p, f32x8), Op);
 #pragma unroll
             for (int dt = 0; dt < kTiles; dt++) {
                 acc[dt] = mfma(f[c % 2][dt], p, acc[dt]);
+                if constexpr (kRest)
+                    acc[dt] = mfma(f[c % 2][dt], rest, acc[dt]);
                 if (c + 1 < kChunks) {
                     f[(c + 1) % 2][dt] = read_v(v, c + 1, dt);
                     weights(e, s, base, c + 1, dt * kShare, kShare);
