@@ -254,6 +254,8 @@ struct Fork {
     int32_t *moves, *short_of;
     int32_t *free_list;  // workspace, as above
     int32_t *fork_of;    // [n_seqs] the fork whose child the row is, -1: none
+    int32_t *tokens;     // [n] of each fork's parent, before any row is written: a parent
+                         // may itself be a child, whose length in place changes meanwhile
     int n;
 };
 
@@ -375,6 +377,7 @@ __device__ void fork_plan(const Pages &p, const Fork &f)
             }
             f.fork_of[f.children[i]] = (int)i;
         }
+        f.tokens[i] = len;
         f.moves[3 * i] = from;
         f.moves[3 * i + 1] = to;
         f.moves[3 * i + 2] = to < 0 ? 0 : tail;
@@ -395,7 +398,7 @@ __device__ void fork_row(const Pages &p, const Fork &f, int s)
         return;
     }
     const int to = f.moves[3 * i + 1];
-    int len = fork_length(p, f, i);
+    int len = f.tokens[i];
     if (len % p.page_size != 0 && to < 0)
         len = 0;  // no page was free
     const int full = len / p.page_size;
@@ -647,7 +650,8 @@ int launch_kv_fork(const bqm_kv_pages *in, const bqm_kv_pages *out, const int32_
 {
     const Pages p = pages_of(in, out, page_size);
     int32_t *ws = static_cast<int32_t *>(workspace);
-    const Fork f = {parents, children, moves, short_of, ws, ws + p.n_pages, n};
+    int32_t *per_seq = ws + p.n_pages;
+    const Fork f = {parents, children, moves, short_of, ws, per_seq, per_seq + p.n_seqs, n};
     return launch_upkeep(fork_kernel<true, true>, fork_kernel<true, false>,
                          fork_kernel<false, true>, 1, p, stream, f);
 }

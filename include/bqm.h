@@ -509,8 +509,9 @@ BQM_API int kv_extend(const bqm_kv_pages *in, const bqm_kv_pages *out, const int
  * the tokens of parents[i]: its full pages shared, a partly filled last page
  * as a new page, for whose tokens moves[i] = (from, to, tokens) is written
  * (-1, -1, 0 where there is none) for kv_copy_pages. A fork that finds no free
- * page leaves its child empty and is counted in short_of[0]. Forks whose row
- * ids lie outside [0, n_seqs) are left out.
+ * page leaves its child empty and is counted in short_of[0]. Parents are as `in`
+ * has them: one that is itself a child of the call holds nothing, and so does
+ * its child then. Forks whose row ids lie outside [0, n_seqs) are left out.
  *   parents, children [n]; moves [n][3]. 0 <= n <= n_seqs. */
 BQM_API int kv_fork(const bqm_kv_pages *in, const bqm_kv_pages *out, const int32_t *parents,
                     const int32_t *children, int32_t n, int32_t page_size, int32_t *moves,
