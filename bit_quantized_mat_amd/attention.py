@@ -6,6 +6,11 @@ What a caller keeps between calls are three small objects over its own tensors:
 pages) and ``KvBatch`` (the new tokens of a step). The functions are those of
 the native module ``_attention`` (``binding/attention.cpp``), which checks and
 marshals arguments; the kernels behind ``include/bqm.h`` compute.
+
+``stream=`` runs a call there instead of on the current stream, as if it were the
+current one: new outputs and workspaces are that stream's memory (outputs also
+count as used by the caller's current stream). What a call reads must be ready
+on its stream, and not be let go of before the call has run.
 """
 import ctypes
 import math

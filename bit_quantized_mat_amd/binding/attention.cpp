@@ -4,6 +4,8 @@
 // Native, because the smallest of these kernels take 2 to 8 us: the same checks
 // in Python over ctypes took 12 to 14 us a call.
 #include <ATen/ops/empty.h>
+#include <c10/core/DeviceGuard.h>
+#include <c10/core/StreamGuard.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/pybind.h>
@@ -106,35 +108,62 @@ std::optional<at::ScalarType> dtype_of(const py::object &d)
     return reinterpret_cast<THPDtype *>(d.ptr())->scalar_type;
 }
 
-// The stream a call runs on: the one given, or the GPU's current one.
-void *stream_of(const py::object &stream, int dev)
-{
-    const py::object s =
-        stream.is_none()
-            ? py::reinterpret_steal<py::object>(PyObject_CallFunction(g_raw_stream, "i", dev))
-            : stream.attr("cuda_stream");
-    if (!s)
-        throw py::error_already_set();
-    void *p = PyLong_AsVoidPtr(s.ptr());
-    if (PyErr_Occurred())
-        throw py::error_already_set();
-    return p;
-}
+// Where a call runs: on the GPU of its tensors, on the stream given or on the GPU's
+// current one. Both are the current ones while this lives, so that what the call
+// allocates is the stream's own: memory of another stream may be in use there still,
+// by kernels of a call that has returned.
+struct On {
+    c10::OptionalDeviceGuard device;
+    c10::OptionalStreamGuard guard;
+    std::optional<c10::Stream> caller;  // the stream that was current, where that is another
+    void *p;
 
-Tensor empty(at::IntArrayRef sizes, at::ScalarType type, const Tensor &like)
-{
-    return at::empty(sizes, like.options().dtype(type));
-}
+    On(const py::object &stream, int dev)
+    {
+        if (stream.is_none()) {
+            device.reset_device(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+        } else {
+            const auto s = c10::Stream::unpack3(
+                stream.attr("stream_id").cast<int64_t>(),
+                (c10::DeviceIndex)stream.attr("device_index").cast<int>(),
+                (c10::DeviceType)stream.attr("device_type").cast<int>());
+            if (s.device_type() != c10::kCUDA || s.device_index() != dev)
+                bad_value("stream is not one of GPU " + std::to_string(dev));
+            guard.reset_stream(s);
+            if (*guard.original_stream() != s)
+                caller = guard.original_stream();
+        }
+        const py::object raw =
+            stream.is_none()
+                ? py::reinterpret_steal<py::object>(PyObject_CallFunction(g_raw_stream, "i", dev))
+                : stream.attr("cuda_stream");
+        if (!raw)
+            throw py::error_already_set();
+        p = PyLong_AsVoidPtr(raw.ptr());
+        if (PyErr_Occurred())
+            throw py::error_already_set();
+    }
 
-// A workspace: the caller's, or one of this call alone; on a stream other than
-// the current one the allocator is told, so that it hands the memory on only
-// after the call.
+    // A new output: the caller's current stream will use it too, and the allocator is
+    // told so.
+    Tensor empty(at::IntArrayRef sizes, at::ScalarType type, const Tensor &like) const
+    {
+        Tensor t = at::empty(sizes, like.options().dtype(type));
+        if (caller)
+            t.record_stream(*caller);
+        return t;
+    }
+};
+
+// A workspace: the caller's, or one of this call alone, which the stream's next call
+// may have again.
 struct Scratch {
     Tensor t;
     void *p = nullptr;
     size_t bytes = 0;
 
-    Scratch(const OptTensor &given, size_t need, const Tensor &like, const py::object &stream)
+    // (`On` stands for its own lifetime: the memory is taken from its stream's)
+    Scratch(const OptTensor &given, size_t need, const Tensor &like, const On &)
     {
         if (given) {
             t = *given;
@@ -145,9 +174,7 @@ struct Scratch {
         } else if (need == 0) {
             return;
         } else {
-            t = empty({(int64_t)need}, at::kByte, like);
-            if (!stream.is_none())
-                py::cast(t).attr("record_stream")(stream);
+            t = at::empty({(int64_t)need}, like.options().dtype(at::kByte));
         }
         p = t.data_ptr();
         bytes = (size_t)t.size(0);
@@ -255,13 +282,14 @@ Tensor rope_table_(const Tensor &inv_freq, int64_t n_pos, double scale, const Op
         bad_value("inv_freq must be contiguous");
     if (n_pos < 0)
         bad_value("n_pos must not be negative");
-    const Tensor out = out_ ? *out_ : empty({n_pos, n, 2}, at::kFloat, inv_freq);
+    const On on(stream, inv_freq.get_device());
+    const Tensor out = out_ ? *out_ : on.empty({n_pos, n, 2}, at::kFloat, inv_freq);
     const Angles a(out, inv_freq.get_device());
     if (a.n_pos != n_pos || a.n_freq != n)
         bad_value("out must be [n_pos, n_freq, 2]");
     done("rope_table",
          rope_table(static_cast<double *>(inv_freq.data_ptr()), a.p, n_pos, to_int32(n, "n_freq"),
-                    scale, stream_of(stream, inv_freq.get_device())));
+                    scale, on.p));
     return out;
 }
 
@@ -272,7 +300,8 @@ Tensor rope_(const Tensor &x, const Tensor &table, const Tensor &positions, bool
     heads(x, "x");
     const int dev = x.get_device();
     const auto want = dtype_of(out_dtype);
-    const Tensor out = out_ ? *out_ : empty(x.sizes(), want.value_or(x.scalar_type()), x);
+    const On on(stream, dev);
+    const Tensor out = out_ ? *out_ : on.empty(x.sizes(), want.value_or(x.scalar_type()), x);
     if (out_) {
         heads(out, "out", dev);
         if (want)
@@ -288,8 +317,7 @@ Tensor rope_(const Tensor &x, const Tensor &table, const Tensor &positions, bool
         done("rope",
              rope(x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0),
                   out.stride(1), pos, a.p, T, to_int32(x.size(1), "x"), to_int32(x.size(2), "x"),
-                  a.n_pos, to_int32(a.n_freq, "table"), interleaved, inverse, in, to,
-                  stream_of(stream, dev)));
+                  a.n_pos, to_int32(a.n_freq, "table"), interleaved, inverse, in, to, on.p));
     return out;
 }
 
@@ -309,6 +337,7 @@ OptTensor rope_kv_append_(const OptTensor &q, const Tensor &k, const Tensor &v,
         return (t.size(1) <= 1 || t.stride(1) == D) && (T <= 1 || t.stride(0) == k.stride(0));
     };
     bool same = even(k) && even(v);
+    const On on(stream, dev);
     OptTensor out;
     if (q) {
         heads(*q, "q", dev);
@@ -316,7 +345,7 @@ OptTensor rope_kv_append_(const OptTensor &q, const Tensor &k, const Tensor &v,
         if (q->size(0) != T || q->size(2) != D)
             bad_value("q must be [total_q, n_q_heads, head_dim] of k's tokens and values");
         same = same && even(*q);
-        out = q_out ? *q_out : empty(q->sizes(), cache.k.scalar_type(), cache.k);
+        out = q_out ? *q_out : on.empty(q->sizes(), cache.k.scalar_type(), cache.k);
         if (q_out) {
             gpu(*out, "q_out", 3, dev);
             typed(*out, "q_out", cache.k.scalar_type());
@@ -335,7 +364,7 @@ OptTensor rope_kv_append_(const OptTensor &q, const Tensor &k, const Tensor &v,
              rope_kv_append(q ? q->data_ptr() : nullptr, k.data_ptr(), v.data_ptr(), k.stride(0),
                             out ? out->data_ptr() : nullptr, &cache.c, &b, pos, a.p, a.n_pos,
                             to_int32(a.n_freq, "table"), interleaved,
-                            q ? to_int32(q->size(1), "q") : 0, in, stream_of(stream, dev)));
+                            q ? to_int32(q->size(1), "q") : 0, in, on.p));
     return out;
 }
 
@@ -360,7 +389,8 @@ Tensor paged_attention_(const Tensor &q, const KvCache &cache, const KvBatch &ba
         bad_value("q has heads of " + std::to_string(D) + " values, the cache of " +
                   std::to_string(cache.c.head_dim));
     const auto want = dtype_of(out_dtype);
-    const Tensor out = out_ ? *out_ : empty(q.sizes(), want.value_or(q.scalar_type()), q);
+    const On on(stream, dev);
+    const Tensor out = out_ ? *out_ : on.empty(q.sizes(), want.value_or(q.scalar_type()), q);
     if (out_) {
         gpu(out, "out", 3, dev);
         if (want)
@@ -371,12 +401,11 @@ Tensor paged_attention_(const Tensor &q, const KvCache &cache, const KvBatch &ba
     const bqm_kv_batch b = batch.of(T, cache);
     const int to = code_of(out.scalar_type());
     if (T) {
-        const Scratch w(workspace, paged_attention_workspace_bytes(&cache.c, &b, H), q, stream);
+        const Scratch w(workspace, paged_attention_workspace_bytes(&cache.c, &b, H), q, on);
         done("paged_attention",
              paged_attention(q.data_ptr(), q.stride(0), q.stride(1), &cache.c, &b, out.data_ptr(),
                              H, (float)scale.value_or(1.0 / std::sqrt((double)D)), causal,
-                             to_int32(window, "window"), to, w.p, w.bytes,
-                             stream_of(stream, dev)));
+                             to_int32(window, "window"), to, w.p, w.bytes, on.p));
     }
     return out;
 }
@@ -418,10 +447,12 @@ struct PagesArg {
 
 // The state read and the one written.
 struct InOut {
-    PagesArg in, out;
+    PagesArg in;
+    On on;
+    PagesArg out;
     py::object result;
 
-    static PagesArg out_of(const PagesArg &in, const py::object &given)
+    static PagesArg out_of(const PagesArg &in, const py::object &given, const On &on)
     {
         if (!given.is_none()) {
             PagesArg o = PagesArg::from(given, "out", in.dev);
@@ -429,13 +460,14 @@ struct InOut {
                 bad_value("out differs from pages in its sizes");
             return o;
         }
-        return PagesArg(empty(in.table.sizes(), at::kInt, in.table),
-                        empty(in.lens.sizes(), at::kInt, in.lens),
-                        empty(in.refs.sizes(), at::kInt, in.refs), "out");
+        return PagesArg(on.empty(in.table.sizes(), at::kInt, in.table),
+                        on.empty(in.lens.sizes(), at::kInt, in.lens),
+                        on.empty(in.refs.sizes(), at::kInt, in.refs), "out");
     }
 
-    InOut(const py::object &pages, const py::object &given)
-        : in(PagesArg::from(pages, "pages")), out(out_of(in, given)), result(given)
+    InOut(const py::object &pages, const py::object &given, const py::object &stream)
+        : in(PagesArg::from(pages, "pages")), on(stream, in.dev), out(out_of(in, given, on)),
+          result(given)
     {
         if (given.is_none())
             result = py::reinterpret_borrow<py::object>(g_pages)(out.table, out.lens, out.refs);
@@ -445,13 +477,13 @@ struct InOut {
 py::tuple kv_extend_(const py::object &pages, const Tensor &n_new, int64_t page_size,
                      const py::object &out, const OptTensor &workspace, const py::object &stream)
 {
-    InOut s(pages, out);
-    const Tensor short_of = empty({1}, at::kInt, s.in.lens);
-    const Scratch w(workspace, kv_pages_workspace_bytes(&s.in.p), s.in.lens, stream);
+    InOut s(pages, out, stream);
+    const Tensor short_of = s.on.empty({1}, at::kInt, s.in.lens);
+    const Scratch w(workspace, kv_pages_workspace_bytes(&s.in.p), s.in.lens, s.on);
     done("kv_extend",
          kv_extend(&s.in.p, &s.out.p, ints(n_new, "n_new", s.in.p.n_seqs, s.in.dev),
                    to_int32(page_size, "page_size"), static_cast<int32_t *>(short_of.data_ptr()),
-                   w.p, w.bytes, stream_of(stream, s.in.dev)));
+                   w.p, w.bytes, s.on.p));
     return py::make_tuple(s.result, short_of);
 }
 
@@ -459,12 +491,12 @@ py::tuple kv_fork_(const py::object &pages, const Tensor &parents, const Tensor 
                    int64_t page_size, const py::object &out, const OptTensor &workspace,
                    const py::object &stream)
 {
-    InOut s(pages, out);
+    InOut s(pages, out, stream);
     gpu(parents, "parents", 1, s.in.dev);
     const int64_t n = parents.size(0);
-    const Tensor moves = empty({n, 3}, at::kInt, s.in.lens);
-    const Tensor short_of = empty({1}, at::kInt, s.in.lens);
-    const Scratch w(workspace, kv_pages_workspace_bytes(&s.in.p), s.in.lens, stream);
+    const Tensor moves = s.on.empty({n, 3}, at::kInt, s.in.lens);
+    const Tensor short_of = s.on.empty({1}, at::kInt, s.in.lens);
+    const Scratch w(workspace, kv_pages_workspace_bytes(&s.in.p), s.in.lens, s.on);
     int32_t *one = static_cast<int32_t *>(short_of.data_ptr());
     // an empty array has no address: any other stands for it
     auto some = [&](void *p) { return p ? static_cast<int32_t *>(p) : one; };
@@ -472,32 +504,32 @@ py::tuple kv_fork_(const py::object &pages, const Tensor &parents, const Tensor 
          kv_fork(&s.in.p, &s.out.p, some(ints(parents, "parents", n, s.in.dev)),
                  some(ints(children, "children", n, s.in.dev)), to_int32(n, "parents"),
                  to_int32(page_size, "page_size"), some(moves.data_ptr()), one, w.p, w.bytes,
-                 stream_of(stream, s.in.dev)));
+                 s.on.p));
     return py::make_tuple(s.result, moves, short_of);
 }
 
 py::object kv_free_(const py::object &pages, const Tensor &seqs, const py::object &out,
                     const py::object &stream)
 {
-    InOut s(pages, out);
+    InOut s(pages, out, stream);
     gpu(seqs, "seqs", 1, s.in.dev);
     const int64_t n = seqs.size(0);
     const int32_t *p = ints(seqs, "seqs", n, s.in.dev);
     done("kv_free", kv_free(&s.in.p, &s.out.p, n ? p : s.in.p.lens, to_int32(n, "seqs"),
-                            stream_of(stream, s.in.dev)));
+                            s.on.p));
     return s.result;
 }
 
 py::tuple kv_compact_(const py::object &pages, int64_t page_size, const py::object &out,
                       const py::object &stream)
 {
-    InOut s(pages, out);
-    const Tensor moves = empty({s.in.p.n_pages / 2, 3}, at::kInt, s.in.lens);
-    const Tensor page_map = empty({s.in.p.n_pages}, at::kInt, s.in.lens);
+    InOut s(pages, out, stream);
+    const Tensor moves = s.on.empty({s.in.p.n_pages / 2, 3}, at::kInt, s.in.lens);
+    const Tensor page_map = s.on.empty({s.in.p.n_pages}, at::kInt, s.in.lens);
     int32_t *map = static_cast<int32_t *>(page_map.data_ptr());
     int32_t *m = moves.numel() ? static_cast<int32_t *>(moves.data_ptr()) : map;
     done("kv_compact", kv_compact(&s.in.p, &s.out.p, to_int32(page_size, "page_size"), map, m,
-                                  stream_of(stream, s.in.dev)));
+                                  s.on.p));
     return py::make_tuple(s.result, moves, page_map);
 }
 
@@ -507,10 +539,11 @@ void kv_copy_pages_(const KvCache &cache, const Tensor &moves, const py::object 
     typed(moves, "moves", at::kInt);
     if (moves.size(1) != 3 || !moves.is_contiguous())
         bad_value("moves must be contiguous [n, 3]");
-    if (moves.size(0))
-        done("kv_copy_pages",
-             kv_copy_pages(&cache.c, static_cast<int32_t *>(moves.data_ptr()), moves.size(0),
-                           stream_of(stream, cache.dev)));
+    if (moves.size(0)) {
+        const On on(stream, cache.dev);
+        done("kv_copy_pages", kv_copy_pages(&cache.c, static_cast<int32_t *>(moves.data_ptr()),
+                                            moves.size(0), on.p));
+    }
 }
 
 }  // namespace
