@@ -415,9 +415,21 @@ _ATTENTION = frozenset((
     "kv_compact", "kv_copy_pages"))
 
 
+def _later(name):
+    """In the place of a name whose library is not there: its calls load it or raise."""
+    def call(*args, **kwargs):
+        from . import attention
+        return getattr(attention, name)(*args, **kwargs)
+    call.__name__ = call.__qualname__ = name
+    return call
+
+
 def __getattr__(name):
     if name not in _ATTENTION:
         raise AttributeError("module %r has no attribute %r" % (__name__, name))
-    from . import attention
+    try:
+        from . import attention
+    except (ImportError, OSError, RuntimeError):
+        return _later(name)  # what is missing is said when it is called
     value = globals()[name] = getattr(attention, name)
     return value
