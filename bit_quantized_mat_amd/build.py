@@ -5,6 +5,7 @@ side, ``binding/attention.cpp``, into ``_attention.so`` beside it."""
 import concurrent.futures
 import glob
 import os
+import shutil
 import subprocess
 import sys
 
@@ -66,14 +67,33 @@ def _compile(srcs, out, verbose):
                 os.remove(o)
 
 
-def _compile_binding(obj, verbose):
-    """The binding's object: host code against torch's headers."""
+def _binding_includes():
     import sysconfig
 
     import torch
     root = os.path.join(os.path.dirname(torch.__file__), "include")
-    inc = [root, os.path.join(root, "torch", "csrc", "api", "include"),
-           sysconfig.get_paths()["include"]]
+    return [root, os.path.join(root, "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"]]
+
+
+def _binding_lacks():
+    """What the binding's build needs, beside the C library, and does not find; or None."""
+    if shutil.which(CXX) is None:
+        return CXX
+    try:
+        inc = _binding_includes()
+    except ImportError:
+        return "torch"
+    for d, f in ((inc[0], "torch/csrc/utils/pybind.h"), (inc[2], "Python.h")):
+        if not os.path.exists(os.path.join(d, f)):
+            return f
+    return None
+
+
+def _compile_binding(obj, verbose):
+    """The binding's object: host code against torch's headers."""
+    import torch
+    inc = _binding_includes()
     _run([CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
           *[a for i in inc for a in ("-isystem", i)], "-c", BINDING_SRC, "-o", obj], verbose)
@@ -91,7 +111,18 @@ def _link_binding(obj, verbose):
 
 def build(verbose: bool = False) -> str:
     """Compile the library, its Python binding and the benchmark's probe
-    library (always recompiles); returns the library path."""
+    library (always recompiles); returns the library path. The C libraries need
+    hipcc alone: where what the binding needs is not there, it is left out (and an
+    older one taken away), and the attention side's Python names raise when called."""
+    lacks = _binding_lacks()
+    if lacks:
+        _compile(sources(), LIB, verbose)
+        _compile([PROBE_SRC], PROBE_LIB, verbose)
+        if os.path.exists(BINDING_LIB):
+            os.remove(BINDING_LIB)
+        print("bit_quantized_mat_amd: built without the Python binding of the attention side "
+              "(%s not found)" % lacks, file=sys.stderr)
+        return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
     obj = os.path.join(OBJ_DIR, "attention_binding.%d.o" % os.getpid())
     try:

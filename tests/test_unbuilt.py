@@ -45,3 +45,52 @@ def test_names_come_with_the_library():
     from bit_quantized_mat_amd import attention
     for n in m._ATTENTION:
         assert getattr(m, n) is getattr(attention, n)
+
+
+@pytest.fixture
+def bare_build(monkeypatch, tmp_path):
+    """The build module with its compilations replaced and its own output folder."""
+    from bit_quantized_mat_amd import build as b
+    made = []
+    monkeypatch.setattr(b, "_compile", lambda srcs, out, verbose: made.append(out))
+    monkeypatch.setattr(b, "OBJ_DIR", str(tmp_path))
+    monkeypatch.setattr(b, "BINDING_LIB", str(tmp_path / "_attention.so"))
+    b.made = made
+    return b
+
+
+def test_build_without_a_host_compiler(bare_build, monkeypatch, capfd):
+    # the C library needs hipcc alone; its Python binding is left out, loudly, and
+    # one of an earlier build does not stay behind
+    open(bare_build.BINDING_LIB, "w").close()
+    monkeypatch.setattr(bare_build, "CXX", "no-such-compiler")
+    assert bare_build.build() == bare_build.LIB
+    assert bare_build.LIB in bare_build.made and bare_build.PROBE_LIB in bare_build.made
+    assert not os.path.exists(bare_build.BINDING_LIB)
+    assert "no-such-compiler" in capfd.readouterr().err
+
+
+def test_build_without_torch(bare_build, monkeypatch, capfd):
+    monkeypatch.setitem(sys.modules, "torch", None)
+    assert bare_build.build() == bare_build.LIB
+    assert bare_build.LIB in bare_build.made
+    assert "torch" in capfd.readouterr().err
+
+
+def test_build_without_pythons_headers(bare_build, monkeypatch, capfd, tmp_path):
+    import sysconfig
+    paths = dict(sysconfig.get_paths(), include=str(tmp_path))
+    monkeypatch.setattr(sysconfig, "get_paths", lambda: paths)
+    assert bare_build.build() == bare_build.LIB
+    assert "Python.h" in capfd.readouterr().err
+
+
+def test_a_binding_that_does_not_compile_is_an_error(bare_build, monkeypatch, tmp_path):
+    bad = tmp_path / "bad.cpp"
+    bad.write_text("#error no\n")
+    monkeypatch.setattr(bare_build, "BINDING_SRC", str(bad))
+    if shutil.which(bare_build.CXX) is None:
+        pytest.skip("no host compiler")
+    with pytest.raises(subprocess.CalledProcessError):
+        bare_build.build()
+    assert bare_build.LIB in bare_build.made
