@@ -335,7 +335,7 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
         if (!find_tile<S::M>(a, a.tiles - 1 - x % a.tiles, t))
             return;
     }
-    const int parts = parts_of(a, t);
+    const int parts = kHalves ? 1 : parts_of(a, t);  // tiles of 256 rows are not cut
     if (split >= parts)
         return;
     // part 0 is what whole chunks leave over; it goes last, and fills the gaps that
@@ -1042,7 +1042,7 @@ Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads, int wi
     const int64_t wanted = wanted_tiles(c->head_dim, of_one, few);
     const int64_t parts = std::max<int64_t>(1, (wanted + (few ? 0 : most_tiles / 2)) / most_tiles);
     int64_t chunk = (room + parts - 1) / parts;
-    if (room - chunk <= (few ? kLeastSavedFew : c->head_dim <= 64 ? kLeastSavedOf64 : kLeastSaved))
+    if (m == 256 || room - chunk <= (few ? kLeastSavedFew : c->head_dim <= 64 ? kLeastSavedOf64 : kLeastSaved))
         chunk = room;
     chunk = std::max<int64_t>(kLeastChunk, chunk);
     // Many sequences of few rows: cut the long among the short ones too (64 of 33 to
@@ -1071,12 +1071,14 @@ int launch_shape(const AttnArgs &a, hipStream_t stream)
         return BQM_ERR_SHAPE;
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(S::kThreads), S::kLds, stream, a);
     const int64_t rows = a.total_q * a.n_q_heads;
-    if (a.n_splits > kFewParts)
-        hipLaunchKernelGGL((attention_join_kernel<O, S::M, 4>), dim3((unsigned)rows), dim3(256), 0,
-                           stream, a);
-    else if (a.n_splits > 1)
-        hipLaunchKernelGGL((attention_join_kernel<O, S::M, 1>), dim3((unsigned)((rows + 3) / 4)),
-                           dim3(256), 0, stream, a);
+    if constexpr (S::M < 256) {
+        if (a.n_splits > kFewParts)
+            hipLaunchKernelGGL((attention_join_kernel<O, S::M, 4>), dim3((unsigned)rows), dim3(256),
+                               0, stream, a);
+        else if (a.n_splits > 1)
+            hipLaunchKernelGGL((attention_join_kernel<O, S::M, 1>), dim3((unsigned)((rows + 3) / 4)),
+                               dim3(256), 0, stream, a);
+    }
     return check_launch();
 }
 
