@@ -64,12 +64,21 @@ class Decoder:
                                  torch.zeros(max_seqs, dtype=torch.int32, device="cuda"),
                                  torch.zeros(pages, dtype=torch.int32, device="cuda"))
 
+    def _take(self, pages, short_of):
+        """The new state, if every sequence got its pages: one that did not keeps its old
+        length, and new tokens would be stored over its last ones. (A server counts the
+        free pages on the host; here the answer is waited for.)"""
+        self.short_of = short_of
+        if int(short_of):
+            raise RuntimeError("no free pages for %d sequences" % int(short_of))
+        self.pages = pages
+
     def step(self, x, new):
         """x fp32 [tokens, dim]: new[s] tokens of each sequence s, in order. Their
         states after all layers, attended over everything before them."""
         n_new = torch.tensor(new, dtype=torch.int32)
         starts = torch.cat((torch.zeros(1, dtype=torch.int32), n_new.cumsum(0, dtype=torch.int32)))
-        self.pages, self.short_of = bqm.kv_extend(self.pages, n_new.cuda(), self.page_size)
+        self._take(*bqm.kv_extend(self.pages, n_new.cuda(), self.page_size))
         batch = bqm.KvBatch(self.pages.table, self.pages.lens, starts.cuda(), max_q=max(new))
         T, H, G = x.shape[0], self.heads, self.kv_heads
         for layer, cache in zip(self.layers, self.caches):
@@ -88,7 +97,8 @@ class Decoder:
     def fork(self, parents, children):
         """Sequences children (empty ones) go on from where parents are."""
         p, c = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in (parents, children))
-        self.pages, moves, self.short_of = bqm.kv_fork(self.pages, p, c, self.page_size)
+        pages, moves, short_of = bqm.kv_fork(self.pages, p, c, self.page_size)
+        self._take(pages, short_of)
         bqm.kv_copy_pages(self.cache, moves)
 
     def end(self, seqs):
