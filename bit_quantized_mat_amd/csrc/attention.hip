@@ -541,12 +541,12 @@ __global__ __launch_bounds__(64 * WM *WK, WAVES) void attention_kernel(AttnArgs 
     // go the exponentials and the operand reads of the next 16, in this order.
     auto weigh_and_multiply = [&](const Scores &s, float base, const char *v) BQM_INLINE {
         constexpr int kShare = 8 / kTiles;
-        // With few rows, where memory bounds the kernel and the matrix units are 7%
-        // busy, what a weight's rounding leaves over is multiplied too: weights of twice
-        // the bits (64 sequences of 300 tokens 20.8 -> 21.3 us, 2 of about 120000 171.3 ->
-        // 171.5). With many rows the products are what the kernel does, and that would be
-        // three for every two.
-        constexpr bool kRest = WM == 1;
+        // For an output of 32 bits what a weight's rounding leaves over is multiplied too,
+        // where rows are few and memory bounds the kernel: weights of twice the bits
+        // (61 ragged sequences of up to 8192 tokens 104.9 -> 105.7 us, 24 of up to 1126
+        // 20.2 -> 21.1). An output of 16 bits rounds as much away itself; and with many
+        // rows the products are what the kernel does, and it would do three for two.
+        constexpr bool kRest = WM == 1 && sizeof(O) == 4;
         f32x8 e;
         Op f[2][kTiles];
 #pragma unroll

@@ -469,8 +469,9 @@ BQM_API int rope_kv_append(const void *q, const void *k, const void *v, int64_t 
  * tokens) does not reach it, NaN and infinities included.
  * q . k and all sums are fp32; e_j is rounded to the cache's type before it
  * meets v_j (in float16 to within 2^-32 of the row's largest, or 2^-12 of itself).
- * Calls of few rows (max_q * n_q_heads / n_heads at most 32) multiply what that
- * rounding leaves over as well: weights of twice the type's bits.
+ * Calls of few rows (max_q * n_q_heads / n_heads at most 32) with an output of
+ * BQM_DTYPE_F32 multiply what that rounding leaves over as well: weights of twice
+ * the type's bits.
  *   q [total_q][n_q_heads][head_dim] of the cache's type, strides in elements
  *   (multiples of 8), values contiguous; out [total_q][n_q_heads][head_dim] of
  *   out_dtype (the cache's type or BQM_DTYPE_F32), contiguous.
