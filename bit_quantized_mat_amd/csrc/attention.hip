@@ -17,12 +17,14 @@
 // which a transposing LDS read delivers V.
 //
 // What bounds it, measured on one MI355X (bf16, heads of 128, 32 over 8):
-//   one token a sequence: memory. 64 sequences of 4096 tokens 203 us (5.3 TB/s; a
-//     large copy reaches 5.0), of 16384 771 us (5.6 TB/s); 64 of 33 to 8192 tokens
-//     104 us (4.2 TB/s), 2 of about 120000 176 us (5.4 TB/s).
-//   a prompt of 8192: issue and the workgroups' ends. 553 us, 995 TFLOP/s where a
-//     large matrix product of the library reaches 1380; matrix units 43% busy, the
+//   one token a sequence: memory. 64 sequences of 4096 tokens 202 us (5.3 TB/s; a
+//     large copy reaches 5.0), of 16384 784 us (5.5 TB/s); 64 of 33 to 8192 tokens
+//     105 us (4.2 TB/s), 2 of about 120000 177 us (5.4 TB/s).
+//   a prompt of 8192: issue and the workgroups' ends. 559 us, 985 TFLOP/s where a
+//     large matrix product of the library reaches 1380; matrix units 44% busy, the
 //     vector unit's softmax beside them, 61 us of start and end of 1024 workgroups.
+//   chunks of 17 sequences, heads of 64, a window of 1024: 40 us; uneven shares (572
+//     workgroups, three a compute unit) and waits, matrix units 15% busy.
 //   one token over 37: latency, 8 us of which an empty launch is 4.
 #include <algorithm>
 
@@ -983,21 +985,21 @@ constexpr int64_t kMostWorkgroups = 8192;    // most of them empty, where length
 constexpr int kLeastChunk = 256, kRaggedChunk = 1024;
 
 // Workgroups, parts counted, that a launch is cut into.
-// Of 32 rows: no more than run at once, two a compute unit, since what does not takes
+// Tiles of 32 rows: no more than run at once, two a compute unit, since what does not takes
 // another round (24 tokens over 1126, heads of 128, 192 tiles: 33 us in two parts, 40
 // in three; 12 over 3000: 41 us in five, 45 in nine), and one part where several would
 // spare no more than kLeastSavedFew tokens (64 over 300: 22 us in one, 33 in two).
-// Of 128 rows: the nearest number of parts is taken, and one where several would spare
+// Tiles of 128 rows: the nearest number of parts is taken, and one where several would spare
 // a workgroup no more than kLeastSaved tokens: their shares' way costs as much (28 heads
 // of 64 over 4, 17 x 72 tokens with a window of 1024: 49 us in two parts, 32 in one;
 // a prompt of 1024, heads of 128: 41 and 33). Heads of 64 run three workgroups a
 // compute unit (17 x 36 tokens over 4096: 70 us in one part, 55 in three; 17 x 108,
-// 408 tiles: 94 in one, 130 in two). Of 128, two; where a sequence's tiles are one or
-// two, its keys and values are hardly read again, memory bounds them and more parts
-// only add to that (8 x 64 tokens over 4096: 76 us in three parts, 88 in four; 32 x 32
-// over 4096: 153 in one, 186 in two), but not where many share them (512 tokens over
-// 8192: 98 us in four parts, 113 in three). Of 256, one, in rounds (4 x 128 tokens over
-// 4096: 103 us in seven parts, 110 in six, 127 in eight).
+// 408 tiles: 94 in one, 130 in two). Heads of 128 run two; where a sequence's tiles are
+// one or two, its keys and values are hardly read again, memory bounds them and more
+// parts only add to that (8 x 64 tokens over 4096: 76 us in three parts, 88 in four;
+// 32 x 32 over 4096: 153 in one, 186 in two), but not where many share them (512 tokens
+// over 8192: 98 us in four parts, 113 in three). Heads of 256 run one, in rounds (4 x 128
+// tokens over 4096: 103 us in seven parts, 110 in six, 127 in eight).
 int64_t wanted_tiles(int head_dim, int64_t of_one, bool few)
 {
     if (few)
@@ -1042,7 +1044,8 @@ Plan plan_of(const bqm_kv_cache *c, const bqm_kv_batch *b, int n_q_heads, int wi
     const int64_t wanted = wanted_tiles(c->head_dim, of_one, few);
     const int64_t parts = std::max<int64_t>(1, (wanted + (few ? 0 : most_tiles / 2)) / most_tiles);
     int64_t chunk = (room + parts - 1) / parts;
-    if (m == 256 || room - chunk <= (few ? kLeastSavedFew : c->head_dim <= 64 ? kLeastSavedOf64 : kLeastSaved))
+    const int64_t least = few ? kLeastSavedFew : c->head_dim <= 64 ? kLeastSavedOf64 : kLeastSaved;
+    if (m == 256 || room - chunk <= least)
         chunk = room;
     chunk = std::max<int64_t>(kLeastChunk, chunk);
     // Many sequences of few rows: cut the long among the short ones too (64 of 33 to
