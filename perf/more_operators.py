@@ -205,13 +205,14 @@ def _plain_sample(s):
     if s["min_p"] is not None:
         keep &= (ws >= s["min_p"].double().unsqueeze(1)) | (place == 0)
     keep &= (heat > 0) | (place == 0)
-    w = torch.zeros_like(w).scatter_(1, order, ws * keep)
-    c = torch.cumsum(w, -1)
+    ws = ws * keep
+    c = torch.cumsum(ws, -1)
     total = c[:, -1:]
-    hit = (c > s["u"].double().unsqueeze(1) * total) & (w > 0)
-    token = hit.to(torch.int8).argmax(-1, keepdim=True)
+    hit = (c > s["u"].double().unsqueeze(1) * total) & (ws > 0)
+    at = hit.to(torch.int8).argmax(-1, keepdim=True)  # the first of the sorted ones
+    token = order.gather(1, at)
     none = total == 0
-    logprob = torch.log(w.gather(1, token)) - torch.log(total)
+    logprob = torch.log(ws.gather(1, at)) - torch.log(total)
     return torch.where(none, -1, token).squeeze(1).to(torch.int32), torch.where(none, float("-inf"), logprob).squeeze(1).float()
 
 
@@ -289,17 +290,14 @@ def _exact_logprob(x, u, heat, k, p, floor):
         return float("-inf")
     if not heat > 0:
         return 0.0
-    val, at = torch.sort(x, descending=True, stable=True)
+    val = torch.sort(x, descending=True).values
     if k > 0:
-        val, at = val[:k], at[:k]
+        val = val[:k]
     w = torch.softmax(val / heat, 0)
     if p < 1.0:
-        n = int((torch.cumsum(w, 0) < p).sum()) + 1
-        val, at, w = val[:n], at[:n], w[:n]
-    at = at[w >= floor * w[0]]
+        w = w[:int((torch.cumsum(w, 0) < p).sum()) + 1]
     w = w[w >= floor * w[0]]
-    at, by = torch.sort(at)
-    w = w[by] / w.sum()
+    w = w / w.sum()
     i = int((torch.cumsum(w, 0) <= u).sum())
     return float(torch.log(w[min(i, len(w) - 1)]))
 
