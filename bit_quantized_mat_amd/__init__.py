@@ -1,6 +1,7 @@
-"""MI355X (gfx950) TQ1_0 (and TQ2_0) x Q8_1 quantized mat-vec, and the
-attention side of a decoder layer (``attention.py``: rotary positions, a paged
-cache, attention over it).
+"""MI355X (gfx950) TQ1_0 (and TQ2_0) x Q8_1 quantized mat-vec, the attention
+side of a decoder layer (``attention.py``: rotary positions, a paged cache,
+attention over it) and its token side (``tokens.py``: the norm, 4-bit matrices,
+sampling).
 
 A thin binding over the C ABI in ``include/bqm.h`` (library ``libbqm.so``,
 built in-tree by ``bit_quantized_mat_amd.build``). Every function here only
@@ -23,6 +24,8 @@ __all__ = [
     "KvCache", "KvBatch", "KvPages", "rope_inv_freq", "rope_table", "rope", "rope_kv_append",
     "paged_attention", "paged_attention_workspace_bytes", "kv_extend", "kv_fork", "kv_free",
     "kv_compact", "kv_copy_pages",
+    "Q4Matrix", "q4_quantize", "q4_dequantize", "mm_q4", "rms_norm", "rms_norm_q8_1", "sample",
+    "sample_workspace_bytes",
     "TQ1_BLOCK_BYTES", "TQ2_BLOCK_BYTES", "Q81_BLOCK_BYTES", "MMVQ_MAX_COLS",
 ]
 
@@ -92,7 +95,8 @@ def library():
                      "mmvq_id_tq1_0_noalloc", "tq1_dequantize", "tq2_pack", "mmvq_tq2_0",
                      "mmvq_tq2_0_block_isums", "rope_table", "rope", "rope_kv_append",
                      "paged_attention", "kv_extend", "kv_fork", "kv_free", "kv_compact",
-                     "kv_copy_pages"):
+                     "kv_copy_pages", "rms_norm", "q4_quantize", "mm_q4", "q4_dequantize",
+                     "sample"):
             getattr(L, name).restype = ctypes.c_int
         f, d = ctypes.c_float, ctypes.c_double
         L.rope_table.argtypes = [_p, _p, _i64, _i32, d, _p]
@@ -109,6 +113,13 @@ def library():
         L.kv_compact.argtypes = [_p, _p, _i32, _p, _p, _p]
         L.kv_copy_pages.argtypes = [_p, _p, _i64, _p]
         L.kv_pages_workspace_bytes.argtypes = [_p]
+        L.rms_norm.argtypes = [_p, _p, _p, _p, _p, _p, _i64, _i64, d, _i32, _i32, _i32, _p]
+        L.q4_quantize.argtypes = [_p, _p, _i32, _p]
+        L.mm_q4.argtypes = [_p, _p, _p, _i64, _p]
+        L.q4_dequantize.argtypes = [_p, _p, _p, _i64, f, _i32, _p]
+        L.sample.argtypes = [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i32, _p, _sz, _p]
+        L.sample_workspace_bytes.argtypes = [_i64, _i64]
+        L.sample_workspace_bytes.restype = _sz
         L.paged_attention_workspace_bytes.restype = _sz
         L.kv_pages_workspace_bytes.restype = _sz
         _lib = L
@@ -408,28 +419,37 @@ def mmvq_id_tq1_0_noalloc(w, a, ids, E, N, K, T, n_used, out=None, stream=None):
     return out
 
 
-# the attention side imports torch, so it is loaded by the first use of a name
+# the attention and token sides import torch, so they are loaded by the first use of a name
 _ATTENTION = frozenset((
     "KvCache", "KvBatch", "KvPages", "rope_inv_freq", "rope_table", "rope", "rope_kv_append",
     "paged_attention", "paged_attention_workspace_bytes", "kv_extend", "kv_fork", "kv_free",
     "kv_compact", "kv_copy_pages"))
+_TOKENS = frozenset(("Q4Matrix", "q4_quantize", "q4_dequantize", "mm_q4", "rms_norm",
+                     "rms_norm_q8_1", "sample", "sample_workspace_bytes"))
+
+
+def _side(name):
+    if name in _TOKENS:
+        from . import tokens
+        return tokens
+    from . import attention
+    return attention
 
 
 def _later(name):
     """In the place of a name whose library is not there: its calls load it or raise."""
     def call(*args, **kwargs):
-        from . import attention
-        return getattr(attention, name)(*args, **kwargs)
+        return getattr(_side(name), name)(*args, **kwargs)
     call.__name__ = call.__qualname__ = name
     return call
 
 
 def __getattr__(name):
-    if name not in _ATTENTION:
+    if name not in _ATTENTION and name not in _TOKENS:
         raise AttributeError("module %r has no attribute %r" % (__name__, name))
     try:
-        from . import attention
+        side = _side(name)
     except (ImportError, OSError, RuntimeError):
         return _later(name)  # what is missing is said when it is called
-    value = globals()[name] = getattr(attention, name)
+    value = globals()[name] = getattr(side, name)
     return value

@@ -1,7 +1,8 @@
 """Build step for the HIP library: compiles every ``csrc/*.hip`` source for
 gfx950 into ``bit_quantized_mat_amd/libbqm.so`` (in-tree, so the built
-library travels with the source tree), and the Python binding of its attention
-side, ``binding/attention.cpp``, into ``_attention.so`` beside it."""
+library travels with the source tree), and the Python bindings of its attention
+and token sides, ``binding/attention.cpp`` and ``binding/tokens.cpp``, into
+``_attention.so`` and ``_tokens.so`` beside it."""
 import concurrent.futures
 import glob
 import os
@@ -31,6 +32,7 @@ FLAGS = [
 
 BINDING_SRC = os.path.join(HERE, "binding", "attention.cpp")
 BINDING_LIB = os.path.join(HERE, "_attention.so")
+TOKENS_SRC = os.path.join(HERE, "binding", "tokens.cpp")
 CXX = os.environ.get("CXX", "g++")
 
 
@@ -90,51 +92,63 @@ def _binding_lacks():
     return None
 
 
-def _compile_binding(obj, verbose):
-    """The binding's object: host code against torch's headers."""
+def _bindings():
+    """(source, library) of each binding."""
+    return [(BINDING_SRC, BINDING_LIB),
+            (TOKENS_SRC, os.path.join(os.path.dirname(BINDING_LIB), "_tokens.so"))]
+
+
+def _compile_binding(src, obj, verbose):
+    """A binding's object: host code against torch's headers."""
     import torch
     inc = _binding_includes()
     _run([CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
-          *[a for i in inc for a in ("-isystem", i)], "-c", BINDING_SRC, "-o", obj], verbose)
+          *[a for i in inc for a in ("-isystem", i)], "-c", src, "-o", obj], verbose)
 
 
-def _link_binding(obj, verbose):
+def _link_binding(obj, out, verbose):
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = BINDING_LIB + ".tmp%d" % os.getpid()
+    tmp = out + ".tmp%d" % os.getpid()
     _run([CXX, "-shared", obj, "-o", tmp, "-L" + HERE, "-l:" + os.path.basename(LIB), "-L" + lib,
           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib],
          verbose)
-    os.replace(tmp, BINDING_LIB)
+    os.replace(tmp, out)
 
 
 def build(verbose: bool = False) -> str:
-    """Compile the library, its Python binding and the benchmark's probe
+    """Compile the library, its Python bindings and the benchmark's probe
     library (always recompiles); returns the library path. The C libraries need
-    hipcc alone: where what the binding needs is not there, it is left out (and an
-    older one taken away), and the attention side's Python names raise when called."""
+    hipcc alone: where what the bindings need is not there, they are left out (and
+    older ones taken away), and the Python names of the attention and token sides
+    raise when called."""
     lacks = _binding_lacks()
     if lacks:
         _compile(sources(), LIB, verbose)
         _compile([PROBE_SRC], PROBE_LIB, verbose)
-        if os.path.exists(BINDING_LIB):
-            os.remove(BINDING_LIB)
-        print("bit_quantized_mat_amd: built without the Python binding of the attention side "
-              "(%s not found)" % lacks, file=sys.stderr)
+        for _, lib in _bindings():
+            if os.path.exists(lib):
+                os.remove(lib)
+        print("bit_quantized_mat_amd: built without the Python bindings of the attention and token "
+              "sides (%s not found)" % lacks, file=sys.stderr)
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
-    obj = os.path.join(OBJ_DIR, "attention_binding.%d.o" % os.getpid())
+    made = [(src, os.path.join(OBJ_DIR, os.path.basename(src) + ".%d.o" % os.getpid()), lib)
+            for src, lib in _bindings()]
     try:
-        with concurrent.futures.ThreadPoolExecutor(1) as ex:
-            binding = ex.submit(_compile_binding, obj, verbose)
+        with concurrent.futures.ThreadPoolExecutor(len(made)) as ex:
+            bindings = [ex.submit(_compile_binding, src, obj, verbose) for src, obj, _ in made]
             _compile(sources(), LIB, verbose)
             _compile([PROBE_SRC], PROBE_LIB, verbose)
-            binding.result()
-        _link_binding(obj, verbose)
+            for b in bindings:
+                b.result()
+        for _, obj, lib in made:
+            _link_binding(obj, lib, verbose)
     finally:
-        if os.path.exists(obj):
-            os.remove(obj)
+        for _, obj, _ in made:
+            if os.path.exists(obj):
+                os.remove(obj)
     return LIB
 
 

@@ -10,7 +10,7 @@
 
 namespace {
 
-constexpr int kVersion = 200;  // 0.2.0
+constexpr int kVersion = 300;  // 0.3.0
 constexpr uint64_t kMaxBufferBytes = 0xfffffffcull;  // 32-bit byte offsets inside one matrix
 
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
@@ -646,6 +646,129 @@ int kv_copy_pages(const bqm_kv_cache *cache, const int32_t *moves, int64_t n, vo
     if (int rc = check_device())
         return rc;
     return n == 0 ? BQM_OK : bqm::launch_kv_copy_pages(cache, moves, n, as_stream(stream));
+}
+
+int rms_norm(const void *x, const void *add, const float *gain, void *sum, void *y, void *a,
+             int64_t T, int64_t K, double eps, int32_t dtype, int32_t add_dtype, int32_t y_dtype,
+             void *stream)
+{
+    if (!x || (!y && !a) || (add && !sum))
+        return BQM_ERR_NULL;
+    if (T < 0 || T > (1 << 23) || K < 32 || K > 65536 || K % 32 != 0 || !(eps >= 0.0) ||
+        !(eps <= 1.7976931348623157e308) || !is_dtype(dtype) || (add && !is_dtype(add_dtype)) ||
+        (y && !is_dtype(y_dtype)))
+        return BQM_ERR_SHAPE;
+    // in place every value is read and written by one thread: same places only
+    if (add && sum == add && add_dtype != dtype)
+        return BQM_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(add, 16) || !aligned(gain, 16) || !aligned(sum, 16) ||
+        !aligned(y, 16) || !aligned4(a))
+        return BQM_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    if (T == 0)
+        return BQM_OK;
+    return bqm::launch_rms_norm(x, add, gain, sum, y, a, T, (int)K, eps, dtype, add_dtype, y_dtype,
+                                as_stream(stream));
+}
+
+static int check_q4(const bqm_q4_matrix *m)
+{
+    if (!m || !m->codes || !m->scales)
+        return BQM_ERR_NULL;
+    if (m->group != 32 && m->group != 64 && m->group != 128)
+        return BQM_ERR_SHAPE;
+    if (m->N < 1 || m->N > 0x7fffffff || m->K < 1 || m->K > (1 << 20) || m->K % m->group != 0)
+        return BQM_ERR_SHAPE;
+    if (!aligned(m->codes, 16) || !aligned4(m->scales))
+        return BQM_ERR_ALIGN;
+    return BQM_OK;
+}
+
+int q4_quantize(const void *x, const bqm_q4_matrix *out, int32_t dtype, void *stream)
+{
+    if (!x)
+        return BQM_ERR_NULL;
+    if (int rc = check_q4(out))
+        return rc;
+    if (!is_dtype(dtype) || out->N * (out->K / 8) > (1ll << 38))
+        return BQM_ERR_SHAPE;
+    if (!aligned(x, 16))
+        return BQM_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return bqm::launch_q4_quantize(x, out, dtype, as_stream(stream));
+}
+
+int mm_q4(const bqm_q4_matrix *w, const void *a, float *y, int64_t T, void *stream)
+{
+    if (!a || !y)
+        return BQM_ERR_NULL;
+    if (int rc = check_q4(w))
+        return rc;
+    if (T < 1 || T > BQM_MM_MAX_COLS)
+        return BQM_ERR_SHAPE;
+    if (!aligned4(a) || !aligned4(y))
+        return BQM_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return bqm::launch_mm_q4(w, a, y, T, as_stream(stream));
+}
+
+int q4_dequantize(const bqm_q4_matrix *w, const int32_t *rows, void *out, int64_t n_rows,
+                  float factor, int32_t out_dtype, void *stream)
+{
+    if (!out)
+        return BQM_ERR_NULL;
+    if (int rc = check_q4(w))
+        return rc;
+    if (n_rows < 0 || n_rows > 0x7fffffff || (!rows && n_rows > w->N) || !is_dtype(out_dtype))
+        return BQM_ERR_SHAPE;
+    if (!aligned4(rows) || !aligned(out, 16))
+        return BQM_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return n_rows == 0 ? BQM_OK
+                       : bqm::launch_q4_dequantize(w, rows, out, n_rows, factor, out_dtype,
+                                                   as_stream(stream));
+}
+
+static bool sample_sizes_ok(int64_t T, int64_t V)
+{
+    return T >= 0 && T <= 65535 && V >= 1 && V < (1 << 20);
+}
+
+size_t sample_workspace_bytes(int64_t T, int64_t V)
+{
+    return sample_sizes_ok(T, V) ? bqm::sample_workspace(T, V) : 0;
+}
+
+int sample(const void *logits, int64_t row_stride, const float *temperature, const int32_t *top_k,
+           const float *top_p, const float *min_p, const float *u, int32_t *tokens,
+           float *logprobs, int64_t T, int64_t V, int32_t dtype, void *workspace,
+           size_t workspace_bytes, void *stream)
+{
+    if (!logits || !u || !tokens)
+        return BQM_ERR_NULL;
+    if (!sample_sizes_ok(T, V) || !is_dtype(dtype) || (T > 1 && row_stride < V) ||
+        row_stride > (1ll << 38))
+        return BQM_ERR_SHAPE;
+    if (!aligned(logits, bytes_of(dtype)) || !aligned4(temperature) || !aligned4(top_k) ||
+        !aligned4(top_p) || !aligned4(min_p) || !aligned4(u) || !aligned4(tokens) ||
+        !aligned4(logprobs))
+        return BQM_ERR_ALIGN;
+    if (const size_t need = bqm::sample_workspace(T, V)) {
+        if (!workspace || workspace_bytes < need)
+            return BQM_ERR_WORKSPACE;
+        if (!aligned(workspace, 256))
+            return BQM_ERR_ALIGN;
+    }
+    if (int rc = check_device())
+        return rc;
+    if (T == 0)
+        return BQM_OK;
+    return bqm::launch_sample(logits, row_stride, temperature, top_k, top_p, min_p, u, tokens,
+                              logprobs, T, V, dtype, workspace, as_stream(stream));
 }
 
 const char *bqm_status_string(int status)

@@ -182,4 +182,18 @@ int launch_paged_attention(const void *q, int64_t q_token, int64_t q_head, const
                            bool causal, int window, int out_dtype, void *workspace,
                            hipStream_t stream);
 
+// The token side (arguments as the entry points', already checked).
+int launch_rms_norm(const void *x, const void *add, const float *gain, void *sum, void *y, void *a,
+                    int64_t T, int K, double eps, int dtype, int add_dtype, int y_dtype,
+                    hipStream_t stream);
+int launch_q4_quantize(const void *x, const bqm_q4_matrix *m, int dtype, hipStream_t stream);
+int launch_mm_q4(const bqm_q4_matrix *m, const void *a, float *y, int64_t T, hipStream_t stream);
+int launch_q4_dequantize(const bqm_q4_matrix *m, const int32_t *rows, void *out, int64_t n_rows,
+                         float factor, int out_dtype, hipStream_t stream);
+size_t sample_workspace(int64_t T, int64_t V);
+int launch_sample(const void *logits, int64_t row_stride, const float *temperature,
+                  const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                  int32_t *tokens, float *logprobs, int64_t T, int64_t V, int dtype,
+                  void *workspace, hipStream_t stream);
+
 }  // namespace bqm

@@ -60,6 +60,44 @@ __device__ __forceinline__ Q81Part q8_1_block_by_2(const float (&x)[16])
     return r;
 }
 
+// The same block by four neighbouring lanes (an aligned quad), lane h holding
+// elements 8h..8h+7: the same bytes. Every lane of the wave must call this.
+struct Q81Quarter {
+    uint32_t q4[2];  // element 8h + 4k + i in byte i of q4[k]
+    uint32_t field;  // the block's d/s field
+};
+
+__device__ __forceinline__ Q81Quarter q8_1_block_by_4(const float (&x)[8])
+{
+    constexpr int kDppQuadXor2 = 0x4e;  // quad_perm [2, 3, 0, 1]
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        m = fmaxf(m, fabsf(x[i]));
+    m = fmaxf(m, __int_as_float(dpp_swap_pair(__float_as_int(m))));
+    m = fmaxf(m, dpp_move<kDppQuadXor2>(m));
+    const float d = m / 127.0f;
+    const float id = d != 0.0f ? 1.0f / d : 0.0f;
+    Q81Quarter r;
+    int sum = 0;
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        uint32_t q4 = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            int q = (int)roundf(x[4 * k + i] * id);
+            q = q > 127 ? 127 : (q < -127 ? -127 : q);
+            sum += q;
+            q4 |= (uint32_t)(q & 0xff) << (8 * i);
+        }
+        r.q4[k] = q4;
+    }
+    sum += dpp_swap_pair(sum);
+    sum += __builtin_amdgcn_mov_dpp(sum, kDppQuadXor2, 0xf, 0xf, true);
+    r.field = f32_to_f16_bits(d) | (f32_to_f16_bits(d * (float)sum) << 16);
+    return r;
+}
+
 // The block's 32-bit d/s field: fp16(d) in the low half, fp16(d * sum) in the high.
 __device__ __forceinline__ uint32_t q8_1_scale_field(const Q81Part &p)
 {

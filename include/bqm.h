@@ -1,6 +1,6 @@
 /*
  * bqm.h -- C ABI of the MI355X (gfx950) TQ1_0 x Q8_1 quantized mat-vec library,
- * with the attention side of a decoder layer (at the end).
+ * with the attention side of a decoder layer and its token side (at the end).
  *
  * The operation: ternary weights stored in the TQ1_0 block format (five
  * base-3 trits per byte, 256-element blocks) multiplied against activations
@@ -539,6 +539,101 @@ BQM_API int kv_copy_pages(const bqm_kv_cache *cache, const int32_t *moves, int64
 
 /* Workspace of kv_extend and kv_fork for tables of these sizes. */
 BQM_API size_t kv_pages_workspace_bytes(const bqm_kv_pages *pages);
+
+/* ---- The token side of a decoder -------------------------------------------
+ * What stands between a token and its logits beside the ternary products and
+ * attention: rows of a table, the norm in front of every product, matrices kept
+ * in 4 bits (the table and the output matrix of a model whose layers are
+ * ternary), and the choice of the next token. None of it is on the pages cited
+ * above; the definitions below are the whole of it. */
+
+/* Root-mean-square norm of each token's values, with the residual's addition:
+ *   s = x + add,  y = s * r * gain,  r = 1 / sqrt(mean of s^2 + eps).
+ * s is rounded to the stream's type (dtype) first, and the norm is that of the
+ * rounded values; the mean is formed in fp64, r is rounded to fp32, and y is
+ * fp32(fp32(s * r) * gain), so that results do not depend on how a row is split.
+ *   x [T][K] of dtype; add [T][K] of add_dtype or NULL (nothing is added); gain
+ *   [K] fp32 or NULL (ones); sum [T][K] of dtype, where s goes (may be x itself,
+ *   or add if of the same type; may be NULL without add); y [T][K] of y_dtype or
+ *   NULL; a [T][K/32] Q8_1 blocks of y's fp32 values (bitwise q8_1_quantize of
+ *   them) or NULL. One of y and a is given, or both.
+ * Shapes: 0 <= T <= 2^23 (0: nothing is done), K a multiple of 32, 32 .. 65536,
+ * eps >= 0 and finite. Alignment: 16 bytes, a 4 bytes. */
+BQM_API int rms_norm(const void *x, const void *add, const float *gain, void *sum, void *y,
+                     void *a, int64_t T, int64_t K, double eps, int32_t dtype,
+                     int32_t add_dtype, int32_t y_dtype, void *stream);
+
+/* A matrix [N][K] kept in 4 bits (host struct; read during the call only). The
+ * value at (n, k) is scales[n][k / group] * (code - zeros[n][k / group]), codes
+ * -8 .. 7 as two's complement. A row of codes is K / 2 bytes, 16 for each run of
+ * 32 values: byte i of them holds the code of value i in its low half and that of
+ * value i + 16 in its high half. */
+typedef struct bqm_q4_matrix {
+    const void *codes;       /* [N][K / 2], 16-byte aligned                     */
+    const void *scales;      /* [N][K / group] fp16, 4-byte aligned             */
+    const int8_t *zeros;     /* [N][K / group], or NULL for zeros of 0          */
+    int64_t N;               /* 1 .. 2^31 - 1                                   */
+    int64_t K;               /* a multiple of group, at most 2^20               */
+    int32_t group;           /* 32, 64 or 128                                   */
+} bqm_q4_matrix;
+
+/* Makes such a matrix of x [N][K] (dtype BQM_DTYPE_*, 16-byte aligned, rows
+ * contiguous). Without zeros: scale = fp16(max |x| / 7), code = x / scale. With
+ * them: scale = fp16((hi - lo) / 15), hi and lo the largest and smallest value and
+ * 0, zero = -8 - lo / scale, code = x / scale + zero. Quotients are fp32, rounded to
+ * the nearest whole number (halves to even), codes and zeros clamped to -8 .. 7,
+ * scales to 65504; a scale of 0 gives zeros and codes of 0. codes, scales and zeros
+ * of `out` are written. */
+BQM_API int q4_quantize(const void *x, const bqm_q4_matrix *out, int32_t dtype, void *stream);
+
+/* Product of a 4-bit matrix and T activation columns:
+ *   y[t][n] = sum_j scale * fp32(d_a[t][j]) * isum[t][n][j],
+ *   isum[t][n][j] = sum_{i < 32} (code - zero) * q[t][32j + i]   (exact)
+ *   a [T][K/32] Q8_1 blocks; y [T][N] fp32.
+ * fp32 results differ from the exact sum by at most 1e-5 of sum_j |scale * d_a|
+ * sum_i |code - zero| |q| (for zeros within -8 .. 7). Shapes: 1 <= T <=
+ * BQM_MM_MAX_COLS. Alignment: a and y 4 bytes. */
+BQM_API int mm_q4(const bqm_q4_matrix *w, const void *a, float *y, int64_t T, void *stream);
+
+/* Rows of a 4-bit matrix (a table's look-up):
+ *   out[i][k] = fp32(fp32(value of (rows[i], k)) * factor), stored as out_dtype;
+ *   rows [n_rows] int32, or NULL for rows 0 .. n_rows - 1 (n_rows <= N then). Ids
+ *   outside [0, N) are not checked; they read the nearest row.
+ * Shapes: 0 <= n_rows <= 2^31 - 1 (0: nothing is done). Alignment: rows 4, out
+ * 16 bytes. */
+BQM_API int q4_dequantize(const bqm_q4_matrix *w, const int32_t *rows, void *out, int64_t n_rows,
+                          float factor, int32_t out_dtype, void *stream);
+
+/* The next token of each row of logits, for given random numbers. Of row t, with
+ * its tokens sorted by logits, largest first and equal ones by their ids:
+ *   weights w = exp((logit - largest) / temperature);
+ *   the first top_k tokens stay (<= 0: all);
+ *   of those, the shortest run of first ones whose weights come to top_p of
+ *   theirs (>= 1: all);
+ *   of those, the tokens of weight >= min_p (the largest weight is 1);
+ *   the first always stays; the token is the first of those left at which the
+ *   running sum of their weights exceeds u of the whole.
+ * temperature <= 0 (or NaN) takes the first token. NaN logits and those of
+ * -infinity are never taken; if there are others of +infinity, those alone have
+ * weight, 1 each. A row with nothing to take gives token -1. logprobs[t] is the
+ * logarithm of the token's share of the weights left (-infinity for token -1).
+ * Weights are formed in fp64 and summed as whole numbers of 2^-44, so results do
+ * not depend on an order of sums; weights below 2^-45 count as none.
+ *   logits [T][V] of dtype (BQM_DTYPE_*), rows row_stride elements apart;
+ *   temperature, top_p, min_p, u [T] fp32, top_k [T] int32; each but u may be NULL
+ *   (1; 1; 0; 0); u in [0, 1), clamped; tokens [T] int32; logprobs [T] fp32 or
+ *   NULL; workspace: at least sample_workspace_bytes(T, V) bytes, 256-byte aligned
+ *   (NULL if that is 0); nothing in it need be kept or cleared, and calls that
+ *   overlap on two streams need one each.
+ * Shapes: 0 <= T <= 65535 (0: nothing is done), 1 <= V < 2^20, row_stride >= V
+ * (any for T = 1). Alignment: to the elements. */
+BQM_API int sample(const void *logits, int64_t row_stride, const float *temperature,
+                   const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                   int32_t *tokens, float *logprobs, int64_t T, int64_t V, int32_t dtype,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace sample needs for these sizes (0 also for sizes it refuses). */
+BQM_API size_t sample_workspace_bytes(int64_t T, int64_t V);
 
 /* Human-readable text for a status code (static storage). */
 BQM_API const char *bqm_status_string(int status);
