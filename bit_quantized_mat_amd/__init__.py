@@ -24,8 +24,8 @@ __all__ = [
     "KvCache", "KvBatch", "KvPages", "rope_inv_freq", "rope_table", "rope", "rope_kv_append",
     "paged_attention", "paged_attention_workspace_bytes", "kv_extend", "kv_fork", "kv_free",
     "kv_compact", "kv_copy_pages",
-    "Q4Matrix", "q4_quantize", "q4_dequantize", "mm_q4", "rms_norm", "rms_norm_q8_1", "sample",
-    "sample_workspace_bytes",
+    "Q4Matrix", "q4_quantize", "q4_dequantize", "mm_q4", "mm_q4_workspace_bytes", "rms_norm",
+    "rms_norm_q8_1", "sample", "sample_workspace_bytes",
     "TQ1_BLOCK_BYTES", "TQ2_BLOCK_BYTES", "Q81_BLOCK_BYTES", "MMVQ_MAX_COLS",
 ]
 
@@ -115,7 +115,9 @@ def library():
         L.kv_pages_workspace_bytes.argtypes = [_p]
         L.rms_norm.argtypes = [_p, _p, _p, _p, _p, _p, _i64, _i64, d, _i32, _i32, _i32, _p]
         L.q4_quantize.argtypes = [_p, _p, _i32, _p]
-        L.mm_q4.argtypes = [_p, _p, _p, _i64, _p]
+        L.mm_q4.argtypes = [_p, _p, _p, _i64, _p, _sz, _p]
+        L.mm_q4_workspace_bytes.argtypes = [_p, _i64]
+        L.mm_q4_workspace_bytes.restype = _sz
         L.q4_dequantize.argtypes = [_p, _p, _p, _i64, f, _i32, _p]
         L.sample.argtypes = [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i32, _p, _sz, _p]
         L.sample_workspace_bytes.argtypes = [_i64, _i64]
@@ -424,8 +426,8 @@ _ATTENTION = frozenset((
     "KvCache", "KvBatch", "KvPages", "rope_inv_freq", "rope_table", "rope", "rope_kv_append",
     "paged_attention", "paged_attention_workspace_bytes", "kv_extend", "kv_fork", "kv_free",
     "kv_compact", "kv_copy_pages"))
-_TOKENS = frozenset(("Q4Matrix", "q4_quantize", "q4_dequantize", "mm_q4", "rms_norm",
-                     "rms_norm_q8_1", "sample", "sample_workspace_bytes"))
+_TOKENS = frozenset(("Q4Matrix", "q4_quantize", "q4_dequantize", "mm_q4", "mm_q4_workspace_bytes",
+                     "rms_norm", "rms_norm_q8_1", "sample", "sample_workspace_bytes"))
 
 
 def _side(name):

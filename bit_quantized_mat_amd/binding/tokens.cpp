@@ -156,7 +156,8 @@ Q4Matrix q4_quantize_(const Tensor &x, int64_t group, bool zeros, const py::obje
     return m;
 }
 
-Tensor mm_q4_(const Q4Matrix &m, const Tensor &a, const OptTensor &out_, const py::object &stream)
+Tensor mm_q4_(const Q4Matrix &m, const Tensor &a, const OptTensor &out_,
+              const OptTensor &workspace, const py::object &stream)
 {
     gpu(a, "a", 2, m.dev);
     typed(a, "a", at::kByte);
@@ -168,9 +169,11 @@ Tensor mm_q4_(const Q4Matrix &m, const Tensor &a, const OptTensor &out_, const p
         whole(out, "out", {T, m.m.N}, m.dev);
         typed(out, "out", at::kFloat);
     }
-    if (T)
-        done("mm_q4",
-             mm_q4(&m.m, a.data_ptr(), static_cast<float *>(out.data_ptr()), T, on.p));
+    if (T) {
+        const Scratch w(workspace, mm_q4_workspace_bytes(&m.m, T), a, on);
+        done("mm_q4", mm_q4(&m.m, a.data_ptr(), static_cast<float *>(out.data_ptr()), T, w.p,
+                            w.bytes, on.p));
+    }
     return out;
 }
 
@@ -256,7 +259,11 @@ PYBIND11_MODULE(_tokens, m)
           py::arg("zeros") = false, stream,
           "The Q4Matrix nearest to x [N, K] (float32, float16 or bfloat16), with zeros for groups that are "
           "not centred.");
-    m.def("mm_q4", &mm_q4_, py::arg("m"), py::arg("a"), out, stream,
+    m.def("mm_q4_workspace_bytes",
+          [](const Q4Matrix &q, int64_t T) { return mm_q4_workspace_bytes(&q.m, T); }, py::arg("m"),
+          py::arg("T"), "Bytes of the uint8 tensor that mm_q4(..., workspace=) takes (0: none).");
+    m.def("mm_q4", &mm_q4_, py::arg("m"), py::arg("a"), out, py::arg("workspace") = py::none(),
+          stream,
           "y fp32 [T, N] = a Q4Matrix times T Q8_1 activation columns a, uint8 [T, K / 32 * 36].");
     m.def("q4_dequantize", &q4_dequantize_, py::arg("m"), py::arg("rows") = py::none(),
           py::arg("scale") = 1.0, py::arg("dtype") = py::none(), out, stream,

@@ -672,13 +672,17 @@ int rms_norm(const void *x, const void *add, const float *gain, void *sum, void 
                                 as_stream(stream));
 }
 
+static bool q4_sizes_ok(const bqm_q4_matrix *m)
+{
+    return (m->group == 32 || m->group == 64 || m->group == 128) && m->N >= 1 &&
+           m->N <= 0x7fffffff && m->K >= 1 && m->K <= (1 << 20) && m->K % m->group == 0;
+}
+
 static int check_q4(const bqm_q4_matrix *m)
 {
     if (!m || !m->codes || !m->scales)
         return BQM_ERR_NULL;
-    if (m->group != 32 && m->group != 64 && m->group != 128)
-        return BQM_ERR_SHAPE;
-    if (m->N < 1 || m->N > 0x7fffffff || m->K < 1 || m->K > (1 << 20) || m->K % m->group != 0)
+    if (!q4_sizes_ok(m))
         return BQM_ERR_SHAPE;
     if (!aligned(m->codes, 16) || !aligned4(m->scales))
         return BQM_ERR_ALIGN;
@@ -700,7 +704,15 @@ int q4_quantize(const void *x, const bqm_q4_matrix *out, int32_t dtype, void *st
     return bqm::launch_q4_quantize(x, out, dtype, as_stream(stream));
 }
 
-int mm_q4(const bqm_q4_matrix *w, const void *a, float *y, int64_t T, void *stream)
+size_t mm_q4_workspace_bytes(const bqm_q4_matrix *w, int64_t T)
+{
+    if (!w || !q4_sizes_ok(w) || T < 1 || T > BQM_MM_MAX_COLS)
+        return 0;
+    return bqm::mm_q4_workspace(T, w->K);
+}
+
+int mm_q4(const bqm_q4_matrix *w, const void *a, float *y, int64_t T, void *workspace,
+          size_t workspace_bytes, void *stream)
 {
     if (!a || !y)
         return BQM_ERR_NULL;
@@ -710,9 +722,15 @@ int mm_q4(const bqm_q4_matrix *w, const void *a, float *y, int64_t T, void *stre
         return BQM_ERR_SHAPE;
     if (!aligned4(a) || !aligned4(y))
         return BQM_ERR_ALIGN;
+    if (const size_t need = bqm::mm_q4_workspace(T, w->K)) {
+        if (!workspace || workspace_bytes < need)
+            return BQM_ERR_WORKSPACE;
+        if (!aligned(workspace, 256))
+            return BQM_ERR_ALIGN;
+    }
     if (int rc = check_device())
         return rc;
-    return bqm::launch_mm_q4(w, a, y, T, as_stream(stream));
+    return bqm::launch_mm_q4(w, a, y, T, workspace, as_stream(stream));
 }
 
 int q4_dequantize(const bqm_q4_matrix *w, const int32_t *rows, void *out, int64_t n_rows,

@@ -133,17 +133,285 @@ int launch_dot(const Q4Args &g, hipStream_t stream)
     return check_launch();
 }
 
+// ---- many columns: the matrix cores ------------------------------------------------
+//
+// Codes less zeros (-15 .. 15) and q (-127 .. 127) are exact in fp16, and sums over a run
+// of 32 are exact in fp32, so a 32 x 32 tile of a run is two 32x32x16 products whose result
+// needs one fma by d_a, and one by the scale at the end of a group. Eight codes become
+// fp16 in ten instructions: a nibble under the exponent of 1024 is 1024 + nibble.
+//
+// The columns are laid out once a call, in the order in which lanes read them: an
+// operand's 64 lanes x 16 bytes in a row. A lane of half h (lane / 32) takes dwords h and
+// h + 2 of a row's run, so its values of product p are 4j + {0, 2}, 16 + 4j + {0, 2},
+// 4j + {1, 3}, 16 + 4j + {1, 3} with j = 2p + h.
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kTileCols = 32;    // columns of a tile
+constexpr int kChunkRuns = 4;    // runs between two barriers
+constexpr int kOperand = 2048;   // bytes of one tile's run: two operands
+
+// Workspace: operands [column tile][run][2][64][16 bytes], then d [column tile][run][32]
+// fp32; runs padded to whole chunks, columns to whole tiles, with zeros.
+struct Laid {
+    char *ops;
+    float *d;
+    int runs, tiles;
+};
+
+Laid laid_out(void *workspace, int64_t T, int nb)
+{
+    Laid l;
+    l.runs = (nb + kChunkRuns - 1) / kChunkRuns * kChunkRuns;
+    l.tiles = (int)((T + kTileCols - 1) / kTileCols);
+    l.ops = static_cast<char *>(workspace);
+    l.d = reinterpret_cast<float *>(l.ops + (size_t)l.tiles * l.runs * kOperand);
+    return l;
+}
+
+size_t laid_out_bytes(int64_t T, int64_t nb)
+{
+    const size_t runs = (nb + kChunkRuns - 1) / kChunkRuns * kChunkRuns;
+    return (size_t)((T + kTileCols - 1) / kTileCols) * runs * (kOperand + kTileCols * 4);
+}
+
+__device__ __forceinline__ uint32_t as_u32(f16x2 v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ f16x2 as_f16x2(uint32_t v) { return __builtin_bit_cast(f16x2, v); }
+
+// Four q as fp16: bytes 0 and 2, bytes 1 and 3.
+__device__ __forceinline__ void halves_of(uint32_t q, uint32_t &even, uint32_t &odd)
+{
+    const uint32_t u = q ^ 0x80808080u;  // q + 128
+    const f16x2 bias = {(_Float16)1152.0f, (_Float16)1152.0f};
+    even = as_u32(as_f16x2(__builtin_amdgcn_perm(0x64646464u, u, 0x04020400u)) - bias);
+    odd = as_u32(as_f16x2(__builtin_amdgcn_perm(0x64646464u, u, 0x04030401u)) - bias);
+}
+
+// A thread a column's run.
+__global__ __launch_bounds__(256) void q4_columns_kernel(const uint8_t *__restrict__ a, Laid l,
+                                                         int64_t T, int nb)
+{
+    const int c = threadIdx.x & 31, run = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int tile = blockIdx.y;
+    const int64_t col = (int64_t)tile * kTileCols + c;
+    if (run >= l.runs)
+        return;
+    uint32_t q[8] = {};
+    float d = 0.0f;
+    if (col < T && run < nb) {
+        const uint32_t *p =
+            reinterpret_cast<const uint32_t *>(a + (col * nb + run) * kQ81BlockBytes);
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            q[k] = p[k];
+        d = f16_bits_to_f32(p[8] & 0xffffu);
+    }
+    char *to = l.ops + ((size_t)tile * l.runs + run) * kOperand + c * 16;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        uint4 v;
+        halves_of(q[j], v.x, v.z);
+        halves_of(q[j + 4], v.y, v.w);
+        *reinterpret_cast<uint4 *>(to + (j >> 1) * 1024 + (j & 1) * 512) = v;
+    }
+    l.d[((size_t)tile * l.runs + run) * kTileCols + c] = d;
+}
+
+// A dword of codes as an operand; low, high: minus (1032 + zero) and (72 + zero), twice.
+__device__ __forceinline__ f16x8 codes_of(uint32_t w, f16x2 low, f16x2 high)
+{
+    const f16x2 part = {(_Float16)0.0625f, (_Float16)0.0625f};
+    const uint32_t u = w ^ 0x88888888u;  // code + 8
+    const uint32_t v = u >> 8;
+    const f16x2 a = as_f16x2((u & 0x000f000fu) | 0x64006400u) + low;
+    const f16x2 b = as_f16x2((u & 0x00f000f0u) | 0x64006400u) * part + high;
+    const f16x2 c = as_f16x2((v & 0x000f000fu) | 0x64006400u) + low;
+    const f16x2 d = as_f16x2((v & 0x00f000f0u) | 0x64006400u) * part + high;
+    return {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// 16 bytes a lane, straight into LDS at base + 16 * lane.
+__device__ __forceinline__ void to_lds(const void *from, void *base)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                     (__attribute__((address_space(3))) void *)base, 16, 0, 0);
+}
+
+// Four waves of 32 rows, NT tiles of 32 columns.
+template <int NT, bool Z>
+__global__ __launch_bounds__(256) void q4_mfma_kernel(const Q4Args g, const Laid l)
+{
+    // operands of a chunk: [run][tile], then d: [run][tile][32]; two of each
+    constexpr int kOps = kChunkRuns * NT * kOperand;
+    __shared__ __attribute__((aligned(16))) char ops[2][kOps];
+    __shared__ float ds[2][kChunkRuns * NT * kTileCols];
+    __shared__ __attribute__((aligned(16))) float ss[4][kChunkRuns][32];  // a wave's scales
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int half = lane >> 5;
+    const int64_t n0 = (int64_t)blockIdx.x * 128 + wave * 32;
+    const int tile0 = blockIdx.y * NT;
+    const int64_t row = n0 + (lane & 31) < g.m.N ? n0 + (lane & 31) : g.m.N - 1;
+    const uint4 *codes = static_cast<const uint4 *>(g.m.codes) + row * g.nb;
+    const int groups = g.nb >> g.shift;
+    const uint16_t *scales = static_cast<const uint16_t *>(g.m.scales) + row * groups;
+    const int8_t *zeros = g.m.zeros + row * groups;
+    const int chunks = l.runs / kChunkRuns;
+
+    auto stage = [&](int chunk, int buf) {
+        // (tiles behind the last are read from the last)
+        for (int i = wave; i < kChunkRuns * NT * 2; i += 4) {
+            const int run = i / (NT * 2), t = i / 2 % NT, p = i & 1;
+            const int tile = tile0 + t < l.tiles ? tile0 + t : l.tiles - 1;
+            to_lds(l.ops + ((size_t)tile * l.runs + chunk * kChunkRuns + run) * kOperand +
+                       p * 1024 + lane * 16,
+                   ops[buf] + (run * NT + t) * kOperand + p * 1024);
+        }
+        for (int i = threadIdx.x; i < kChunkRuns * NT * kTileCols; i += 256) {
+            const int run = i / (NT * kTileCols), t = i / kTileCols % NT, c = i % kTileCols;
+            const int tile = tile0 + t < l.tiles ? tile0 + t : l.tiles - 1;
+            ds[buf][i] = l.d[((size_t)tile * l.runs + chunk * kChunkRuns + run) * kTileCols + c];
+        }
+    };
+
+    f32x16 acc[NT] = {}, part[NT] = {};
+    stage(0, 0);
+    for (int chunk = 0; chunk < chunks; chunk++) {
+        const int buf = chunk & 1;
+        __syncthreads();
+        if (chunk + 1 < chunks)
+            stage(chunk + 1, buf ^ 1);
+        // lanes of half h hold runs 2i + h of the chunk's pairs
+        uint32_t w[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const int b = chunk * kChunkRuns + 2 * i + half;
+            const uint4 c = codes[b < g.nb ? b : g.nb - 1];
+            w[i][0] = c.x, w[i][1] = c.y, w[i][2] = c.z, w[i][3] = c.w;
+        }
+#pragma unroll
+        for (int r = 0; r < kChunkRuns; r++) {
+            const int run = chunk * kChunkRuns + r;
+            // a group's scales, through LDS to the rows that a lane's results are of
+            const int at = run >> g.shift;
+            const bool there = at < groups;
+            if ((run & ((1 << g.shift) - 1)) == 0 && half == 0)
+                ss[wave][r][lane] = there ? f16_bits_to_f32(scales[at]) : 0.0f;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            f16x2 low = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+            f16x2 high = {(_Float16)-72.0f, (_Float16)-72.0f};
+            if constexpr (Z) {
+                const _Float16 z = (_Float16)(float)(there ? zeros[at] : 0);
+                low -= f16x2{z, z};
+                high -= f16x2{z, z};
+            }
+            // after the swap the lower half holds dword 0 (2) of the pair's first run and
+            // the upper half dword 1 (3); the other register the same of the second run
+            if ((r & 1) == 0) {
+                auto x = __builtin_amdgcn_permlane32_swap(w[r / 2][0], w[r / 2][1], false, false);
+                auto y = __builtin_amdgcn_permlane32_swap(w[r / 2][2], w[r / 2][3], false, false);
+                w[r / 2][0] = x[0], w[r / 2][1] = x[1], w[r / 2][2] = y[0], w[r / 2][3] = y[1];
+            }
+            const f16x8 a0 = codes_of(w[r / 2][r & 1], low, high);
+            const f16x8 a1 = codes_of(w[r / 2][2 + (r & 1)], low, high);
+#pragma unroll
+            for (int t = 0; t < NT; t++) {
+                const char *op = ops[buf] + (r * NT + t) * kOperand + lane * 16;
+                const f16x8 b0 = *reinterpret_cast<const f16x8 *>(op);
+                const f16x8 b1 = *reinterpret_cast<const f16x8 *>(op + 1024);
+                const float d = ds[buf][(r * NT + t) * kTileCols + (lane & 31)];
+                f32x16 v = {};
+                v = __builtin_amdgcn_mfma_f32_32x32x16_f16(a0, b0, v, 0, 0, 0);
+                v = __builtin_amdgcn_mfma_f32_32x32x16_f16(a1, b1, v, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    part[t][i] = fmaf(v[i], d, part[t][i]);
+            }
+            if (((run + 1) & ((1 << g.shift) - 1)) == 0) {
+                const int first = r & ~((1 << g.shift) - 1);
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    const float4 sc =
+                        *reinterpret_cast<const float4 *>(&ss[wave][first][8 * q + 4 * half]);
+                    const float sv[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+                    for (int t = 0; t < NT; t++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            acc[t][4 * q + i] = fmaf(sv[i], part[t][4 * q + i], acc[t][4 * q + i]);
+                            part[t][4 * q + i] = 0.0f;
+                        }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+        const int64_t col = (int64_t)(tile0 + t) * kTileCols + (lane & 31);
+        if (col >= g.T)
+            continue;
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int64_t n = n0 + 8 * q + 4 * half + i;
+                if (n < g.m.N)
+                    g.y[col * g.m.N + n] = acc[t][4 * q + i];
+            }
+    }
+}
+
+template <int NT>
+int launch_mfma(const Q4Args &g, const Laid &l, hipStream_t stream)
+{
+    hipLaunchKernelGGL(q4_columns_kernel, dim3((unsigned)((l.runs + 7) / 8), (unsigned)l.tiles),
+                       dim3(256), 0, stream, g.a, l, g.T, g.nb);
+    if (int rc = check_launch())
+        return rc;
+    const dim3 grid((unsigned)((g.m.N + 127) / 128), (unsigned)((l.tiles + NT - 1) / NT));
+    if (g.m.zeros)
+        hipLaunchKernelGGL((q4_mfma_kernel<NT, true>), grid, dim3(256), 0, stream, g, l);
+    else
+        hipLaunchKernelGGL((q4_mfma_kernel<NT, false>), grid, dim3(256), 0, stream, g, l);
+    return check_launch();
+}
+
+constexpr int kDotCols = 8;       // the most columns without the matrix cores
+constexpr int64_t kMostCols = 8192;  // laid out at once
+
 }  // namespace
 
-int launch_mm_q4(const bqm_q4_matrix *m, const void *a, float *y, int64_t T, hipStream_t stream)
+size_t mm_q4_workspace(int64_t T, int64_t K)
 {
-    const Q4Args g = {*m, static_cast<const uint8_t *>(a), y, T, (int)(m->K / 32),
-                      m->group == 32 ? 0 : m->group == 64 ? 1 : 2};
+    return T <= kDotCols ? 0 : laid_out_bytes(std::min(T, kMostCols), K / 32);
+}
+
+int launch_mm_q4(const bqm_q4_matrix *m, const void *a, float *y, int64_t T, void *workspace,
+                 hipStream_t stream)
+{
+    Q4Args g = {*m, static_cast<const uint8_t *>(a), y, T, (int)(m->K / 32),
+                m->group == 32 ? 0 : m->group == 64 ? 1 : 2};
     if (T == 1)
         return launch_dot<1, 4>(g, stream);
     if (T == 2)
         return launch_dot<2, 4>(g, stream);
-    return launch_dot<4, 4>(g, stream);
+    if (T <= 4)
+        return launch_dot<4, 4>(g, stream);
+    if (T <= kDotCols)
+        return launch_dot<8, 4>(g, stream);
+    for (int64_t t = 0; t < T; t += kMostCols) {
+        g.T = std::min(T - t, kMostCols);
+        g.a = static_cast<const uint8_t *>(a) + t * g.nb * kQ81BlockBytes;
+        g.y = y + t * m->N;
+        const Laid l = laid_out(workspace, g.T, g.nb);
+        const int rc = g.T <= 32 ? launch_mfma<1>(g, l, stream)
+                       : g.T <= 64 ? launch_mfma<2>(g, l, stream)
+                                   : launch_mfma<4>(g, l, stream);
+        if (rc)
+            return rc;
+    }
+    return BQM_OK;
 }
 
 }  // namespace bqm

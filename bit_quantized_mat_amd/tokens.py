@@ -18,11 +18,11 @@ except ImportError as e:
     raise RuntimeError("bit_quantized_mat_amd._tokens is not built; run "
                        "bit_quantized_mat_amd.build.build() (or __graft_entry__.build()) first") from e
 
-from ._tokens import (Q4Matrix, mm_q4, q4_dequantize, q4_quantize, rms_norm, rms_norm_q8_1,  # noqa: E402
-                      sample)
+from ._tokens import (Q4Matrix, mm_q4, mm_q4_workspace_bytes, q4_dequantize, q4_quantize,  # noqa: E402
+                      rms_norm, rms_norm_q8_1, sample)
 
-__all__ = ["Q4Matrix", "mm_q4", "q4_dequantize", "q4_quantize", "rms_norm", "rms_norm_q8_1", "sample",
-           "sample_workspace_bytes"]
+__all__ = ["Q4Matrix", "mm_q4", "mm_q4_workspace_bytes", "q4_dequantize", "q4_quantize", "rms_norm",
+           "rms_norm_q8_1", "sample", "sample_workspace_bytes"]
 
 
 class _Q4Struct(ctypes.Structure):

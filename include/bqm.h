@@ -591,9 +591,17 @@ BQM_API int q4_quantize(const void *x, const bqm_q4_matrix *out, int32_t dtype, 
  *   isum[t][n][j] = sum_{i < 32} (code - zero) * q[t][32j + i]   (exact)
  *   a [T][K/32] Q8_1 blocks; y [T][N] fp32.
  * fp32 results differ from the exact sum by at most 1e-5 of sum_j |scale * d_a|
- * sum_i |code - zero| |q| (for zeros within -8 .. 7). Shapes: 1 <= T <=
- * BQM_MM_MAX_COLS. Alignment: a and y 4 bytes. */
-BQM_API int mm_q4(const bqm_q4_matrix *w, const void *a, float *y, int64_t T, void *stream);
+ * sum_i |code - zero| |q| (for zeros within -8 .. 7).
+ *   workspace: at least mm_q4_workspace_bytes(w, T) bytes, 256-byte aligned (NULL
+ *   if that is 0); nothing in it need be kept or cleared, and calls that overlap on
+ *   two streams need one each.
+ * Shapes: 1 <= T <= BQM_MM_MAX_COLS. Alignment: a and y 4 bytes. */
+BQM_API int mm_q4(const bqm_q4_matrix *w, const void *a, float *y, int64_t T, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/* Workspace mm_q4 needs for T columns (0 also for what it refuses; of the matrix
+ * only the sizes are read). */
+BQM_API size_t mm_q4_workspace_bytes(const bqm_q4_matrix *w, int64_t T);
 
 /* Rows of a 4-bit matrix (a table's look-up):
  *   out[i][k] = fp32(fp32(value of (rows[i], k)) * factor), stored as out_dtype;

@@ -57,7 +57,7 @@ MATRIX_BAD = [
 def test_q4_rejects():
     lib = bqm.library()
     quantize = lambda m=matrix(), x=P(GOOD), dtype=0: lib.q4_quantize(x, m, dtype, None)  # noqa: E731
-    mm = lambda m=matrix(), a=P(GOOD), y=P(FAR), T=3: lib.mm_q4(m, a, y, T, None)  # noqa: E731
+    mm = lambda m=matrix(), a=P(GOOD), y=P(FAR), T=3: lib.mm_q4(m, a, y, T, P(0x100000), 1 << 40, None)  # noqa: E731
     rows = lambda m=matrix(), r=P(GOOD), o=P(FAR), n=3, f=1.0, t=0: lib.q4_dequantize(m, r, o, n, f, t, None)  # noqa: E731
     for fn in (quantize, mm, rows):
         assert fn() == DEVICE and fn(matrix(zeros=GOOD + 1)) == DEVICE and fn(None) == NULL
@@ -70,6 +70,20 @@ def test_q4_rejects():
     assert rows(o=None) == NULL and rows(r=P(ODD)) == ALIGN and rows(o=P(FAR + 8)) == ALIGN
     assert rows(n=-1) == SHAPE and rows(n=1 << 31) == SHAPE and rows(t=3) == SHAPE
     assert rows(r=None, n=6) == SHAPE and rows(r=None, n=5) == DEVICE and rows(n=0) == DEVICE
+
+
+def test_mm_q4_workspace():
+    lib = bqm.library()
+    for T in (1, 8, 9, 33, 8193, 65536):
+        m = matrix(K=4096)
+        need = lib.mm_q4_workspace_bytes(m, T)
+        if need:
+            assert lib.mm_q4(m, P(GOOD), P(FAR), T, None, 1 << 40, None) == WORKSPACE
+            assert lib.mm_q4(m, P(GOOD), P(FAR), T, P(0x100000), need - 1, None) == WORKSPACE
+            assert lib.mm_q4(m, P(GOOD), P(FAR), T, P(0x100010), need, None) == ALIGN
+        assert lib.mm_q4(m, P(GOOD), P(FAR), T, P(0x100000), need, None) == DEVICE
+    for m, T in ((None, 9), (matrix(K=288), 9), (matrix(), 0), (matrix(), 65537)):
+        assert lib.mm_q4_workspace_bytes(m, T) == 0
 
 
 SAMPLE = ["logits", "stride", "heat", "k", "p", "least", "u", "tokens", "logprobs", "T", "V", "dtype", "ws",
