@@ -232,21 +232,30 @@ __device__ __forceinline__ f16x8 codes_of(uint32_t w, f16x2 low, f16x2 high)
     return {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// 16 bytes a lane, straight into LDS at base + 16 * lane.
-__device__ __forceinline__ void to_lds(const void *from, void *base)
+// 16 or 4 bytes a lane, straight into LDS at base + that many bytes times lane.
+__device__ __forceinline__ void to_lds16(const void *from, void *base)
 {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
                                      (__attribute__((address_space(3))) void *)base, 16, 0, 0);
 }
 
-// Four waves of 32 rows, NT tiles of 32 columns.
-template <int NT, bool Z>
-__global__ __launch_bounds__(256) void q4_mfma_kernel(const Q4Args g, const Laid l)
+__device__ __forceinline__ void to_lds4(const void *from, void *base)
 {
-    // operands of a chunk: [run][tile], then d: [run][tile][32]; two of each
-    constexpr int kOps = kChunkRuns * NT * kOperand;
-    __shared__ __attribute__((aligned(16))) char ops[2][kOps];
-    __shared__ float ds[2][kChunkRuns * NT * kTileCols];
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                     (__attribute__((address_space(3))) void *)base, 4, 0, 0);
+}
+
+// Four waves of 32 rows, NT tiles of 32 columns; groups of 32 << SH. (Two workgroups a
+// compute unit: with at most 256 registers a wave products' results stay out of the
+// accumulator registers, from which each would have to be copied.)
+template <int NT, int SH, bool Z>
+__global__ __launch_bounds__(256, 2) void q4_mfma_kernel(const Q4Args g, const Laid l)
+{
+    // a chunk's operands and d: [tile][run]; two of each
+    constexpr int kOps = kChunkRuns * kOperand;
+    constexpr int kDs = kChunkRuns * kTileCols;
+    __shared__ __attribute__((aligned(16))) char ops[2][NT * kOps];
+    __shared__ float ds[2][NT * kDs];
     __shared__ __attribute__((aligned(16))) float ss[4][kChunkRuns][32];  // a wave's scales
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int half = lane >> 5;
@@ -254,58 +263,77 @@ __global__ __launch_bounds__(256) void q4_mfma_kernel(const Q4Args g, const Laid
     const int tile0 = blockIdx.y * NT;
     const int64_t row = n0 + (lane & 31) < g.m.N ? n0 + (lane & 31) : g.m.N - 1;
     const uint4 *codes = static_cast<const uint4 *>(g.m.codes) + row * g.nb;
-    const int groups = g.nb >> g.shift;
+    constexpr int kGroupRuns = 1 << SH;
+    const int groups = g.nb >> SH;
     const uint16_t *scales = static_cast<const uint16_t *>(g.m.scales) + row * groups;
     const int8_t *zeros = g.m.zeros + row * groups;
     const int chunks = l.runs / kChunkRuns;
 
     auto stage = [&](int chunk, int buf) {
-        // (tiles behind the last are read from the last)
-        for (int i = wave; i < kChunkRuns * NT * 2; i += 4) {
-            const int run = i / (NT * 2), t = i / 2 % NT, p = i & 1;
+#pragma unroll
+        for (int i = 0; i < NT * 2; i++) {  // a wave takes 1 KB of each 4
+            const int t = i / 2, at = (i % 2) * 4096 + wave * 1024;
+            // (tiles behind the last are read from the last)
             const int tile = tile0 + t < l.tiles ? tile0 + t : l.tiles - 1;
-            to_lds(l.ops + ((size_t)tile * l.runs + chunk * kChunkRuns + run) * kOperand +
-                       p * 1024 + lane * 16,
-                   ops[buf] + (run * NT + t) * kOperand + p * 1024);
+            const size_t piece = (size_t)tile * (l.runs / kChunkRuns) + chunk;
+            to_lds16(l.ops + piece * kOps + at + lane * 16, ops[buf] + t * kOps + at);
         }
-        for (int i = threadIdx.x; i < kChunkRuns * NT * kTileCols; i += 256) {
-            const int run = i / (NT * kTileCols), t = i / kTileCols % NT, c = i % kTileCols;
+        for (int i = wave; i < NT * 2; i += 4) {
+            const int t = i / 2, at = (i % 2) * 64;
             const int tile = tile0 + t < l.tiles ? tile0 + t : l.tiles - 1;
-            ds[buf][i] = l.d[((size_t)tile * l.runs + chunk * kChunkRuns + run) * kTileCols + c];
+            const size_t piece = (size_t)tile * (l.runs / kChunkRuns) + chunk;
+            to_lds4(l.d + piece * kDs + at + lane, ds[buf] + t * kDs + at);
         }
     };
-
-    f32x16 acc[NT] = {}, part[NT] = {};
-    stage(0, 0);
-    for (int chunk = 0; chunk < chunks; chunk++) {
-        const int buf = chunk & 1;
-        __syncthreads();
-        if (chunk + 1 < chunks)
-            stage(chunk + 1, buf ^ 1);
-        // lanes of half h hold runs 2i + h of the chunk's pairs
-        uint32_t w[2][4];
+    // A chunk's codes, scales and zeros of a lane's row, a chunk ahead: lanes of half h
+    // hold runs 2i + h of the chunk's pairs.
+    constexpr int kGroups = kChunkRuns / kGroupRuns;
+    uint4 next[2];
+    uint32_t next_scale[kGroups];
+    int next_zero[kGroups];
+    auto fetch = [&](int chunk) {
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             const int b = chunk * kChunkRuns + 2 * i + half;
-            const uint4 c = codes[b < g.nb ? b : g.nb - 1];
-            w[i][0] = c.x, w[i][1] = c.y, w[i][2] = c.z, w[i][3] = c.w;
+            next[i] = codes[b < g.nb ? b : g.nb - 1];
+        }
+#pragma unroll
+        for (int i = 0; i < kGroups; i++) {
+            const int at = chunk * kGroups + i;
+            next_scale[i] = at < groups ? scales[at] : 0;  // (runs behind the end count nothing)
+            next_zero[i] = Z && at < groups ? zeros[at] : 0;
+        }
+    };
+
+    f32x16 acc[NT] = {}, part[NT];
+    stage(0, 0);
+    fetch(0);
+    for (int chunk = 0; chunk < chunks; chunk++) {
+        const int buf = chunk & 1;
+        __syncthreads();
+        uint32_t w[2][4];
+        f16x2 low[kGroups], high[kGroups];
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            w[i][0] = next[i].x, w[i][1] = next[i].y, w[i][2] = next[i].z, w[i][3] = next[i].w;
+#pragma unroll
+        for (int i = 0; i < kGroups; i++) {
+            // scales go through LDS to the rows that a lane's results are of
+            if (half == 0)
+                ss[wave][i][lane] = f16_bits_to_f32(next_scale[i]);
+            const _Float16 z = (_Float16)(float)next_zero[i];
+            low[i] = f16x2{(_Float16)-1032.0f, (_Float16)-1032.0f} - f16x2{z, z};
+            high[i] = f16x2{(_Float16)-72.0f, (_Float16)-72.0f} - f16x2{z, z};
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (chunk + 1 < chunks) {
+            stage(chunk + 1, buf ^ 1);
+            fetch(chunk + 1);
         }
 #pragma unroll
         for (int r = 0; r < kChunkRuns; r++) {
-            const int run = chunk * kChunkRuns + r;
-            // a group's scales, through LDS to the rows that a lane's results are of
-            const int at = run >> g.shift;
-            const bool there = at < groups;
-            if ((run & ((1 << g.shift) - 1)) == 0 && half == 0)
-                ss[wave][r][lane] = there ? f16_bits_to_f32(scales[at]) : 0.0f;
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            f16x2 low = {(_Float16)-1032.0f, (_Float16)-1032.0f};
-            f16x2 high = {(_Float16)-72.0f, (_Float16)-72.0f};
-            if constexpr (Z) {
-                const _Float16 z = (_Float16)(float)(there ? zeros[at] : 0);
-                low -= f16x2{z, z};
-                high -= f16x2{z, z};
-            }
+            constexpr int kLast = kGroupRuns - 1;
+            const int grp = r / kGroupRuns;
             // after the swap the lower half holds dword 0 (2) of the pair's first run and
             // the upper half dword 1 (3); the other register the same of the second run
             if ((r & 1) == 0) {
@@ -313,37 +341,46 @@ __global__ __launch_bounds__(256) void q4_mfma_kernel(const Q4Args g, const Laid
                 auto y = __builtin_amdgcn_permlane32_swap(w[r / 2][2], w[r / 2][3], false, false);
                 w[r / 2][0] = x[0], w[r / 2][1] = x[1], w[r / 2][2] = y[0], w[r / 2][3] = y[1];
             }
-            const f16x8 a0 = codes_of(w[r / 2][r & 1], low, high);
-            const f16x8 a1 = codes_of(w[r / 2][2 + (r & 1)], low, high);
+            const f16x8 a0 = codes_of(w[r / 2][r & 1], low[grp], high[grp]);
+            const f16x8 a1 = codes_of(w[r / 2][2 + (r & 1)], low[grp], high[grp]);
+            float sv[16];  // of the rows that a lane's results are of
+            auto load_scales = [&]() {
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    const float4 v =
+                        *reinterpret_cast<const float4 *>(&ss[wave][grp][8 * q + 4 * half]);
+                    sv[4 * q] = v.x, sv[4 * q + 1] = v.y, sv[4 * q + 2] = v.z, sv[4 * q + 3] = v.w;
+                }
+            };
+            if constexpr (SH == 0)
+                load_scales();
 #pragma unroll
             for (int t = 0; t < NT; t++) {
-                const char *op = ops[buf] + (r * NT + t) * kOperand + lane * 16;
+                const char *op = ops[buf] + t * kOps + r * kOperand + lane * 16;
                 const f16x8 b0 = *reinterpret_cast<const f16x8 *>(op);
                 const f16x8 b1 = *reinterpret_cast<const f16x8 *>(op + 1024);
-                const float d = ds[buf][(r * NT + t) * kTileCols + (lane & 31)];
+                const float d = ds[buf][t * kDs + r * kTileCols + (lane & 31)];
                 f32x16 v = {};
                 v = __builtin_amdgcn_mfma_f32_32x32x16_f16(a0, b0, v, 0, 0, 0);
                 v = __builtin_amdgcn_mfma_f32_32x32x16_f16(a1, b1, v, 0, 0, 0);
 #pragma unroll
-                for (int i = 0; i < 16; i++)
-                    part[t][i] = fmaf(v[i], d, part[t][i]);
-            }
-            if (((run + 1) & ((1 << g.shift) - 1)) == 0) {
-                const int first = r & ~((1 << g.shift) - 1);
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    const float4 sc =
-                        *reinterpret_cast<const float4 *>(&ss[wave][first][8 * q + 4 * half]);
-                    const float sv[4] = {sc.x, sc.y, sc.z, sc.w};
-#pragma unroll
-                    for (int t = 0; t < NT; t++)
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            acc[t][4 * q + i] = fmaf(sv[i], part[t][4 * q + i], acc[t][4 * q + i]);
-                            part[t][4 * q + i] = 0.0f;
-                        }
+                for (int i = 0; i < 16; i++) {
+                    if constexpr (SH == 0)
+                        acc[t][i] = fmaf(sv[i], v[i] * d, acc[t][i]);
+                    else
+                        part[t][i] = r % kGroupRuns ? fmaf(v[i], d, part[t][i]) : v[i] * d;
                 }
             }
+            if (SH > 0 && r % kGroupRuns == kLast) {
+                load_scales();
+#pragma unroll
+                for (int t = 0; t < NT; t++)
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        acc[t][i] = fmaf(sv[i], part[t][i], acc[t][i]);
+            }
+            if constexpr (SH < 2 && NT == 4)
+                __builtin_amdgcn_sched_barrier(0);  // or later runs' reads ahead spill registers
         }
     }
 #pragma unroll
@@ -362,6 +399,17 @@ __global__ __launch_bounds__(256) void q4_mfma_kernel(const Q4Args g, const Laid
     }
 }
 
+template <int NT, int SH>
+int launch_mfma_group(const Q4Args &g, const Laid &l, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((g.m.N + 127) / 128), (unsigned)((l.tiles + NT - 1) / NT));
+    if (g.m.zeros)
+        hipLaunchKernelGGL((q4_mfma_kernel<NT, SH, true>), grid, dim3(256), 0, stream, g, l);
+    else
+        hipLaunchKernelGGL((q4_mfma_kernel<NT, SH, false>), grid, dim3(256), 0, stream, g, l);
+    return check_launch();
+}
+
 template <int NT>
 int launch_mfma(const Q4Args &g, const Laid &l, hipStream_t stream)
 {
@@ -369,12 +417,9 @@ int launch_mfma(const Q4Args &g, const Laid &l, hipStream_t stream)
                        dim3(256), 0, stream, g.a, l, g.T, g.nb);
     if (int rc = check_launch())
         return rc;
-    const dim3 grid((unsigned)((g.m.N + 127) / 128), (unsigned)((l.tiles + NT - 1) / NT));
-    if (g.m.zeros)
-        hipLaunchKernelGGL((q4_mfma_kernel<NT, true>), grid, dim3(256), 0, stream, g, l);
-    else
-        hipLaunchKernelGGL((q4_mfma_kernel<NT, false>), grid, dim3(256), 0, stream, g, l);
-    return check_launch();
+    return g.shift == 0   ? launch_mfma_group<NT, 0>(g, l, stream)
+           : g.shift == 1 ? launch_mfma_group<NT, 1>(g, l, stream)
+                          : launch_mfma_group<NT, 2>(g, l, stream);
 }
 
 constexpr int kDotCols = 8;       // the most columns without the matrix cores
