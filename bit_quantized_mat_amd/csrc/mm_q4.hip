@@ -219,16 +219,25 @@ __global__ __launch_bounds__(256) void q4_columns_kernel(const uint8_t *__restri
     l.d[((size_t)tile * l.runs + run) * kTileCols + c] = d;
 }
 
+// Bits of w turned by c where mask is set, c elsewhere: the nibbles of a mask, plus 8,
+// under an exponent.
+__device__ __forceinline__ f16x2 under(uint32_t w, uint32_t mask, uint32_t c)
+{
+    return as_f16x2(__builtin_amdgcn_bitop3_b32(w, mask, c, 0x6a));
+}
+
 // A dword of codes as an operand; low, high: minus (1032 + zero) and (72 + zero), twice.
+// (High nibbles stand for 16 times themselves; nothing is rounded.)
 __device__ __forceinline__ f16x8 codes_of(uint32_t w, f16x2 low, f16x2 high)
 {
     const f16x2 part = {(_Float16)0.0625f, (_Float16)0.0625f};
-    const uint32_t u = w ^ 0x88888888u;  // code + 8
-    const uint32_t v = u >> 8;
-    const f16x2 a = as_f16x2((u & 0x000f000fu) | 0x64006400u) + low;
-    const f16x2 b = as_f16x2((u & 0x00f000f0u) | 0x64006400u) * part + high;
-    const f16x2 c = as_f16x2((v & 0x000f000fu) | 0x64006400u) + low;
-    const f16x2 d = as_f16x2((v & 0x00f000f0u) | 0x64006400u) * part + high;
+    const uint32_t v = w >> 8;
+    const f16x2 a = under(w, 0x000f000fu, 0x64086408u) + low;
+    const f16x2 b =
+        __builtin_elementwise_fma(under(w, 0x00f000f0u, 0x64806480u), part, high);
+    const f16x2 c = under(v, 0x000f000fu, 0x64086408u) + low;
+    const f16x2 d =
+        __builtin_elementwise_fma(under(v, 0x00f000f0u, 0x64806480u), part, high);
     return {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
@@ -257,7 +266,7 @@ __global__ __launch_bounds__(256, 2) void q4_mfma_kernel(const Q4Args g, const L
     __shared__ __attribute__((aligned(16))) char ops[2][NT * kOps];
     __shared__ float ds[2][NT * kDs];
     __shared__ __attribute__((aligned(16))) float ss[4][kChunkRuns][32];  // a wave's scales
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int half = lane >> 5;
     const int64_t n0 = (int64_t)blockIdx.x * 128 + wave * 32;
     const int tile0 = blockIdx.y * NT;
@@ -271,18 +280,18 @@ __global__ __launch_bounds__(256, 2) void q4_mfma_kernel(const Q4Args g, const L
 
     auto stage = [&](int chunk, int buf) {
 #pragma unroll
-        for (int i = 0; i < NT * 2; i++) {  // a wave takes 1 KB of each 4
-            const int t = i / 2, at = (i % 2) * 4096 + wave * 1024;
+        for (int t = 0; t < NT; t++) {
             // (tiles behind the last are read from the last)
             const int tile = tile0 + t < l.tiles ? tile0 + t : l.tiles - 1;
-            const size_t piece = (size_t)tile * (l.runs / kChunkRuns) + chunk;
-            to_lds16(l.ops + piece * kOps + at + lane * 16, ops[buf] + t * kOps + at);
-        }
-        for (int i = wave; i < NT * 2; i += 4) {
-            const int t = i / 2, at = (i % 2) * 64;
-            const int tile = tile0 + t < l.tiles ? tile0 + t : l.tiles - 1;
-            const size_t piece = (size_t)tile * (l.runs / kChunkRuns) + chunk;
-            to_lds4(l.d + piece * kDs + at + lane, ds[buf] + t * kDs + at);
+            const size_t piece = (size_t)tile * chunks + chunk;
+            const char *from = l.ops + piece * kOps + wave * 1024;  // 1 KB a wave of each 4
+            char *to = ops[buf] + t * kOps + wave * 1024;
+            to_lds16(from + lane * 16u, to);
+            to_lds16(from + 4096 + lane * 16u, to + 4096);
+            if (wave == t)
+                to_lds4(l.d + piece * kDs + (uint32_t)lane, ds[buf] + t * kDs);
+            if (wave == (t ^ 1))
+                to_lds4(l.d + piece * kDs + 64 + (uint32_t)lane, ds[buf] + t * kDs + 64);
         }
     };
     // A chunk's codes, scales and zeros of a lane's row, a chunk ahead: lanes of half h
@@ -305,14 +314,47 @@ __global__ __launch_bounds__(256, 2) void q4_mfma_kernel(const Q4Args g, const L
         }
     };
 
-    f32x16 acc[NT] = {}, part[NT];
+    // Steps of one run and column tile, run by run: a step issues the products of the
+    // next one between its own sums, so results have the time of 16 sums to come, and
+    // reads the operands of the one after.
+    constexpr int kSteps = kChunkRuns * NT;
+    f32x16 acc[NT] = {}, part[NT] = {}, v[2];
+    float sv[16] = {};  // scales of the group that `part` is of, for the rows of a lane's results
+    uint32_t w[2][4];
+    f16x2 low[kGroups], high[kGroups];
+    f16x8 a[2][2], b[2];  // codes of a run and the next; columns of the next step
+    float d[3];
+    auto unpack = [&](int r, int p) {
+        // after the swap the lower half holds dword 0 (2) of the pair's first run and
+        // the upper half dword 1 (3); the other register the same of the second run
+        uint32_t *x = w[r / 2];
+        if ((r & 1) == 0) {
+            auto y = __builtin_amdgcn_permlane32_swap(x[2 * p], x[2 * p + 1], false, false);
+            x[2 * p] = y[0], x[2 * p + 1] = y[1];
+        }
+        a[r & 1][p] = codes_of(x[2 * p + (r & 1)], low[r / kGroupRuns], high[r / kGroupRuns]);
+    };
+    auto scales_of = [&](int group) {
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const float4 x =
+                *reinterpret_cast<const float4 *>(&ss[wave][group][8 * q + 4 * half]);
+            sv[4 * q] = x.x, sv[4 * q + 1] = x.y, sv[4 * q + 2] = x.z, sv[4 * q + 3] = x.w;
+        }
+    };
     stage(0, 0);
     fetch(0);
     for (int chunk = 0; chunk < chunks; chunk++) {
         const int buf = chunk & 1;
         __syncthreads();
-        uint32_t w[2][4];
-        f16x2 low[kGroups], high[kGroups];
+        auto read = [&](int s) {  // a step's columns
+            const int r = s / NT, t = s % NT;
+            const char *op = ops[buf] + t * kOps + r * kOperand + lane * 16;
+            b[0] = *reinterpret_cast<const f16x8 *>(op);
+            b[1] = *reinterpret_cast<const f16x8 *>(op + 1024);
+            d[s % 3] = ds[buf][t * kDs + r * kTileCols + (lane & 31)];
+        };
+        read(0);
 #pragma unroll
         for (int i = 0; i < 2; i++)
             w[i][0] = next[i].x, w[i][1] = next[i].y, w[i][2] = next[i].z, w[i][3] = next[i].w;
@@ -330,58 +372,67 @@ __global__ __launch_bounds__(256, 2) void q4_mfma_kernel(const Q4Args g, const L
             stage(chunk + 1, buf ^ 1);
             fetch(chunk + 1);
         }
+        if constexpr (SH == 0)
+            scales_of(0);
+        unpack(0, 0);
+        unpack(0, 1);
+        v[0] = f32x16{};
+        v[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[0][0], b[0], v[0], 0, 0, 0);
+        v[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[0][1], b[1], v[0], 0, 0, 0);
+        read(1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int r = 0; r < kChunkRuns; r++) {
-            constexpr int kLast = kGroupRuns - 1;
-            const int grp = r / kGroupRuns;
-            // after the swap the lower half holds dword 0 (2) of the pair's first run and
-            // the upper half dword 1 (3); the other register the same of the second run
-            if ((r & 1) == 0) {
-                auto x = __builtin_amdgcn_permlane32_swap(w[r / 2][0], w[r / 2][1], false, false);
-                auto y = __builtin_amdgcn_permlane32_swap(w[r / 2][2], w[r / 2][3], false, false);
-                w[r / 2][0] = x[0], w[r / 2][1] = x[1], w[r / 2][2] = y[0], w[r / 2][3] = y[1];
-            }
-            const f16x8 a0 = codes_of(w[r / 2][r & 1], low[grp], high[grp]);
-            const f16x8 a1 = codes_of(w[r / 2][2 + (r & 1)], low[grp], high[grp]);
-            float sv[16];  // of the rows that a lane's results are of
-            auto load_scales = [&]() {
+        for (int s = 0; s < kSteps; s++) {
+            const int r = s / NT, t = s % NT, u = s + 1, ur = u / NT;
+            auto sums = [&](int from) {
 #pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    const float4 v =
-                        *reinterpret_cast<const float4 *>(&ss[wave][grp][8 * q + 4 * half]);
-                    sv[4 * q] = v.x, sv[4 * q + 1] = v.y, sv[4 * q + 2] = v.z, sv[4 * q + 3] = v.w;
+                for (int i = from; i < from + 8; i++) {
+                    const float x = v[s & 1][i];
+                    if constexpr (SH == 0) {
+                        acc[t][i] = fmaf(sv[i], x * d[s % 3], acc[t][i]);
+                    } else if (r % kGroupRuns) {
+                        part[t][i] = fmaf(x, d[s % 3], part[t][i]);
+                    } else {  // a group begins: the one before is done
+                        acc[t][i] = fmaf(sv[i], part[t][i], acc[t][i]);
+                        part[t][i] = x * d[s % 3];
+                    }
                 }
             };
-            if constexpr (SH == 0)
-                load_scales();
-#pragma unroll
-            for (int t = 0; t < NT; t++) {
-                const char *op = ops[buf] + t * kOps + r * kOperand + lane * 16;
-                const f16x8 b0 = *reinterpret_cast<const f16x8 *>(op);
-                const f16x8 b1 = *reinterpret_cast<const f16x8 *>(op + 1024);
-                const float d = ds[buf][t * kDs + r * kTileCols + (lane & 31)];
-                f32x16 v = {};
-                v = __builtin_amdgcn_mfma_f32_32x32x16_f16(a0, b0, v, 0, 0, 0);
-                v = __builtin_amdgcn_mfma_f32_32x32x16_f16(a1, b1, v, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    if constexpr (SH == 0)
-                        acc[t][i] = fmaf(sv[i], v[i] * d, acc[t][i]);
-                    else
-                        part[t][i] = r % kGroupRuns ? fmaf(v[i], d, part[t][i]) : v[i] * d;
-                }
+            // the next run's codes, half of them at a time, before its first step's products
+            if (NT == 1 && r + 1 < kChunkRuns) {
+                unpack(r + 1, 0);
+                unpack(r + 1, 1);
             }
-            if (SH > 0 && r % kGroupRuns == kLast) {
-                load_scales();
-#pragma unroll
-                for (int t = 0; t < NT; t++)
-#pragma unroll
-                    for (int i = 0; i < 16; i++)
-                        acc[t][i] = fmaf(sv[i], part[t][i], acc[t][i]);
+            if (u < kSteps) {
+                v[u & 1] = f32x16{};
+                v[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[ur & 1][0], b[0], v[u & 1], 0, 0, 0);
             }
-            if constexpr (SH < 2 && NT == 4)
-                __builtin_amdgcn_sched_barrier(0);  // or later runs' reads ahead spill registers
+            __builtin_amdgcn_sched_barrier(0);
+            sums(0);
+            if (NT > 1 && t == NT - 2 && r + 1 < kChunkRuns)
+                unpack(r + 1, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (u < kSteps)
+                v[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[ur & 1][1], b[1], v[u & 1], 0, 0, 0);
+            if (s + 2 < kSteps)
+                read(s + 2);
+            __builtin_amdgcn_sched_barrier(0);
+            sums(8);
+            if (NT > 1 && t == NT - 2 && r + 1 < kChunkRuns)
+                unpack(r + 1, 1);
+            if (SH == 0 && t == NT - 1 && r + 1 < kChunkRuns)
+                scales_of(r + 1);
+            if (SH > 0 && t == NT - 1 && (r + 1) % kGroupRuns == 0)
+                scales_of(r / kGroupRuns);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    }
+    if constexpr (SH > 0) {
+#pragma unroll
+        for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                acc[t][i] = fmaf(sv[i], part[t][i], acc[t][i]);
     }
 #pragma unroll
     for (int t = 0; t < NT; t++) {
