@@ -136,24 +136,23 @@ int launch_dot(const Q4Args &g, hipStream_t stream)
 // ---- many columns: the matrix cores ------------------------------------------------
 //
 // Codes less zeros (-15 .. 15) and q (-127 .. 127) are exact in fp16, and sums over a run
-// of 32 are exact in fp32, so a 32 x 32 tile of a run is two 32x32x16 products whose result
+// of 32 are exact in fp32, so a 16 x 16 tile of a run is one 16x16x32 product whose result
 // needs one fma by d_a, and one by the scale at the end of a group. Eight codes become
-// fp16 in ten instructions: a nibble under the exponent of 1024 is 1024 + nibble.
+// fp16 in nine instructions: a nibble under the exponent of 1024 is 1024 + nibble.
 //
-// The columns are laid out once a call, in the order in which lanes read them: an
-// operand's 64 lanes x 16 bytes in a row. A lane of half h (lane / 32) takes dwords h and
-// h + 2 of a row's run, so its values of product p are 4j + {0, 2}, 16 + 4j + {0, 2},
-// 4j + {1, 3}, 16 + 4j + {1, 3} with j = 2p + h.
+// A lane of group h (lane / 16) takes dword h of a row's run: the values 4h + {0, 2},
+// 16 + 4h + {0, 2}, 4h + {1, 3}, 16 + 4h + {1, 3}. The columns are laid out once a call, in
+// the order in which lanes read them: an operand's 64 lanes x 16 bytes in a row.
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTileCols = 32;    // columns of a tile
 constexpr int kChunkRuns = 4;    // runs between two barriers
 constexpr int kOperand = 2048;   // bytes of one tile's run: two operands
 
-// Workspace: operands [column tile][run][2][64][16 bytes], then d [column tile][run][32]
+// Workspace: operands [column tile][run][half of the columns][64][16 bytes], then d [column tile][run][32]
 // fp32; runs padded to whole chunks, columns to whole tiles, with zeros.
 struct Laid {
     char *ops;
@@ -208,13 +207,13 @@ __global__ __launch_bounds__(256) void q4_columns_kernel(const uint8_t *__restri
             q[k] = p[k];
         d = f16_bits_to_f32(p[8] & 0xffffu);
     }
-    char *to = l.ops + ((size_t)tile * l.runs + run) * kOperand + c * 16;
+    char *to = l.ops + ((size_t)tile * l.runs + run) * kOperand + (c >> 4) * 1024 + (c & 15) * 16;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         uint4 v;
         halves_of(q[j], v.x, v.z);
         halves_of(q[j + 4], v.y, v.w);
-        *reinterpret_cast<uint4 *>(to + (j >> 1) * 1024 + (j & 1) * 512) = v;
+        *reinterpret_cast<uint4 *>(to + j * 256) = v;
     }
     l.d[((size_t)tile * l.runs + run) * kTileCols + c] = d;
 }
@@ -241,246 +240,559 @@ __device__ __forceinline__ f16x8 codes_of(uint32_t w, f16x2 low, f16x2 high)
     return {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// 16 or 4 bytes a lane, straight into LDS at base + that many bytes times lane.
-__device__ __forceinline__ void to_lds16(const void *from, void *base)
-{
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                     (__attribute__((address_space(3))) void *)base, 16, 0, 0);
-}
-
-__device__ __forceinline__ void to_lds4(const void *from, void *base)
-{
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                     (__attribute__((address_space(3))) void *)base, 4, 0, 0);
-}
-
 // Four waves of 32 rows, NT tiles of 32 columns; groups of 32 << SH. (Two workgroups a
 // compute unit: with at most 256 registers a wave products' results stay out of the
 // accumulator registers, from which each would have to be copied.)
-template <int NT, int SH, bool Z>
-__global__ __launch_bounds__(256, 2) void q4_mfma_kernel(const Q4Args g, const Laid l)
+//
+// A step is one tile and run: four products and the sums of their results. Steps go tile by
+// tile, so only one tile has a group's sum beside its total. A step issues the products of
+// the next one between its own sums, so results have the time of 16 sums to come. The next
+// chunk's columns come through registers, half of them at a time: loads that go straight
+// into LDS would have every later read of LDS wait for them.
+//
+// Scales and zeros are gathered, a row a lane, which costs the loads' path as much as 1 KB of
+// columns each time: kKept groups at once.
+constexpr int kKept = 8;
+
+template <int NT, int W, int SH, bool Z>
+__global__ __launch_bounds__(64 * W, 2) void q4_mfma_kernel(const Q4Args g, const Laid l)
 {
     // a chunk's operands and d: [tile][run]; two of each
     constexpr int kOps = kChunkRuns * kOperand;
     constexpr int kDs = kChunkRuns * kTileCols;
+    constexpr int kGroupRuns = 1 << SH;
+    constexpr int kGroups = kChunkRuns / kGroupRuns;
     __shared__ __attribute__((aligned(16))) char ops[2][NT * kOps];
     __shared__ float ds[2][NT * kDs];
-    __shared__ __attribute__((aligned(16))) float ss[4][kChunkRuns][32];  // a wave's scales
+    // a wave's scales and zeros of kKept groups, those in use and the next ones
+    __shared__ __attribute__((aligned(8))) uint16_t kept_scales[W][2][kKept][32];
+    __shared__ int8_t kept_zeros[W][2][kKept][32];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int half = lane >> 5;
-    const int64_t n0 = (int64_t)blockIdx.x * 128 + wave * 32;
+    const int h = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * (32 * W) + wave * 32;
     const int tile0 = blockIdx.y * NT;
-    const int64_t row = n0 + (lane & 31) < g.m.N ? n0 + (lane & 31) : g.m.N - 1;
-    const uint4 *codes = static_cast<const uint4 *>(g.m.codes) + row * g.nb;
-    constexpr int kGroupRuns = 1 << SH;
     const int groups = g.nb >> SH;
-    const uint16_t *scales = static_cast<const uint16_t *>(g.m.scales) + row * groups;
-    const int8_t *zeros = g.m.zeros + row * groups;
+    auto row_of = [&](int i) { return n0 + i < g.m.N ? n0 + i : g.m.N - 1; };
     const int chunks = l.runs / kChunkRuns;
 
-    auto stage = [&](int chunk, int buf) {
+    // columns on their way: half of a chunk's pieces of 16 bytes, and d
+    constexpr int kPieces = NT * 4 / W;
+    constexpr int kDPieces = (NT * 2 + W - 1) / W;
+    u32x4 on_way[kPieces];
+    float d_on_way[kDPieces];
+    const int tiles = l.tiles - tile0 < NT ? l.tiles - tile0 : NT;
+    const __amdgpu_buffer_rsrc_t columns = make_rsrc(
+        l.ops + (size_t)tile0 * l.runs * kOperand, (uint64_t)tiles * l.runs * kOperand);
+    const float *const all_d = l.d + (size_t)tile0 * l.runs * kTileCols;
+    auto chunk_of = [&](int t, int chunk) {  // (tiles behind the last are read from the last)
+        return (t < tiles ? t : tiles - 1) * chunks + chunk;
+    };
+    auto load = [&](int chunk, int part) {
 #pragma unroll
-        for (int t = 0; t < NT; t++) {
-            // (tiles behind the last are read from the last)
-            const int tile = tile0 + t < l.tiles ? tile0 + t : l.tiles - 1;
-            const size_t piece = (size_t)tile * chunks + chunk;
-            const char *from = l.ops + piece * kOps + wave * 1024;  // 1 KB a wave of each 4
-            char *to = ops[buf] + t * kOps + wave * 1024;
-            to_lds16(from + lane * 16u, to);
-            to_lds16(from + 4096 + lane * 16u, to + 4096);
-            if (wave == t)
-                to_lds4(l.d + piece * kDs + (uint32_t)lane, ds[buf] + t * kDs);
-            if (wave == (t ^ 1))
-                to_lds4(l.d + piece * kDs + 64 + (uint32_t)lane, ds[buf] + t * kDs + 64);
+        for (int i = 0; i < kPieces; i++) {
+            const int at = (part * kPieces + i) * W * 1024;  // of the tiles' chunks in a row
+            on_way[i] = __builtin_amdgcn_raw_buffer_load_b128(
+                columns, threadIdx.x * 16, chunk_of(at / kOps, chunk) * kOps + at % kOps, 0);
+        }
+        if (part == 0) {
+#pragma unroll
+            for (int i = 0; i < kDPieces; i++) {
+                const int t = i * (W / 2) + (wave >> 1);  // two waves a tile
+                if ((i + 1) * (W / 2) <= NT || t < NT)
+                    d_on_way[i] = all_d[chunk_of(t, chunk) * kDs + (threadIdx.x & 127u)];
+            }
         }
     };
-    // A chunk's codes, scales and zeros of a lane's row, a chunk ahead: lanes of half h
-    // hold runs 2i + h of the chunk's pairs.
-    constexpr int kGroups = kChunkRuns / kGroupRuns;
-    uint4 next[2];
-    uint32_t next_scale[kGroups];
-    int next_zero[kGroups];
+    auto store = [&](int buf, int part) {
+#pragma unroll
+        for (int i = 0; i < kPieces; i++)
+            *reinterpret_cast<u32x4 *>(ops[buf] + (part * kPieces + i) * W * 1024 +
+                                       threadIdx.x * 16) = on_way[i];
+        if (part == 0) {
+#pragma unroll
+            for (int i = 0; i < kDPieces; i++)
+                if ((i + 1) * (W / 2) <= NT || i * (W / 2) + (wave >> 1) < NT)
+                    ds[buf][i * W * 64 + threadIdx.x] = d_on_way[i];
+        }
+    };
+
+    // A chunk's codes of a lane's two rows, a chunk ahead: lanes of group h hold run h. (Rows
+    // behind the last are zeros; runs behind a row's last meet columns of zero.)
+    const int64_t rows = g.m.N - n0 < 32 ? g.m.N - n0 : 32;
+    const __amdgpu_buffer_rsrc_t codes =
+        make_rsrc(static_cast<const char *>(g.m.codes) + n0 * g.nb * 16,
+                  rows > 0 ? (uint64_t)rows * g.nb * 16 : 0);
+    u32x4 next[2];
     auto fetch = [&](int chunk) {
 #pragma unroll
+        for (int i = 0; i < 2; i++)
+            next[i] = __builtin_amdgcn_raw_buffer_load_b128(
+                codes, ((16 * i + (lane & 15)) * g.nb + h) * 16, chunk * (kChunkRuns * 16), 0);
+    };
+    // Half a period's scales and zeros of row lane % 32; none behind the row's end.
+    uint64_t scales_on_way;
+    uint32_t zeros_on_way;
+    auto gather = [&](int period) {
+        const int at = period * kKept + lane / 32 * (kKept / 2);
+        const int64_t place = row_of(lane & 31) * groups + at;
+        const uint16_t *sp = static_cast<const uint16_t *>(g.m.scales) + place;
+        scales_on_way = 0;
+        zeros_on_way = 0;
+        if (at + 4 <= groups) {
+            __builtin_memcpy(&scales_on_way, sp, 8);
+            if constexpr (Z)
+                __builtin_memcpy(&zeros_on_way, g.m.zeros + place, 4);
+        } else {
+            for (int i = 0; at + i < groups; i++) {
+                scales_on_way |= (uint64_t)sp[i] << (16 * i);
+                if constexpr (Z)
+                    zeros_on_way |= (uint32_t)(uint8_t)g.m.zeros[place + i] << (8 * i);
+            }
+        }
+    };
+    auto keep = [&](int period) {
+#pragma unroll
+        for (int i = 0; i < kKept / 2; i++) {
+            const int at = lane / 32 * (kKept / 2) + i;
+            kept_scales[wave][period & 1][at][lane & 31] = (uint16_t)(scales_on_way >> (16 * i));
+            if constexpr (Z)
+                kept_zeros[wave][period & 1][at][lane & 31] = (int8_t)(zeros_on_way >> (8 * i));
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    };
+    int zero[kGroups][2] = {};  // of the next chunk, for a lane's two rows
+    auto zeros_of = [&](int chunk) {
+        if constexpr (Z) {
+#pragma unroll
+            for (int i = 0; i < kGroups; i++) {
+                const int at = chunk * kGroups + i;
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+                    zero[i][j] = kept_zeros[wave][at / kKept & 1][at % kKept][16 * j + (lane & 15)];
+            }
+        }
+    };
+
+    constexpr int kSteps = kChunkRuns * NT;
+    // [tile][row tile, column half], four rows each
+    f32x4 acc[NT][4] = {}, part[4], v[2][4];
+    float sv[kGroups][2][4];  // scales of the rows that a lane's results are of
+    f16x8 a[kChunkRuns][2], b[2][2];  // a chunk's codes; columns of a step and the next
+    float d[3][2];
+    // the next chunk's codes: lanes of group h hold run h; exchanged, register r holds dword
+    // h of run r
+    auto exchange = [&](u32x4 &c) {
+        auto p = __builtin_amdgcn_permlane32_swap(c.x, c.z, false, false);
+        auto q = __builtin_amdgcn_permlane32_swap(c.y, c.w, false, false);
+        auto x = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false);
+        auto y = __builtin_amdgcn_permlane16_swap(p[1], q[1], false, false);
+        c = u32x4{x[0], x[1], y[0], y[1]};
+    };
+    auto unpack = [&](int r) {
+#pragma unroll
         for (int i = 0; i < 2; i++) {
-            const int b = chunk * kChunkRuns + 2 * i + half;
-            next[i] = codes[b < g.nb ? b : g.nb - 1];
+            const uint32_t w = next[i][r];
+            const _Float16 z = (_Float16)(float)zero[r / kGroupRuns][i];
+            a[r][i] = codes_of(w, f16x2{(_Float16)-1032.0f, (_Float16)-1032.0f} - f16x2{z, z},
+                               f16x2{(_Float16)-72.0f, (_Float16)-72.0f} - f16x2{z, z});
+        }
+    };
+    fetch(0);
+    gather(0);
+    load(0, 0);
+    keep(0);
+    gather(1);
+    store(0, 0);
+    load(0, 1);
+    store(0, 1);
+    zeros_of(0);
+    exchange(next[0]);
+    exchange(next[1]);
+#pragma unroll
+    for (int r = 0; r < kChunkRuns; r++)
+        unpack(r);
+    for (int chunk = 0; chunk < chunks; chunk++) {
+        const int buf = chunk & 1;
+        const int after = chunk + 1 < chunks ? chunk + 1 : chunk;  // (the last one again)
+        __syncthreads();
+        auto read = [&](int s) {  // a step's columns
+            const int t = s / kChunkRuns, r = s % kChunkRuns;
+            const char *op = ops[buf] + t * kOps + r * kOperand + lane * 16;
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                b[s & 1][i] = *reinterpret_cast<const f16x8 *>(op + 1024 * i);
+                d[s % 3][i] = ds[buf][t * kDs + r * kTileCols + 16 * i + (lane & 15)];
+            }
+        };
+        read(0);
+        read(1);
+        constexpr int kPeriod = kKept / kGroups;  // chunks
+        if (chunk % kPeriod == kPeriod - 1) {
+            keep(chunk / kPeriod + 1);
+            gather(chunk / kPeriod + 2);
         }
 #pragma unroll
         for (int i = 0; i < kGroups; i++) {
             const int at = chunk * kGroups + i;
-            next_scale[i] = at < groups ? scales[at] : 0;  // (runs behind the end count nothing)
-            next_zero[i] = Z && at < groups ? zeros[at] : 0;
-        }
-    };
-
-    // Steps of one run and column tile, run by run: a step issues the products of the
-    // next one between its own sums, so results have the time of 16 sums to come, and
-    // reads the operands of the one after.
-    constexpr int kSteps = kChunkRuns * NT;
-    f32x16 acc[NT] = {}, part[NT] = {}, v[2];
-    float sv[16] = {};  // scales of the group that `part` is of, for the rows of a lane's results
-    uint32_t w[2][4];
-    f16x2 low[kGroups], high[kGroups];
-    f16x8 a[2][2], b[2];  // codes of a run and the next; columns of the next step
-    float d[3];
-    auto unpack = [&](int r, int p) {
-        // after the swap the lower half holds dword 0 (2) of the pair's first run and
-        // the upper half dword 1 (3); the other register the same of the second run
-        uint32_t *x = w[r / 2];
-        if ((r & 1) == 0) {
-            auto y = __builtin_amdgcn_permlane32_swap(x[2 * p], x[2 * p + 1], false, false);
-            x[2 * p] = y[0], x[2 * p + 1] = y[1];
-        }
-        a[r & 1][p] = codes_of(x[2 * p + (r & 1)], low[r / kGroupRuns], high[r / kGroupRuns]);
-    };
-    auto scales_of = [&](int group) {
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-            const float4 x =
-                *reinterpret_cast<const float4 *>(&ss[wave][group][8 * q + 4 * half]);
-            sv[4 * q] = x.x, sv[4 * q + 1] = x.y, sv[4 * q + 2] = x.z, sv[4 * q + 3] = x.w;
+            for (int j = 0; j < 2; j++) {
+                const u32x2 x = *reinterpret_cast<const u32x2 *>(
+                    &kept_scales[wave][at / kKept & 1][at % kKept][16 * j + 4 * h]);
+                sv[i][j][0] = f16_bits_to_f32(x[0] & 0xffff), sv[i][j][1] = f16_bits_to_f32(x[0] >> 16);
+                sv[i][j][2] = f16_bits_to_f32(x[1] & 0xffff), sv[i][j][3] = f16_bits_to_f32(x[1] >> 16);
+            }
         }
-    };
-    stage(0, 0);
-    fetch(0);
-    for (int chunk = 0; chunk < chunks; chunk++) {
-        const int buf = chunk & 1;
-        __syncthreads();
-        auto read = [&](int s) {  // a step's columns
-            const int r = s / NT, t = s % NT;
-            const char *op = ops[buf] + t * kOps + r * kOperand + lane * 16;
-            b[0] = *reinterpret_cast<const f16x8 *>(op);
-            b[1] = *reinterpret_cast<const f16x8 *>(op + 1024);
-            d[s % 3] = ds[buf][t * kDs + r * kTileCols + (lane & 31)];
-        };
-        read(0);
+        fetch(after);
+        load(after, 0);
 #pragma unroll
-        for (int i = 0; i < 2; i++)
-            w[i][0] = next[i].x, w[i][1] = next[i].y, w[i][2] = next[i].z, w[i][3] = next[i].w;
-#pragma unroll
-        for (int i = 0; i < kGroups; i++) {
-            // scales go through LDS to the rows that a lane's results are of
-            if (half == 0)
-                ss[wave][i][lane] = f16_bits_to_f32(next_scale[i]);
-            const _Float16 z = (_Float16)(float)next_zero[i];
-            low[i] = f16x2{(_Float16)-1032.0f, (_Float16)-1032.0f} - f16x2{z, z};
-            high[i] = f16x2{(_Float16)-72.0f, (_Float16)-72.0f} - f16x2{z, z};
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (chunk + 1 < chunks) {
-            stage(chunk + 1, buf ^ 1);
-            fetch(chunk + 1);
-        }
-        if constexpr (SH == 0)
-            scales_of(0);
-        unpack(0, 0);
-        unpack(0, 1);
-        v[0] = f32x16{};
-        v[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[0][0], b[0], v[0], 0, 0, 0);
-        v[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[0][1], b[1], v[0], 0, 0, 0);
-        read(1);
+        for (int m = 0; m < 4; m++)
+            v[0][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0][m >> 1], b[0][m & 1], f32x4{}, 0,
+                                                            0, 0);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int s = 0; s < kSteps; s++) {
-            const int r = s / NT, t = s % NT, u = s + 1, ur = u / NT;
-            auto sums = [&](int from) {
+            const int t = s / kChunkRuns, r = s % kChunkRuns, u = s + 1;
+            if (s == kSteps / 2) {
+                store(buf ^ 1, 0);
+                load(after, 1);
+            }
+            if (t == NT - 1 && r == 0) {
+                exchange(next[0]);
+                exchange(next[1]);
+                zeros_of(after);
+            }
 #pragma unroll
-                for (int i = from; i < from + 8; i++) {
-                    const float x = v[s & 1][i];
+            for (int m = 0; m < 4; m++) {
+                if (u < kSteps)
+                    v[u & 1][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                        a[u % kChunkRuns][m >> 1], b[u & 1][m & 1], f32x4{}, 0, 0, 0);
+                if (m == 0 && s + 2 < kSteps)
+                    read(s + 2);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float x = v[s & 1][m][i], e = d[s % 3][m & 1];
+                    const float scale = sv[r / kGroupRuns][m >> 1][i];
                     if constexpr (SH == 0) {
-                        acc[t][i] = fmaf(sv[i], x * d[s % 3], acc[t][i]);
-                    } else if (r % kGroupRuns) {
-                        part[t][i] = fmaf(x, d[s % 3], part[t][i]);
-                    } else {  // a group begins: the one before is done
-                        acc[t][i] = fmaf(sv[i], part[t][i], acc[t][i]);
-                        part[t][i] = x * d[s % 3];
+                        acc[t][m][i] = fmaf(scale, x * e, acc[t][m][i]);
+                    } else {
+                        part[m][i] = r % kGroupRuns ? fmaf(x, e, part[m][i]) : x * e;
+                        if ((r + 1) % kGroupRuns == 0)
+                            acc[t][m][i] = fmaf(scale, part[m][i], acc[t][m][i]);
                     }
                 }
-            };
-            // the next run's codes, half of them at a time, before its first step's products
-            if (NT == 1 && r + 1 < kChunkRuns) {
-                unpack(r + 1, 0);
-                unpack(r + 1, 1);
+                // the next chunk's run in the place of one whose products are all issued
+                if (t == NT - 1 && m == 3)
+                    unpack(r);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            if (u < kSteps) {
-                v[u & 1] = f32x16{};
-                v[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[ur & 1][0], b[0], v[u & 1], 0, 0, 0);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            sums(0);
-            if (NT > 1 && t == NT - 2 && r + 1 < kChunkRuns)
-                unpack(r + 1, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            if (u < kSteps)
-                v[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[ur & 1][1], b[1], v[u & 1], 0, 0, 0);
-            if (s + 2 < kSteps)
-                read(s + 2);
-            __builtin_amdgcn_sched_barrier(0);
-            sums(8);
-            if (NT > 1 && t == NT - 2 && r + 1 < kChunkRuns)
-                unpack(r + 1, 1);
-            if (SH == 0 && t == NT - 1 && r + 1 < kChunkRuns)
-                scales_of(r + 1);
-            if (SH > 0 && t == NT - 1 && (r + 1) % kGroupRuns == 0)
-                scales_of(r / kGroupRuns);
-            __builtin_amdgcn_sched_barrier(0);
         }
-    }
-    if constexpr (SH > 0) {
-#pragma unroll
-        for (int t = 0; t < NT; t++)
-#pragma unroll
-            for (int i = 0; i < 16; i++)
-                acc[t][i] = fmaf(sv[i], part[t][i], acc[t][i]);
+        store(buf ^ 1, 1);
     }
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
-        const int64_t col = (int64_t)(tile0 + t) * kTileCols + (lane & 31);
-        if (col >= g.T)
-            continue;
+    for (int t = 0; t < NT; t++)
 #pragma unroll
-        for (int q = 0; q < 4; q++)
+        for (int m = 0; m < 4; m++) {
+            const int64_t col = (int64_t)(tile0 + t) * kTileCols + 16 * (m & 1) + (lane & 15);
+            if (col >= g.T)
+                continue;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const int64_t n = n0 + 8 * q + 4 * half + i;
+                const int64_t n = n0 + 16 * (m >> 1) + 4 * h + i;
                 if (n < g.m.N)
-                    g.y[col * g.m.N + n] = acc[t][4 * q + i];
+                    g.y[col * g.m.N + n] = acc[t][m][i];
             }
-    }
+        }
 }
 
-template <int NT, int SH>
+template <int NT, int W, int SH>
 int launch_mfma_group(const Q4Args &g, const Laid &l, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((g.m.N + 127) / 128), (unsigned)((l.tiles + NT - 1) / NT));
+    const dim3 grid((unsigned)((g.m.N + 32 * W - 1) / (32 * W)), (unsigned)((l.tiles + NT - 1) / NT));
     if (g.m.zeros)
-        hipLaunchKernelGGL((q4_mfma_kernel<NT, SH, true>), grid, dim3(256), 0, stream, g, l);
+        hipLaunchKernelGGL((q4_mfma_kernel<NT, W, SH, true>), grid, dim3(64 * W), 0, stream, g, l);
     else
-        hipLaunchKernelGGL((q4_mfma_kernel<NT, SH, false>), grid, dim3(256), 0, stream, g, l);
+        hipLaunchKernelGGL((q4_mfma_kernel<NT, W, SH, false>), grid, dim3(64 * W), 0, stream, g, l);
     return check_launch();
 }
 
-template <int NT>
+template <int NT, int W>
 int launch_mfma(const Q4Args &g, const Laid &l, hipStream_t stream)
 {
     hipLaunchKernelGGL(q4_columns_kernel, dim3((unsigned)((l.runs + 7) / 8), (unsigned)l.tiles),
                        dim3(256), 0, stream, g.a, l, g.T, g.nb);
     if (int rc = check_launch())
         return rc;
-    return g.shift == 0   ? launch_mfma_group<NT, 0>(g, l, stream)
-           : g.shift == 1 ? launch_mfma_group<NT, 1>(g, l, stream)
-                          : launch_mfma_group<NT, 2>(g, l, stream);
+    return g.shift == 0   ? launch_mfma_group<NT, W, 0>(g, l, stream)
+           : g.shift == 1 ? launch_mfma_group<NT, W, 1>(g, l, stream)
+                          : launch_mfma_group<NT, W, 2>(g, l, stream);
 }
 
-constexpr int kDotCols = 8;       // the most columns without the matrix cores
+// ---- a few columns: the matrix cores, all columns in LDS -------------------------------
+//
+// Up to 32 columns that fit in LDS stay there, as int8 operands, and every wave goes through
+// rows by itself, without a barrier between its loads: what counts is bytes on their way.
+// A code in the high half of its byte is 16 times the code, so an operand takes three
+// instructions; a zero's share goes into the products' start, -16 * zero * sum of q. The
+// products' rows are columns of the call and their columns rows of the matrix: a lane's
+// results are all of one row, whose scales and zeros it loads itself.
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+// LDS of a run's 16 columns: q [64][8 bytes], d [16] fp16, sums of q [16] int16
+constexpr int kFewRun = 512 + 32 + 32;
+
+size_t few_lds(int ct, int nb) { return (size_t)((nb + 3) / 4 * 4) * ct * kFewRun; }
+
+// W waves of 16 rows, CT tiles of 16 columns, groups of 32 << SH. A workgroup has an
+// even share of the row tiles, one a wave at a time; where fewer than half its waves have
+// one left, or there are few rows at all, waves share a tile, a part of the runs each.
+template <int CT, int W, int SH, bool Z>
+__global__ __launch_bounds__(64 * W) void q4_few_kernel(const Q4Args g, int tiles)
+{
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr int kGroupRuns = 1 << SH;
+    constexpr int kGroups = 4 / kGroupRuns;  // of a chunk of four runs
+    constexpr int kAhead = 3;                // chunks of codes on their way
+    constexpr int kPeriod = 4 / kGroups;     // chunks of four groups
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int c = lane & 15, h = lane >> 4;
+    const int chunks = (g.nb + 3) / 4, groups = g.nb >> SH;
+    int tile = (int)((int64_t)tiles * blockIdx.x / gridDim.x);
+    const int tile_end = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+
+    // The waves' next tiles: log2 of the waves a tile has, this wave's part.
+    int ks, first, end;
+    __amdgpu_buffer_rsrc_t codes;
+    int64_t n0;
+    u32x4 next[kAhead];
+    auto fetch = [&](int slot, int chunk) {  // lanes of group h: run h
+        next[slot] =
+            __builtin_amdgcn_raw_buffer_load_b128(codes, (c * g.nb + h) * 16, chunk * 64, 0);
+    };
+    // Scales and zeros of a tile's rows, which each cost the loads' path as much as 256 bytes
+    // of codes: a lane has four groups of row c at once (none behind the row's end), and
+    // those of group h the h-th four of sixteen. In use: four groups, the same in all.
+    uint64_t scales, scales_held, scales_next;
+    uint32_t zeros, zeros_held, zeros_next;
+    auto gather = [&](int sixteen) {
+        const int64_t n = n0 + c;
+        const int at = 16 * sixteen + 4 * h;
+        scales_next = 0;
+        zeros_next = 0;
+        if (n >= g.m.N)
+            return;
+        const uint16_t *sp = static_cast<const uint16_t *>(g.m.scales) + n * groups + at;
+        const int8_t *zp = g.m.zeros + n * groups + at;
+        if (at + 4 <= groups) {
+            __builtin_memcpy(&scales_next, sp, 8);
+            if constexpr (Z)
+                __builtin_memcpy(&zeros_next, zp, 4);
+        } else {
+            for (int k = 0; at + k < groups; k++) {
+                scales_next |= (uint64_t)sp[k] << (16 * k);
+                if constexpr (Z)
+                    zeros_next |= (uint32_t)(uint8_t)zp[k] << (8 * k);
+            }
+        }
+    };
+    auto take = [&](int period, bool fresh) {
+        if ((period & 3) == 0 || fresh) {
+            scales_held = scales_next;
+            zeros_held = zeros_next;
+            gather((period >> 2) + 1);
+        }
+        const int from = 4 * (16 * (period & 3) + c);
+        const uint32_t lo = __builtin_amdgcn_ds_bpermute(from, (int)(uint32_t)scales_held);
+        const uint32_t hi = __builtin_amdgcn_ds_bpermute(from, (int)(uint32_t)(scales_held >> 32));
+        scales = (uint64_t)hi << 32 | lo;
+        if constexpr (Z)
+            zeros = __builtin_amdgcn_ds_bpermute(from, (int)zeros_held);
+    };
+    auto begin = [&]() {  // the next tiles' first loads
+        const int left = tile_end - tile;
+        ks = 0;
+        while ((2 << ks) <= W && (left << (ks + 1)) <= W && (chunks >> ks) >= 4)
+            ks++;
+        const int mine = tile + (wave >> ks), part = wave & ((1 << ks) - 1);
+        // whole periods of four groups
+        const int periods = (chunks + kPeriod - 1) / kPeriod;
+        first = (periods * part >> ks) * kPeriod;
+        end = (periods * (part + 1) >> ks) * kPeriod;
+        end = end < chunks ? end : chunks;
+        n0 = (int64_t)mine * 16;
+        int64_t rows = mine < tile_end ? g.m.N - n0 : 0;
+        rows = rows < 16 ? rows : 16;
+        codes = make_rsrc(static_cast<const char *>(g.m.codes) + (rows ? n0 : 0) * g.nb * 16,
+                          (uint64_t)rows * g.nb * 16);
+        if (rows == 0)
+            n0 = g.m.N;  // (a wave without a tile goes along)
+#pragma unroll
+        for (int i = 0; i < kAhead; i++)
+            fetch(i, first + i);
+        gather(first / kPeriod / 4);
+    };
+    begin();
+
+    // the columns: a thread a column's run
+    for (int i = threadIdx.x; i < chunks * 4 * CT * 16; i += 64 * W) {
+        const int col = i & 15, run = i >> 4 & 3, t = (i >> 6) % CT, b = i / (64 * CT) * 4 + run;
+        uint32_t q[8] = {}, d = 0;
+        int sum = 0;
+        if (16 * t + col < g.T && b < g.nb) {
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(
+                g.a + ((int64_t)(16 * t + col) * g.nb + b) * kQ81BlockBytes);
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                q[k] = p[k];
+                sum = sdot4(q[k], 0x01010101u, sum);
+            }
+            d = p[8];
+        }
+        char *to = lds + (b * CT + t) * kFewRun;
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            *reinterpret_cast<u32x2 *>(to + (k * 16 + col) * 8) = u32x2{q[k], q[k + 4]};
+        *reinterpret_cast<uint16_t *>(to + 512 + col * 2) = (uint16_t)d;
+        *reinterpret_cast<int16_t *>(to + 544 + col * 2) = (int16_t)sum;
+    }
+    __syncthreads();
+
+    for (;;) {
+        float acc[CT][4] = {}, sums[CT][4];
+        const int shared = ks;
+        const int64_t n1 = n0;
+        for (int at = first; at < end; at += kAhead) {
+#pragma unroll
+            for (int slot = 0; slot < kAhead; slot++) {
+                const int chunk = at + slot;
+                if (chunk >= end)
+                    break;
+                if (chunk % kPeriod == 0)
+                    take(chunk / kPeriod, chunk == first);
+                // exchanged, register r holds dword h of run r
+                auto x = __builtin_amdgcn_permlane32_swap(next[slot][0], next[slot][2], false, false);
+                auto y = __builtin_amdgcn_permlane32_swap(next[slot][1], next[slot][3], false, false);
+                auto p = __builtin_amdgcn_permlane16_swap(x[0], y[0], false, false);
+                auto q = __builtin_amdgcn_permlane16_swap(x[1], y[1], false, false);
+                const uint32_t w[4] = {p[0], p[1], q[0], q[1]};
+                fetch(slot, chunk + kAhead);  // (behind the part: not used)
+#pragma unroll
+                for (int j = 0; j < kGroups; j++) {
+                    const int at4 = kGroups == 4 ? j : (chunk * kGroups + j) & 3;
+                    const float scale =
+                        f16_bits_to_f32((uint32_t)(scales >> (16 * at4)) & 0xffffu) * 0.0625f;
+                    const int zero = Z ? -16 * (int)(int8_t)(zeros >> (8 * at4)) : 0;
+#pragma unroll
+                    for (int r = j * kGroupRuns; r < (j + 1) * kGroupRuns; r++) {
+                        const uint32_t lo = (w[r] << 4) & 0xf0f0f0f0u, hi = w[r] & 0xf0f0f0f0u;
+#pragma unroll
+                        for (int t = 0; t < CT; t++) {
+                            const char *from = lds + ((chunk * 4 + r) * CT + t) * kFewRun;
+                            const long q8 = *reinterpret_cast<const long *>(from + lane * 8);
+                            const f16x4 d = *reinterpret_cast<const f16x4 *>(from + 512 + h * 8);
+                            i32x4 v = {0, 0, 0, 0};
+                            if constexpr (Z) {
+                                const i16x4 of_q = *reinterpret_cast<const i16x4 *>(from + 544 + h * 8);
+#pragma unroll
+                                for (int k = 0; k < 4; k++)
+                                    v[k] = __mul24(zero, (int)of_q[k]);
+                            }
+                            v = __builtin_amdgcn_mfma_i32_16x16x32_i8(
+                                q8, (long)((uint64_t)hi << 32 | lo), v, 0, 0, 0);
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {
+                                const float s = (float)v[k], e = (float)d[k];
+                                sums[t][k] = r % kGroupRuns ? fmaf(s, e, sums[t][k]) : s * e;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < CT; t++)
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            acc[t][k] = fmaf(scale, sums[t][k], acc[t][k]);
+                }
+            }
+        }
+        tile += W >> shared;
+        const bool again = tile < tile_end;  // (the same for all waves; never after a shared tile)
+        if (again)
+            begin();
+        if (shared) {  // the parts' sums, in order; the columns are done with
+            __syncthreads();
+            float *const mine = reinterpret_cast<float *>(lds) + wave * CT * 4 * 64 + lane;
+#pragma unroll
+            for (int i = 0; i < CT * 4; i++)
+                mine[i * 64] = acc[i / 4][i % 4];
+            __syncthreads();
+            if (wave & ((1 << shared) - 1))
+                return;
+            for (int o = 1; o < 1 << shared; o++)
+#pragma unroll
+                for (int i = 0; i < CT * 4; i++)
+                    acc[i / 4][i % 4] += mine[(o * CT * 4 + i) * 64];
+        }
+        const int64_t n = n1 + c;
+#pragma unroll
+        for (int t = 0; t < CT; t++)
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const int col = 16 * t + 4 * h + k;
+                if (n < g.m.N && col < g.T)
+                    g.y[(int64_t)col * g.m.N + n] = acc[t][k];
+            }
+        if (!again)
+            return;
+    }
+}
+
+template <int CT, int W, int SH>
+int launch_few_group(const Q4Args &g, hipStream_t stream)
+{
+    const int tiles = (int)((g.m.N + 15) / 16);
+    const int grid = std::min(tiles, compute_units());
+    const size_t bytes = std::max(few_lds(CT, g.nb), (size_t)W * 64 * CT * 16);
+    auto run = [&](auto *kernel) {
+        allow_dynamic_lds(reinterpret_cast<const void *>(kernel), bytes);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * W), bytes, stream, g, tiles);
+        return check_launch();
+    };
+    return g.m.zeros ? run(q4_few_kernel<CT, W, SH, true>) : run(q4_few_kernel<CT, W, SH, false>);
+}
+
+template <int CT, int W>
+int launch_few_waves(const Q4Args &g, hipStream_t stream)
+{
+    return g.shift == 0   ? launch_few_group<CT, W, 0>(g, stream)
+           : g.shift == 1 ? launch_few_group<CT, W, 1>(g, stream)
+                          : launch_few_group<CT, W, 2>(g, stream);
+}
+
+// Sixteen waves where each has a tile of its own: 55 us against 64 for 100003 rows of 4096
+// and 9 columns; for 4096 rows eight are faster (7.3 against 9.0).
+template <int CT>
+int launch_few(const Q4Args &g, hipStream_t stream)
+{
+    return g.m.N >= (int64_t)compute_units() * 256 ? launch_few_waves<CT, 16>(g, stream)
+                                                   : launch_few_waves<CT, 8>(g, stream);
+}
+
+bool few_supported(int64_t T, int nb)
+{
+    return T <= 32 && few_lds(T <= 16 ? 1 : 2, nb) <= kLdsMax;
+}
+
+constexpr int kDotCols = 2;       // the most columns without the matrix cores
 constexpr int64_t kMostCols = 8192;  // laid out at once
 
 }  // namespace
 
 size_t mm_q4_workspace(int64_t T, int64_t K)
 {
-    return T <= kDotCols ? 0 : laid_out_bytes(std::min(T, kMostCols), K / 32);
+    return T <= kDotCols || few_supported(T, (int)(K / 32)) ? 0 : laid_out_bytes(std::min(T, kMostCols), K / 32);
 }
 
 int launch_mm_q4(const bqm_q4_matrix *m, const void *a, float *y, int64_t T, void *workspace,
@@ -490,20 +802,18 @@ int launch_mm_q4(const bqm_q4_matrix *m, const void *a, float *y, int64_t T, voi
                 m->group == 32 ? 0 : m->group == 64 ? 1 : 2};
     if (T == 1)
         return launch_dot<1, 4>(g, stream);
-    if (T == 2)
-        return launch_dot<2, 4>(g, stream);
-    if (T <= 4)
-        return launch_dot<4, 4>(g, stream);
     if (T <= kDotCols)
-        return launch_dot<8, 4>(g, stream);
+        return launch_dot<2, 4>(g, stream);
+    if (few_supported(T, g.nb))
+        return T <= 16 ? launch_few<1>(g, stream) : launch_few<2>(g, stream);
     for (int64_t t = 0; t < T; t += kMostCols) {
         g.T = std::min(T - t, kMostCols);
         g.a = static_cast<const uint8_t *>(a) + t * g.nb * kQ81BlockBytes;
         g.y = y + t * m->N;
         const Laid l = laid_out(workspace, g.T, g.nb);
-        const int rc = g.T <= 32 ? launch_mfma<1>(g, l, stream)
-                       : g.T <= 64 ? launch_mfma<2>(g, l, stream)
-                                   : launch_mfma<4>(g, l, stream);
+        const int rc = g.T <= 32 ? launch_mfma<1, 4>(g, l, stream)
+                       : g.T <= 64 ? launch_mfma<2, 4>(g, l, stream)
+                                   : launch_mfma<4, 4>(g, l, stream);
         if (rc)
             return rc;
     }
