@@ -154,26 +154,45 @@ constexpr int kOperand = 2048;   // bytes of one tile's run: two operands
 
 // Workspace: operands [column tile][run][half of the columns][64][16 bytes], then d [column tile][run][32]
 // fp32; runs padded to whole chunks, columns to whole tiles, with zeros.
+// Where there are few tiles, the runs are cut into parts, whose sums [part][T][N] come after.
 struct Laid {
     char *ops;
-    float *d;
-    int runs, tiles;
+    float *d, *sums;
+    int runs, tiles, parts;
 };
 
-Laid laid_out(void *workspace, int64_t T, int nb)
+// Parts for N rows and T columns: as many as fill the device's 512 places, of four chunks
+// (512 values) at least. 4096 x 4096 and 64 columns: 22 us in 16 parts, 41 in one; two parts
+// cost more than they give (14336 x 4096, 256 columns: 76 us in two, 70 in one).
+int parts_of(int64_t N, int64_t T, int64_t nb)
 {
-    Laid l;
-    l.runs = (nb + kChunkRuns - 1) / kChunkRuns * kChunkRuns;
-    l.tiles = (int)((T + kTileCols - 1) / kTileCols);
-    l.ops = static_cast<char *>(workspace);
-    l.d = reinterpret_cast<float *>(l.ops + (size_t)l.tiles * l.runs * kOperand);
-    return l;
+    const int64_t tiles = (T + kTileCols - 1) / kTileCols;
+    const int64_t groups = (N + 127) / 128 * (tiles <= 2 ? 1 : (tiles + 3) / 4);
+    const int64_t chunks = (nb + kChunkRuns - 1) / kChunkRuns;
+    const int parts = (int)std::min<int64_t>({512 / groups, chunks / 4, 16});
+    return parts > 2 ? parts : 1;
 }
 
-size_t laid_out_bytes(int64_t T, int64_t nb)
+size_t padded_runs(int64_t nb) { return (nb + kChunkRuns - 1) / kChunkRuns * kChunkRuns; }
+
+size_t laid_out_bytes(int64_t N, int64_t T, int64_t nb)
 {
-    const size_t runs = (nb + kChunkRuns - 1) / kChunkRuns * kChunkRuns;
-    return (size_t)((T + kTileCols - 1) / kTileCols) * runs * (kOperand + kTileCols * 4);
+    const int64_t parts = parts_of(N, T, nb);
+    return (size_t)((T + kTileCols - 1) / kTileCols) * padded_runs(nb) *
+               (kOperand + kTileCols * 4) +
+           (parts > 1 ? (size_t)parts * T * N * 4 : 0);
+}
+
+Laid laid_out(void *workspace, int64_t N, int64_t T, int nb)
+{
+    Laid l;
+    l.runs = (int)padded_runs(nb);
+    l.tiles = (int)((T + kTileCols - 1) / kTileCols);
+    l.parts = parts_of(N, T, nb);
+    l.ops = static_cast<char *>(workspace);
+    l.d = reinterpret_cast<float *>(l.ops + (size_t)l.tiles * l.runs * kOperand);
+    l.sums = l.d + (size_t)l.tiles * l.runs * kTileCols;
+    return l;
 }
 
 __device__ __forceinline__ uint32_t as_u32(f16x2 v) { return __builtin_bit_cast(uint32_t, v); }
@@ -254,10 +273,11 @@ __device__ __forceinline__ f16x8 codes_of(uint32_t w, f16x2 low, f16x2 high)
 // columns each time: kKept groups at once.
 constexpr int kKept = 8;
 
-template <int NT, int W, int SH, bool Z>
-__global__ __launch_bounds__(64 * W, 2) void q4_mfma_kernel(const Q4Args g, const Laid l)
+template <int NT, int SH, bool Z>
+__global__ __launch_bounds__(256, 2) void q4_mfma_kernel(const Q4Args g, const Laid l)
 {
     // a chunk's operands and d: [tile][run]; two of each
+    constexpr int W = 4;  // waves
     constexpr int kOps = kChunkRuns * kOperand;
     constexpr int kDs = kChunkRuns * kTileCols;
     constexpr int kGroupRuns = 1 << SH;
@@ -397,23 +417,26 @@ __global__ __launch_bounds__(64 * W, 2) void q4_mfma_kernel(const Q4Args g, cons
                                f16x2{(_Float16)-72.0f, (_Float16)-72.0f} - f16x2{z, z});
         }
     };
-    fetch(0);
-    gather(0);
-    load(0, 0);
-    keep(0);
-    gather(1);
+    const int begin = (int)((int64_t)chunks * blockIdx.z / gridDim.z);
+    const int end = (int)((int64_t)chunks * (blockIdx.z + 1) / gridDim.z);
+    constexpr int kPeriod = kKept / kGroups;  // chunks
+    fetch(begin);
+    gather(begin / kPeriod);
+    load(begin, 0);
+    keep(begin / kPeriod);
+    gather(begin / kPeriod + 1);
     store(0, 0);
-    load(0, 1);
+    load(begin, 1);
     store(0, 1);
-    zeros_of(0);
+    zeros_of(begin);
     exchange(next[0]);
     exchange(next[1]);
 #pragma unroll
     for (int r = 0; r < kChunkRuns; r++)
         unpack(r);
-    for (int chunk = 0; chunk < chunks; chunk++) {
-        const int buf = chunk & 1;
-        const int after = chunk + 1 < chunks ? chunk + 1 : chunk;  // (the last one again)
+    for (int chunk = begin; chunk < end; chunk++) {
+        const int buf = (chunk - begin) & 1;
+        const int after = chunk + 1 < end ? chunk + 1 : chunk;  // (the last one again)
         __syncthreads();
         auto read = [&](int s) {  // a step's columns
             const int t = s / kChunkRuns, r = s % kChunkRuns;
@@ -426,7 +449,6 @@ __global__ __launch_bounds__(64 * W, 2) void q4_mfma_kernel(const Q4Args g, cons
         };
         read(0);
         read(1);
-        constexpr int kPeriod = kKept / kGroups;  // chunks
         if (chunk % kPeriod == kPeriod - 1) {
             keep(chunk / kPeriod + 1);
             gather(chunk / kPeriod + 2);
@@ -489,6 +511,7 @@ __global__ __launch_bounds__(64 * W, 2) void q4_mfma_kernel(const Q4Args g, cons
         }
         store(buf ^ 1, 1);
     }
+    float *const y = gridDim.z > 1 ? l.sums + (size_t)blockIdx.z * g.T * g.m.N : g.y;
 #pragma unroll
     for (int t = 0; t < NT; t++)
 #pragma unroll
@@ -500,32 +523,53 @@ __global__ __launch_bounds__(64 * W, 2) void q4_mfma_kernel(const Q4Args g, cons
             for (int i = 0; i < 4; i++) {
                 const int64_t n = n0 + 16 * (m >> 1) + 4 * h + i;
                 if (n < g.m.N)
-                    g.y[col * g.m.N + n] = acc[t][m][i];
+                    y[col * g.m.N + n] = acc[t][m][i];
             }
         }
 }
 
-template <int NT, int W, int SH>
+// y = the parts' sums, in their order.
+__global__ __launch_bounds__(256) void q4_parts_kernel(const float *__restrict__ sums,
+                                                       float *__restrict__ y, int64_t n, int parts)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n)
+        return;
+    float v = sums[i];
+    for (int p = 1; p < parts; p++)
+        v += sums[p * n + i];
+    y[i] = v;
+}
+
+template <int NT, int SH>
 int launch_mfma_group(const Q4Args &g, const Laid &l, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((g.m.N + 32 * W - 1) / (32 * W)), (unsigned)((l.tiles + NT - 1) / NT));
+    const dim3 grid((unsigned)((g.m.N + 127) / 128), (unsigned)((l.tiles + NT - 1) / NT),
+                    (unsigned)l.parts);
     if (g.m.zeros)
-        hipLaunchKernelGGL((q4_mfma_kernel<NT, W, SH, true>), grid, dim3(64 * W), 0, stream, g, l);
+        hipLaunchKernelGGL((q4_mfma_kernel<NT, SH, true>), grid, dim3(256), 0, stream, g, l);
     else
-        hipLaunchKernelGGL((q4_mfma_kernel<NT, W, SH, false>), grid, dim3(64 * W), 0, stream, g, l);
+        hipLaunchKernelGGL((q4_mfma_kernel<NT, SH, false>), grid, dim3(256), 0, stream, g, l);
     return check_launch();
 }
 
-template <int NT, int W>
+template <int NT>
 int launch_mfma(const Q4Args &g, const Laid &l, hipStream_t stream)
 {
     hipLaunchKernelGGL(q4_columns_kernel, dim3((unsigned)((l.runs + 7) / 8), (unsigned)l.tiles),
                        dim3(256), 0, stream, g.a, l, g.T, g.nb);
     if (int rc = check_launch())
         return rc;
-    return g.shift == 0   ? launch_mfma_group<NT, W, 0>(g, l, stream)
-           : g.shift == 1 ? launch_mfma_group<NT, W, 1>(g, l, stream)
-                          : launch_mfma_group<NT, W, 2>(g, l, stream);
+    if (int rc = g.shift == 0   ? launch_mfma_group<NT, 0>(g, l, stream)
+                 : g.shift == 1 ? launch_mfma_group<NT, 1>(g, l, stream)
+                                : launch_mfma_group<NT, 2>(g, l, stream))
+        return rc;
+    if (l.parts == 1)
+        return BQM_OK;
+    const int64_t n = g.T * g.m.N;
+    hipLaunchKernelGGL(q4_parts_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream,
+                       l.sums, g.y, n, l.parts);
+    return check_launch();
 }
 
 // ---- a few columns: the matrix cores, all columns in LDS -------------------------------
@@ -790,9 +834,9 @@ constexpr int64_t kMostCols = 8192;  // laid out at once
 
 }  // namespace
 
-size_t mm_q4_workspace(int64_t T, int64_t K)
+size_t mm_q4_workspace(int64_t N, int64_t T, int64_t K)
 {
-    return T <= kDotCols || few_supported(T, (int)(K / 32)) ? 0 : laid_out_bytes(std::min(T, kMostCols), K / 32);
+    return T <= kDotCols || few_supported(T, (int)(K / 32)) ? 0 : laid_out_bytes(N, std::min(T, kMostCols), K / 32);
 }
 
 int launch_mm_q4(const bqm_q4_matrix *m, const void *a, float *y, int64_t T, void *workspace,
@@ -810,10 +854,10 @@ int launch_mm_q4(const bqm_q4_matrix *m, const void *a, float *y, int64_t T, voi
         g.T = std::min(T - t, kMostCols);
         g.a = static_cast<const uint8_t *>(a) + t * g.nb * kQ81BlockBytes;
         g.y = y + t * m->N;
-        const Laid l = laid_out(workspace, g.T, g.nb);
-        const int rc = g.T <= 32 ? launch_mfma<1, 4>(g, l, stream)
-                       : g.T <= 64 ? launch_mfma<2, 4>(g, l, stream)
-                                   : launch_mfma<4, 4>(g, l, stream);
+        const Laid l = laid_out(workspace, m->N, g.T, g.nb);
+        const int rc = g.T <= 32 ? launch_mfma<1>(g, l, stream)
+                       : g.T <= 64 ? launch_mfma<2>(g, l, stream)
+                                   : launch_mfma<4>(g, l, stream);
         if (rc)
             return rc;
     }
