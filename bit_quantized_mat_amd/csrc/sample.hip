@@ -12,6 +12,13 @@
 //
 // Weights are whole numbers of 2^-44: sums are exact, atomics in any order give the
 // same bits.
+//
+// A row is a workgroup's. Where there are fewer rows than would fill the device, the
+// two passes over all of a row (its largest logit; its bins) are shared by several
+// workgroups each, launches of their own before it.
+#include <algorithm>
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -21,11 +28,21 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 1024;      // of a row's workgroup
+constexpr int kPartThreads = 512;   // of a part's
 constexpr int kBins = 2048;
+constexpr int kPartsMax = 64;
 constexpr int kFew = 2048;  // tokens that are sorted in LDS
 constexpr int kSteps = 1024;  // of the table of powers, in a factor of 2
 constexpr double kOne = 17592186044416.0;  // 2^44
+
+// A row's part of the workspace: what its parts add up.
+struct RowSums {
+    u64 weight[kBins];
+    uint32_t count[kBins];
+    u64 kept;  // weights that min_p leaves
+    u64 best[kPartsMax];
+};
 
 struct SampleArgs {
     const void *logits;
@@ -35,28 +52,64 @@ struct SampleArgs {
     const float *top_p, *min_p, *u;
     int32_t *tokens;
     float *logprobs;
-    int V;
+    RowSums *rows;  // where rows are shared
+    int V, parts;
 };
 
 struct Lds {
     double power[kSteps];      // 2^(i / kSteps)
     u64 weight[kBins + 1];     // sums of the bins before each
-    uint32_t count[kBins + 1];
+    uint32_t count[kBins + 1];  // (or bounds of them, where top_k does not ask)
     u64 few[kFew];             // key << 32 | ~id, sorted downwards
     u64 upto[kFew];            // weights of those up to and with each
     u64 part[16];
-    uint32_t part_n[16];
     u64 found_w;               // an answer: the weights up to and with the token,
     uint32_t found_id;         // the token,
     int found_bin;
     uint32_t n, key_lo, key_hi;
 };
 
-template <class V>
-__device__ __forceinline__ float logit(const V *x, int i)
+struct PartLds {
+    double power[kSteps];
+    u64 weight[kBins];
+    uint32_t count[kBins];
+    u64 kept;
+};
+
+// f(i, value) for the logits from .. to - 1 of a row as they are, dealt to n threads, each
+// one's in ascending order: 16 bytes at a time, kDeep of them on their way.
+template <int kDeep, class V, class F>
+__device__ __forceinline__ void each(const V *x, int from, int to, int n, F f)
 {
-    const float v = (float)x[i] + 0.0f;  // (-0 is 0)
-    return v == v ? v : -__builtin_inff();
+    constexpr int kPer = 16 / sizeof(V);
+    auto one = [&](int i, V v) { f(i, (float)v); };
+    const int odd = (int)((16 - (reinterpret_cast<uintptr_t>(x + from) & 15)) & 15) / (int)sizeof(V);
+    const int head = odd < to - from ? odd : to - from;
+    const int tid = threadIdx.x;
+    if (tid < head)
+        one(from + tid, x[from + tid]);
+    const int first = from + head, pieces = (to - first) / kPer;
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(x + first);
+    auto piece = [&](int i, const u32x4 &raw) {
+        V v[kPer];
+        __builtin_memcpy(v, &raw, 16);
+#pragma unroll
+        for (int k = 0; k < kPer; k++)
+            one(first + i * kPer + k, v[k]);
+    };
+    for (int i = tid; i < pieces; i += kDeep * n) {
+        u32x4 raw[kDeep];
+#pragma unroll
+        for (int k = 0; k < kDeep; k++)
+            raw[k] = p[i + k * n < pieces ? i + k * n : i];
+#pragma unroll
+        for (int k = 0; k < kDeep; k++)
+            if (i + k * n < pieces)
+                piece(i + k * n, raw[k]);
+    }
+    const int tail = first + pieces * kPer;
+    if (tid < to - tail)
+        one(tail + tid, x[tail + tid]);
 }
 
 // Ascending with the value.
@@ -71,20 +124,72 @@ __device__ __forceinline__ float value_of(uint32_t key)
     return __uint_as_float((key >> 31) ? key & 0x7fffffffu : ~key);
 }
 
+__device__ __forceinline__ u64 largest(u64 a, u64 b) { return a > b ? a : b; }
+
+// The largest of a thread's logits, the first of equal ones; NaN is none.
+struct Top {
+    float v = -__builtin_inff();
+    int i = 0x7fffffff;
+
+    __device__ __forceinline__ void see(int at, float u)
+    {
+        if (u > v) {
+            v = u;
+            i = at;
+        }
+    }
+    __device__ __forceinline__ u64 packed() const
+    {
+        return (u64)key_of(v + 0.0f) << 32 | (uint32_t)~i;  // (-0 is 0)
+    }
+};
+
+__device__ __forceinline__ u64 wave_largest(u64 v)
+{
+    for (int m = 32; m; m >>= 1)
+        v = largest(v, __shfl_xor(v, m, 64));
+    return v;
+}
+
+// A row's settings.
+struct Settings {
+    float heat, p, floor;
+    int k;
+    bool first;  // the first token is taken (written so that NaN settings do, too)
+
+    __device__ __forceinline__ Settings(const SampleArgs &g, int t)
+        : heat(g.temperature ? g.temperature[t] : 1.0f), p(g.top_p ? g.top_p[t] : 1.0f),
+          floor(g.min_p ? g.min_p[t] : 0.0f), k(g.top_k ? g.top_k[t] : 0)
+    {
+        first = !(heat > 0.0f) || k == 1 || !(p > 0.0f) || !(floor <= 1.0f);
+    }
+};
+
+__device__ __forceinline__ void fill_powers(double *power, int n)
+{
+    for (int i = threadIdx.x; i < kSteps; i += n)
+        power[i] = exp2((double)i / kSteps);
+}
+
 // A logit's weight, a whole number of 2^-44, and bin.
 struct Weights {
     const double *power;
     double top, c;  // the largest logit; kSteps * log2(e) / temperature
     bool infinite;
 
-    __device__ __forceinline__ u64 of(float v, int &bin) const
+    __device__ __forceinline__ void set(const double *table, float largest_logit, float heat)
     {
-        bin = 0;
-        if (infinite)
-            return v == __builtin_inff() ? (u64)kOne : 0;
-        const double y = ((double)v - top) * c;
-        if (!(y > -46.0 * kSteps))
-            return 0;
+        power = table;
+        top = largest_logit;
+        infinite = largest_logit == __builtin_inff();
+        c = kSteps * 1.4426950408889634 / (double)heat;
+    }
+
+    // (of logits of which none is +infinity)
+    __device__ __forceinline__ u64 of_finite(float v, int &bin) const
+    {
+        // what is further down, -infinity, NaN and what -infinity makes NaN round to nothing
+        const double y = fmax(((double)v - top) * c, -46.0 * kSteps);
         const double f = floor(y);
         const int k = (int)f;
         bin = (-k) >> 5;
@@ -98,7 +203,76 @@ struct Weights {
         w = ldexp(w, 44 + (k >> 10)) + 4503599627370496.0;
         return (u64)__double_as_longlong(w) & 0xfffffffffffffull;
     }
+
+    __device__ __forceinline__ u64 of(float v, int &bin) const
+    {
+        if (!infinite)
+            return of_finite(v, bin);
+        bin = 0;
+        return v == __builtin_inff() ? (u64)kOne : 0;
+    }
+
+    // No logit below this has a bin of at most `bin`; none above that, one of at least `bin`.
+    __device__ __forceinline__ float least(int bin) const
+    {
+        if (infinite)
+            return -__builtin_inff();
+        const double v = top - (32.0 * (bin + 1) + 1.0) / c;
+        return (float)(v - fabs(v) * 1e-6);
+    }
+    __device__ __forceinline__ float most(int bin) const
+    {
+        if (infinite || bin == 0)
+            return __builtin_inff();
+        const double v = top - (32.0 * bin - 2.0) / c;
+        return (float)(v + fabs(v) * 1e-6);
+    }
 };
+
+// Weights and, for top_k alone, counts of the bins of logits from .. to - 1, into LDS that
+// holds zeros. (A count costs LDS as much as a weight.)
+template <class V>
+__device__ __forceinline__ u64 fill_bins(const V *x, int from, int to, int n, const Weights &w,
+                                         u64 *weight, uint32_t *count, const Settings &set)
+{
+    const u64 least = (u64)ceil((double)set.floor * kOne);
+    u64 kept = 0;
+    auto fill = [&](auto weight_of, auto counts, auto floors) {
+        each<2>(x, from, to, n, [&](int, float v) {
+            int bin;
+            const u64 u = weight_of(v, bin);
+            if (u) {
+                atomicAdd(&weight[bin], u);
+                if constexpr (counts.value)
+                    atomicAdd(&count[bin], 1u);
+                if constexpr (floors.value)
+                    kept += u >= least ? u : 0;
+            }
+        });
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    auto any = [&](float v, int &bin) { return w.of(v, bin); };
+    auto finite = [&](float v, int &bin) { return w.of_finite(v, bin); };
+    if (w.infinite)
+        fill(any, yes, yes);
+    else if (set.k > 0)
+        fill(finite, yes, yes);
+    else if (set.floor > 0.0f)
+        fill(finite, no, yes);
+    else
+        fill(finite, no, no);
+    return set.floor > 0.0f ? kept : 0;
+}
+
+// How many tokens a bin of this weight holds at most: none weighs less than the bin's lower
+// end, 2.2% below its upper one.
+__device__ __forceinline__ uint32_t most_tokens(u64 weight, int bin, const double *power)
+{
+    const int k = -32 * (bin + 1);
+    const double each = ldexp(power[k & (kSteps - 1)], 44 + (k >> 10)) * 0.9999 - 0.5;
+    return weight ? (uint32_t)((double)weight / (each > 1.0 ? each : 1.0)) + 1 : 0;
+}
 
 // What of the row a pass takes: bins lo .. hi, keys key_lo .. key_hi.
 struct Range {
@@ -113,36 +287,71 @@ struct Row {
     Lds &s;
     Weights w;
 
-    __device__ __forceinline__ bool takes(const Range &r, int i, uint32_t &key, u64 &weight) const
+    __device__ __forceinline__ float logit(int i) const
     {
-        const float v = logit(x, i);
+        const float v = (float)x[i] + 0.0f;
+        return v == v ? v : -__builtin_inff();
+    }
+
+    __device__ __forceinline__ bool takes(const Range &r, float v, uint32_t &key, u64 &weight) const
+    {
         int bin;
-        key = key_of(v);
+        key = key_of(v + 0.0f);  // (-0 is 0)
         weight = w.of(v, bin);
         return weight && bin >= r.lo && bin <= r.hi && key >= r.key_lo && key <= r.key_hi;
     }
+
+    // f(i, key, weight) for what a range takes
+    template <class F>
+    __device__ __forceinline__ void each_of(const Range &r, F f) const
+    {
+        // (a comparison spares most tokens their weight)
+        const float least = w.least(r.hi), most = w.most(r.lo);
+        each<1>(x, 0, n, kThreads, [&](int i, float v) {
+            uint32_t key;
+            u64 weight;
+            if (v >= least && v <= most && takes(r, v, key, weight))
+                f(i, key, weight);
+        });
+    }
 };
+
+// Of a wave's lanes: the sums up to and with each.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 from_lane(u64 v)
+{
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROWS, 0xf, false);
+    return (u64)hi << 32 | lo;
+}
+
+__device__ __forceinline__ u64 wave_scan(u64 v)
+{
+    v += from_lane<0x111, 0xf>(v);  // row_shr:1
+    v += from_lane<0x112, 0xf>(v);  // row_shr:2
+    v += from_lane<0x114, 0xf>(v);  // row_shr:4
+    v += from_lane<0x118, 0xf>(v);  // row_shr:8
+    v += from_lane<0x142, 0xa>(v);  // row_bcast:15, into rows 1 and 3
+    v += from_lane<0x143, 0xc>(v);  // row_bcast:31, into rows 2 and 3
+    return v;
+}
 
 // Sums of v over the threads before this one; total: over all.
 __device__ u64 scan(Lds &s, u64 v, u64 &total)
 {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    u64 up = v;
-    for (int m = 1; m < 64; m <<= 1) {
-        const u64 o = __shfl_up(up, m, 64);
-        if (lane >= m)
-            up += o;
-    }
+    const u64 up = wave_scan(v);
     __syncthreads();
     if (lane == 63)
         s.part[wave] = up;
     __syncthreads();
     u64 before = 0;
     total = 0;
+#pragma unroll
     for (int i = 0; i < 16; i++) {
-        if (i < wave)
-            before += s.part[i];
-        total += s.part[i];
+        const u64 p = s.part[i];
+        before += i < wave ? p : 0;
+        total += p;
     }
     return before + up - v;
 }
@@ -150,19 +359,29 @@ __device__ u64 scan(Lds &s, u64 v, u64 &total)
 // Sums of `weight` and `count` (kBins of them) become sums of those before each.
 __device__ void scan_bins(Lds &s, u64 *weight, uint32_t *count)
 {
-    const int i = 2 * threadIdx.x;
+    const int i = 2 * threadIdx.x, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const u64 w0 = weight[i], w1 = weight[i + 1];
     const uint32_t n0 = count[i], n1 = count[i + 1];
-    u64 total, total_n;
-    const u64 before = scan(s, w0 + w1, total);
-    const u64 before_n = scan(s, n0 + n1, total_n);
+    const u64 w = wave_scan(w0 + w1), n = wave_scan(n0 + n1);
+    u64 *const counts = s.few;  // (not in use yet)
+    if (lane == 63) {
+        s.part[wave] = w;
+        counts[wave] = n;
+    }
+    __syncthreads();
+    u64 before = w - w0 - w1, before_n = n - n0 - n1;
+#pragma unroll
+    for (int k = 0; k < 16; k++) {
+        before += k < wave ? s.part[k] : 0;
+        before_n += k < wave ? counts[k] : 0;
+    }
     weight[i] = before;
     weight[i + 1] = before + w0;
     count[i] = (uint32_t)before_n;
     count[i + 1] = (uint32_t)before_n + n0;
-    if (threadIdx.x == 0) {
-        weight[kBins] = total;
-        count[kBins] = (uint32_t)total_n;
+    if (threadIdx.x == kThreads - 1) {
+        weight[kBins] = before + w0 + w1;
+        count[kBins] = (uint32_t)before_n + n0 + n1;
     }
     __syncthreads();
 }
@@ -174,13 +393,12 @@ struct Ask {
     uint32_t count;
 };
 
-// The place among `bins` sums that holds the answer, given base before the first.
-__device__ int find_bin(Lds &s, const Ask &q, u64 base_w, uint32_t base_n)
+// The bin that holds the answer.
+__device__ int find_bin(Lds &s, const Ask &q)
 {
     for (int i = threadIdx.x; i < kBins; i += kThreads) {
-        const bool in = q.count ? base_n + s.count[i] < q.count && q.count <= base_n + s.count[i + 1]
-                                : base_w + s.weight[i] < q.weight &&
-                                      q.weight <= base_w + s.weight[i + 1];
+        const bool in = q.count ? s.count[i] < q.count && q.count <= s.count[i + 1]
+                                : s.weight[i] < q.weight && q.weight <= s.weight[i + 1];
         if (in)
             s.found_bin = i;
     }
@@ -190,7 +408,74 @@ __device__ int find_bin(Lds &s, const Ask &q, u64 base_w, uint32_t base_n)
     return b;
 }
 
-// Gathers a range's tokens (at most kFew) and sorts them; sums start at base.
+// Sorts the first n places of the few, downwards, zeros last; values lie within least ..
+// most. Few are ranked by comparing each with all. More are first dealt to 1024 cells of
+// equal width in their values, and ranked within those: 1000 in 2.5 us, where compare and
+// exchange in 55 steps took 8.
+__device__ void sort_few(Lds &s, int n, float least, float most)
+{
+    constexpr int kCells = kThreads;
+    uint32_t *const cell_n = reinterpret_cast<uint32_t *>(s.upto);
+    uint32_t *const cell_at = cell_n + kCells;
+    const bool cells = n > 256;
+    const float per = (float)kCells / (most - least);
+    const bool deal = per > 0.0f && per < __builtin_inff();
+    u64 mine[2];
+    int cell[2], at[2];
+    if (cells) {
+        cell_n[threadIdx.x] = 0;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const int i = threadIdx.x + k * kThreads;
+        mine[k] = i < n ? s.few[i] : 0;
+        if (cells && mine[k]) {
+            const float c = (most - value_of((uint32_t)(mine[k] >> 32))) * per;
+            cell[k] = deal ? c > 0.0f ? c < kCells - 1 ? (int)c : kCells - 1 : 0 : 0;
+            at[k] = (int)atomicAdd(&cell_n[cell[k]], 1u);
+        }
+    }
+    __syncthreads();
+    if (cells) {
+        u64 total;
+        cell_at[threadIdx.x] = (uint32_t)scan(s, cell_n[threadIdx.x], total);
+        for (int i = threadIdx.x; i < n; i += kThreads)
+            s.few[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 2; k++)
+            if (mine[k])
+                s.few[cell_at[cell[k]] + at[k]] = mine[k];
+        __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        if (!mine[k])
+            continue;
+        const int first = cells ? (int)cell_at[cell[k]] : 0;
+        const int end = cells ? first + (int)cell_n[cell[k]] : n;
+        int rank = first;
+        for (int i = first; i < end; i++)
+            rank += s.few[i] > mine[k];
+        at[k] = rank;
+    }
+    __syncthreads();
+    if (!cells) {
+        for (int i = threadIdx.x; i < n; i += kThreads)
+            s.few[i] = 0;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < 2; k++)
+        if (mine[k])
+            s.few[at[k]] = mine[k];
+    __syncthreads();
+}
+
+// Gathers a range's tokens, at most kFew, and sorts them; sums start at base. A comparison
+// lets in some of the bins beside the range (at the lowest temperatures many), which are
+// taken out again.
 template <class V>
 __device__ void load_few(const Row<V> &row, const Range &range, u64 base)
 {
@@ -200,32 +485,45 @@ __device__ void load_few(const Row<V> &row, const Range &range, u64 base)
     for (int i = threadIdx.x; i < kFew; i += kThreads)
         s.few[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < row.n; i += kThreads) {
-        uint32_t key;
-        u64 weight;
-        if (row.takes(range, i, key, weight)) {
+    const float least = row.w.least(range.hi), most = row.w.most(range.lo);
+    each<8>(row.x, 0, row.n, kThreads, [&](int i, float v) {
+        if (v >= least && v <= most) {
+            const uint32_t at = atomicAdd(&s.n, 1u);
+            if (at < (uint32_t)kFew)
+                s.few[at] = (u64)key_of(v + 0.0f) << 32 | (uint32_t)~i;
+        }
+    });
+    __syncthreads();
+    int let_in = (int)s.n;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s.n = 0;
+    if (let_in > kFew) {
+        for (int i = threadIdx.x; i < kFew; i += kThreads)
+            s.few[i] = 0;
+        __syncthreads();
+        row.each_of(range, [&](int i, uint32_t key, u64) {
             const uint32_t at = atomicAdd(&s.n, 1u);
             if (at < (uint32_t)kFew)
                 s.few[at] = (u64)key << 32 | (uint32_t)~i;
-        }
+        });
+        __syncthreads();
+        let_in = (int)s.n < kFew ? (int)s.n : kFew;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            s.n = 0;
     }
     __syncthreads();
-    int p = 2;
-    while (p < (int)s.n)
-        p <<= 1;
-    for (int size = 2; size <= p; size <<= 1)
-        for (int step = size >> 1; step; step >>= 1) {
-            const int i = threadIdx.x;  // pairs: at most 1024
-            if (i < p / 2) {
-                const int a = 2 * i - (i & (step - 1)), b = a + step;
-                const u64 u = s.few[a], v = s.few[b];
-                if ((u < v) == ((a & size) == 0)) {
-                    s.few[a] = v;
-                    s.few[b] = u;
-                }
-            }
-            __syncthreads();
-        }
+    for (int i = threadIdx.x; i < let_in; i += kThreads) {
+        uint32_t key;
+        u64 weight;
+        if (row.takes(range, value_of((uint32_t)(s.few[i] >> 32)), key, weight))
+            atomicAdd(&s.n, 1u);
+        else
+            s.few[i] = 0;
+    }
+    __syncthreads();
+    sort_few(s, let_in, row.w.least(range.hi), fminf(row.w.most(range.lo), (float)row.w.top));
     const int i = 2 * threadIdx.x;
     int bin;
     const u64 w0 = s.few[i] ? row.w.of(value_of((uint32_t)(s.few[i] >> 32)), bin) : 0;
@@ -254,7 +552,8 @@ __device__ void answer_few(Lds &s, const Ask &q, u64 base_w, uint32_t base_n)
 
 // The answer within a bin of many tokens.
 template <class V>
-__device__ void answer_many(const Row<V> &row, const Ask &q, int bin, u64 base_w, uint32_t base_n)
+__device__ __attribute__((noinline)) void answer_many(const Row<V> row, Ask q, int bin, u64 base_w,
+                                                      uint32_t base_n)
 {
     Lds &s = row.s;
     Range r = {bin, bin, 0, 0xffffffffu};
@@ -269,14 +568,10 @@ __device__ void answer_many(const Row<V> &row, const Ask &q, int bin, u64 base_w
         }
         __syncthreads();
         uint32_t lo = 0xffffffffu, hi = 0;
-        for (int i = threadIdx.x; i < row.n; i += kThreads) {
-            uint32_t key;
-            u64 w;
-            if (row.takes(r, i, key, w)) {
-                lo = key < lo ? key : lo;
-                hi = key > hi ? key : hi;
-            }
-        }
+        row.each_of(r, [&](int, uint32_t key, u64) {
+            lo = key < lo ? key : lo;
+            hi = key > hi ? key : hi;
+        });
         atomicMin(&s.key_lo, lo);
         atomicMax(&s.key_hi, hi);
         __syncthreads();
@@ -293,15 +588,11 @@ __device__ void answer_many(const Row<V> &row, const Ask &q, int bin, u64 base_w
             count[i] = 0;
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < row.n; i += kThreads) {
-            uint32_t key;
-            u64 w;
-            if (row.takes(r, i, key, w)) {
-                const uint32_t b = (r.key_hi - key) >> shift;
-                atomicAdd(&weight[b], w);
-                atomicAdd(&count[b], 1u);
-            }
-        }
+        row.each_of(r, [&](int, uint32_t key, u64 w) {
+            const uint32_t b = (r.key_hi - key) >> shift;
+            atomicAdd(&weight[b], w);
+            atomicAdd(&count[b], 1u);
+        });
         __syncthreads();
         const u64 w0 = weight[threadIdx.x];
         const uint32_t n0 = count[threadIdx.x];
@@ -337,7 +628,7 @@ __device__ void answer_many(const Row<V> &row, const Ask &q, int bin, u64 base_w
     u64 w1 = 0, w;
     uint32_t n = 0, key;
     for (int i = first; i < end; i++)
-        if (row.takes(r, i, key, w)) {
+        if (row.takes(r, row.logit(i), key, w)) {
             n++;
             w1 = w;
         }
@@ -348,7 +639,7 @@ __device__ void answer_many(const Row<V> &row, const Ask &q, int bin, u64 base_w
         if (before < place && place <= before + n) {
             uint32_t left = (uint32_t)place - before;
             for (int i = first; i < end; i++)
-                if (row.takes(r, i, key, w) && --left == 0)
+                if (row.takes(r, row.logit(i), key, w) && --left == 0)
                     s.found_id = (uint32_t)i;
             s.found_w = base_w + place * w1;
         }
@@ -356,37 +647,108 @@ __device__ void answer_many(const Row<V> &row, const Ask &q, int bin, u64 base_w
     __syncthreads();
 }
 
+__device__ __forceinline__ int part_start(const SampleArgs &g, int part)
+{
+    return (int)((int64_t)g.V * part / g.parts);
+}
+
+// A part's largest logit, the first of equal ones; and the row's sums set to zero.
 template <class V>
+__global__ __launch_bounds__(kPartThreads) void sample_top_kernel(const SampleArgs g)
+{
+    __shared__ u64 wave_best[kPartThreads / 64];
+    const int t = blockIdx.y, part = blockIdx.x;
+    RowSums &row = g.rows[t];
+    for (int i = part * kPartThreads + threadIdx.x; i < kBins; i += g.parts * kPartThreads) {
+        row.weight[i] = 0;
+        row.count[i] = 0;
+    }
+    if (part == 0 && threadIdx.x == 0)
+        row.kept = 0;
+    Top own;
+    each<4>(static_cast<const V *>(g.logits) + t * g.row_stride, part_start(g, part),
+            part_start(g, part + 1), kPartThreads, [&](int i, float v) { own.see(i, v); });
+    u64 best = wave_largest(own.packed());
+    if ((threadIdx.x & 63) == 0)
+        wave_best[threadIdx.x >> 6] = best;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kPartThreads / 64; i++)
+            best = largest(best, wave_best[i]);
+        row.best[part] = best;
+    }
+}
+
+// The parts' best as the row's (every thread has it).
+__device__ __forceinline__ u64 best_of(const RowSums &row, int parts)
+{
+    const int lane = threadIdx.x & 63;
+    return wave_largest(lane < parts ? row.best[lane] : 0);
+}
+
+// A part's bins, added to the row's.
+template <class V>
+__global__ __launch_bounds__(kPartThreads) void sample_bins_kernel(const SampleArgs g)
+{
+    __shared__ PartLds s;
+    const int t = blockIdx.y, part = blockIdx.x;
+    RowSums &row = g.rows[t];
+    const float top = value_of((uint32_t)(best_of(row, g.parts) >> 32));
+    const Settings set(g, t);
+    if (set.first || top == -__builtin_inff())
+        return;
+    fill_powers(s.power, kPartThreads);
+    for (int i = threadIdx.x; i < kBins; i += kPartThreads) {
+        s.weight[i] = 0;
+        s.count[i] = 0;
+    }
+    if (threadIdx.x == 0)
+        s.kept = 0;
+    Weights w;
+    w.set(s.power, top, set.heat);
+    __syncthreads();
+    const u64 kept = fill_bins(static_cast<const V *>(g.logits) + t * g.row_stride,
+                               part_start(g, part), part_start(g, part + 1), kPartThreads, w,
+                               s.weight, s.count, set);
+    atomicAdd(&s.kept, kept);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kPartThreads)
+        if (s.weight[i]) {
+            atomicAdd(&row.weight[i], s.weight[i]);
+            if (set.k > 0)
+                atomicAdd(&row.count[i], s.count[i]);
+        }
+    if (threadIdx.x == 0)
+        atomicAdd(&row.kept, s.kept);
+}
+
+// SHARED: the launches above have the row's best and bins.
+template <class V, bool SHARED>
 __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs g)
 {
     extern __shared__ __attribute__((aligned(16))) char mem[];
     Lds &s = *reinterpret_cast<Lds *>(mem);
     const int t = blockIdx.x, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     Row<V> row = {static_cast<const V *>(g.logits) + t * g.row_stride, g.V, s, {}};
+    const Settings set(g, t);
 
     // the largest logit, the first of equal ones
     u64 best = 0;
-    for (int i = threadIdx.x; i < g.V; i += kThreads) {
-        const u64 k = (u64)key_of(logit(row.x, i)) << 32 | (uint32_t)~i;
-        best = k > best ? k : best;
+    if constexpr (SHARED) {
+        best = best_of(g.rows[t], g.parts);
+    } else {
+        Top own;
+        each<8>(row.x, 0, g.V, kThreads, [&](int i, float v) { own.see(i, v); });
+        best = wave_largest(own.packed());
+        if (lane == 0)
+            s.part[wave] = best;
+        __syncthreads();
+        for (int i = 0; i < 16; i++)
+            best = largest(best, s.part[i]);
     }
-    for (int m = 32; m; m >>= 1) {
-        const u64 o = __shfl_xor(best, m, 64);
-        best = o > best ? o : best;
-    }
-    if (lane == 0)
-        s.part[wave] = best;
-    __syncthreads();
-    for (int i = 0; i < 16; i++)
-        best = s.part[i] > best ? s.part[i] : best;
     const float top = value_of((uint32_t)(best >> 32));
-    const float heat = g.temperature ? g.temperature[t] : 1.0f;
-    const int k = g.top_k ? g.top_k[t] : 0;
-    const float p = g.top_p ? g.top_p[t] : 1.0f;
-    const float floor_p = g.min_p ? g.min_p[t] : 0.0f;
     const bool none = top == -__builtin_inff();
-    // (written so that NaN settings take the first token)
-    if (none || !(heat > 0.0f) || k == 1 || !(p > 0.0f) || !(floor_p <= 1.0f)) {
+    if (none || set.first) {
         if (threadIdx.x == 0) {
             g.tokens[t] = none ? -1 : (int32_t)~(uint32_t)best;
             if (g.logprobs)
@@ -400,76 +762,72 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs g)
         s.found_id = 0;
         s.found_w = (u64)kOne;
     }
-    for (int i = threadIdx.x; i < kSteps; i += kThreads)
-        s.power[i] = exp2((double)i / kSteps);
+    fill_powers(s.power, kThreads);
     for (int i = threadIdx.x; i < kBins; i += kThreads) {
-        s.weight[i] = 0;
-        s.count[i] = 0;
+        s.weight[i] = SHARED ? g.rows[t].weight[i] : 0;
+        s.count[i] = SHARED ? g.rows[t].count[i] : 0;
     }
-    row.w.power = s.power;
-    row.w.top = top;
-    row.w.infinite = top == __builtin_inff();
-    row.w.c = kSteps * 1.4426950408889634 / (double)heat;
+    row.w.set(s.power, top, set.heat);
     __syncthreads();
-
-    // counts and weights of the bins, and the weights that min_p leaves
-    const double least = (double)floor_p * kOne;
-    u64 kept = 0;
-    for (int i = threadIdx.x; i < g.V; i += kThreads) {
-        int bin;
-        const u64 w = row.w.of(logit(row.x, i), bin);
-        if (w) {
-            atomicAdd(&s.weight[bin], w);
-            atomicAdd(&s.count[bin], 1u);
-            if ((double)w >= least)
-                kept += w;
-        }
+    u64 left;  // what min_p leaves, then all filters
+    if constexpr (SHARED) {
+        left = g.rows[t].kept;
+    } else {
+        const u64 kept = fill_bins(row.x, 0, g.V, kThreads, row.w, s.weight, s.count, set);
+        scan(s, kept, left);
     }
+    if (set.k <= 0)
+        for (int i = threadIdx.x; i < kBins; i += kThreads)
+            s.count[i] = most_tokens(s.weight[i], i, s.power);
     __syncthreads();
     scan_bins(s, s.weight, s.count);
-    u64 left;
-    scan(s, kept, left);
 
-    // the sorted few: bins lo .. hi, if any
+    // top_k, top_p and the draw, each asked where it says anything; `all` is what top_k and
+    // top_p leave, `left` what min_p does, then all three. The sorted few: bins lo .. hi, if any.
     int lo = 0, hi = -1;
-    auto ask = [&](const Ask &q, bool last) {
-        const int b = find_bin(s, q, 0, 0);
-        if (b < lo || b > hi) {
-            if (s.count[b + 1] - s.count[b] > (uint32_t)kFew) {
-                lo = 0;
-                hi = -1;  // (the few's memory is used for the search)
-                answer_many(row, q, b, s.weight[b], s.count[b]);
-                return;
-            }
-            lo = !last && s.count[b + 1] <= (uint32_t)kFew ? 0 : b;
-            hi = b;
-            load_few(row, Range{lo, hi, 0, 0xffffffffu}, s.weight[lo]);
-        }
-        answer_few(s, q, s.weight[lo], s.count[lo]);
-    };
     u64 all = s.weight[kBins];
-    if (k > 0 && (uint32_t)k < s.count[kBins]) {
-        ask(Ask{0, (uint32_t)k}, false);
-        all = s.found_w;
+    for (int turn = 0; turn < 3; turn++) {
+        Ask q = {0, 0};
+        if (turn == 0) {
+            if (set.k <= 0 || (uint32_t)set.k >= s.count[kBins])
+                continue;
+            q.count = (uint32_t)set.k;
+        } else if (turn == 1) {
+            if (!(set.p < 1.0f))
+                continue;
+            q.weight = (u64)ceil((double)set.p * (double)all);
+            q.weight = q.weight < 1 ? 1 : q.weight > all ? all : q.weight;
+        } else {
+            float u = g.u[t];
+            u = u > 0.0f ? u : 0.0f;
+            left = set.floor > 0.0f && left < all ? left : all;
+            q.weight = (u64)((double)u * (double)left) + 1;
+            q.weight = q.weight > left ? left : q.weight;
+        }
+        const int b = find_bin(s, q);
+        const int next = b + 2 < kBins ? b + 2 : kBins, before = b > 0 ? b - 1 : 0;
+        if ((b < lo || b > hi) && s.count[next] - s.count[before] > (uint32_t)kFew) {
+            lo = 0;
+            hi = -1;  // (the few's memory is used for the search)
+            answer_many(row, q, b, s.weight[b], s.count[b]);
+        } else {
+            if (b < lo || b > hi) {
+                lo = turn < 2 && s.count[next] <= (uint32_t)kFew ? 0 : b;
+                hi = b;
+                load_few(row, Range{lo, hi, 0, 0xffffffffu}, s.weight[lo]);
+            }
+            answer_few(s, q, s.weight[lo], s.count[lo]);
+        }
+        if (turn < 2)
+            all = s.found_w;
         __syncthreads();
     }
-    left = left < all ? left : all;
-    if (p < 1.0f) {
-        const u64 need = (u64)ceil((double)p * (double)all);
-        ask(Ask{need < 1 ? 1 : need > all ? all : need, 0}, false);
-        left = s.found_w < left ? s.found_w : left;
-        __syncthreads();
-    }
-    float u = g.u[t];
-    u = u > 0.0f ? u : 0.0f;
-    const u64 at = (u64)((double)u * (double)left) + 1;
-    ask(Ask{at > left ? left : at, 0}, true);
     if (threadIdx.x == 0) {
         const uint32_t id = s.found_id;
         g.tokens[t] = (int32_t)id;
         if (g.logprobs) {
-            const float v = logit(row.x, (int)id);
-            const double e = row.w.infinite ? 0.0 : ((double)v - (double)top) / (double)heat;
+            const float v = row.logit((int)id);
+            const double e = row.w.infinite ? 0.0 : ((double)v - (double)top) / (double)set.heat;
             g.logprobs[t] = (float)(e - log((double)left / kOne));
         }
     }
@@ -478,23 +836,46 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs g)
 template <class V>
 int launch(const SampleArgs &g, int64_t T, hipStream_t stream)
 {
-    allow_dynamic_lds(reinterpret_cast<const void *>(sample_kernel<V>), sizeof(Lds));
-    hipLaunchKernelGGL((sample_kernel<V>), dim3((unsigned)T), dim3(kThreads), sizeof(Lds), stream,
-                       g);
-    return check_launch();
+    auto row = [&](auto *kernel) {
+        allow_dynamic_lds(reinterpret_cast<const void *>(kernel), sizeof(Lds));
+        hipLaunchKernelGGL(kernel, dim3((unsigned)T), dim3(kThreads), sizeof(Lds), stream, g);
+        return check_launch();
+    };
+    if (g.parts == 1)
+        return row(sample_kernel<V, false>);
+    const dim3 grid((unsigned)g.parts, (unsigned)T);
+    hipLaunchKernelGGL((sample_top_kernel<V>), grid, dim3(kPartThreads), 0, stream, g);
+    if (int rc = check_launch())
+        return rc;
+    hipLaunchKernelGGL((sample_bins_kernel<V>), grid, dim3(kPartThreads), 0, stream, g);
+    if (int rc = check_launch())
+        return rc;
+    return row(sample_kernel<V, true>);
+}
+
+// Workgroups that share a row: none but its own from 128 rows on (256 rows of 100003: 92 us
+// by one each, 105 by two), else as many as give the device 512, of 2048 logits at least.
+int parts_of(int64_t T, int64_t V)
+{
+    if (T < 1 || T >= 128)
+        return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({512 / T, V / 2048, kPartsMax}));
 }
 
 }  // namespace
 
-size_t sample_workspace(int64_t, int64_t) { return 0; }
+size_t sample_workspace(int64_t T, int64_t V)
+{
+    return parts_of(T, V) == 1 ? 0 : ((size_t)T * sizeof(RowSums) + 255) / 256 * 256;
+}
 
 int launch_sample(const void *logits, int64_t row_stride, const float *temperature,
                   const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
-                  int32_t *tokens, float *logprobs, int64_t T, int64_t V, int dtype, void *,
-                  hipStream_t stream)
+                  int32_t *tokens, float *logprobs, int64_t T, int64_t V, int dtype,
+                  void *workspace, hipStream_t stream)
 {
-    const SampleArgs g = {logits, row_stride, temperature, top_k, top_p, min_p,
-                          u,      tokens,     logprobs,    (int)V};
+    const SampleArgs g = {logits, row_stride, temperature, top_k, top_p, min_p, u, tokens, logprobs,
+                          static_cast<RowSums *>(workspace), (int)V, parts_of(T, V)};
     if (dtype == BQM_DTYPE_F32)
         return launch<float>(g, T, stream);
     if (dtype == BQM_DTYPE_F16)
