@@ -4,11 +4,13 @@ cache that is moved together.
 
 Each layer is the library's quantized products around its attention side:
 
-    q, k, v = W_qkv . quantize(norm(x))      mm_tq1_0 (or mmvq_tq1_0)
+    q, k, v = W_qkv . quantize(norm(x))      rms_norm_q8_1, mm_tq1_0 (or mmvq_tq1_0)
     q, cache <- rope(q), rope(k), v          rope_kv_append
     a = attention(q, cache)                  paged_attention, fp32 out
     x = x + W_out . quantize(a)              mmvq_tq1_0_add
     x = x + W_down . quantize(silu(W_gate . n) * (W_up . n)),  n = quantize(norm(x))
+
+(`generate.py` puts tokens in front of them and behind.)
 
     python examples/decoder_layer.py [--layers 4 --tokens 600 --steps 16]
 """
@@ -82,11 +84,11 @@ class Decoder:
         batch = bqm.KvBatch(self.pages.table, self.pages.lens, starts.cuda(), max_q=max(new))
         T, H, G = x.shape[0], self.heads, self.kv_heads
         for layer, cache in zip(self.layers, self.caches):
-            row = layer["qkv"](bqm.q8_1_quantize(norm(x)), T).view(T, H + 2 * G, self.head)
+            row = layer["qkv"](bqm.rms_norm_q8_1(x)[0], T).view(T, H + 2 * G, self.head)
             q = bqm.rope_kv_append(row[:, :H], row[:, H:H + G], row[:, H + G:], cache, batch, self.angles)
             a = bqm.paged_attention(q, cache, batch, out_dtype=torch.float32)
             x = layer["out"](bqm.q8_1_quantize(a.view(T, self.dim)), T, add=x)
-            n = bqm.q8_1_quantize(norm(x))
+            n, _ = bqm.rms_norm_q8_1(x)
             if T <= bqm.GLU_MAX_COLS:
                 h = bqm.mmvq_tq1_0_glu(layer["gate"].w, layer["up"].w, n, self.hidden, self.dim, T)
             else:

@@ -426,16 +426,16 @@ def test_sample_masks():
 
 
 def test_sample_odd_settings():
-    nan, x = math.nan, randn(8, 900, seed=2)
-    check_sample(x, [-1.0, nan, 1.0, 2.0, math.inf, -math.inf, 0.3, 0.4])
-    best = x.argmax(-1).to(torch.int32)
-    for kw in (dict(heat=[nan] * 8), dict(p=[nan] * 8), dict(p=[-1.0] * 8), dict(least=[nan] * 8), dict(least=[1.5] * 8),
-               dict(k=[1] * 8)):
-        assert torch.equal(check_sample(x, US, **{k: v for k, v in kw.items() if v[0] == v[0]}) if list(kw.values())[0][0] ==
-                           list(kw.values())[0][0] else bqm.sample(x, torch.tensor(US, device="cuda"), **{
-                               {"heat": "temperature", "p": "top_p", "least": "min_p"}[k]: torch.tensor(v, device="cuda")
-                               for k, v in kw.items()})[0], best), kw
+    x = randn(8, 900, seed=2)
+    check_sample(x, [-1.0, math.nan, 1.0, 2.0, math.inf, -math.inf, 0.3, 0.4])
     check_sample(x, US, k=[-5] * 8)
+    # a setting that is no number, or that leaves nothing, takes the first token
+    best = x.argmax(-1).to(torch.int32)
+    u = torch.tensor(US, device="cuda")
+    for name, value in (("temperature", math.nan), ("temperature", -1.0), ("top_p", math.nan), ("top_p", -1.0), ("top_p", 0.0),
+                        ("min_p", math.nan), ("min_p", 1.5), ("min_p", 1.0)):
+        tokens, logprobs = bqm.sample(x, u, **{name: torch.full((8,), value, device="cuda")})
+        assert torch.equal(tokens, best) and bool((logprobs == 0).all()), (name, value)
 
 
 def test_sample_shares():
