@@ -836,7 +836,12 @@ constexpr int64_t kMostCols = 8192;  // laid out at once
 
 size_t mm_q4_workspace(int64_t N, int64_t T, int64_t K)
 {
-    return T <= kDotCols || few_supported(T, (int)(K / 32)) ? 0 : laid_out_bytes(N, std::min(T, kMostCols), K / 32);
+    if (T <= kDotCols || few_supported(T, (int)(K / 32)))
+        return 0;
+    // (the columns of the last turn, where there are several, may be few enough for parts)
+    const int64_t last = (T - 1) % kMostCols + 1;
+    return std::max(laid_out_bytes(N, std::min(T, kMostCols), K / 32),
+                    laid_out_bytes(N, last, K / 32));
 }
 
 int launch_mm_q4(const bqm_q4_matrix *m, const void *a, float *y, int64_t T, void *workspace,
