@@ -111,3 +111,27 @@ def test_sample_does_not_depend_on_the_number_of_rows(kind, V, dtype):
             got = draw(x, times, **settings)
             assert torch.equal(got[0], tokens.repeat(times)), (times, settings)
             assert torch.equal(got[1], logprobs.repeat(times)), (times, settings)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [32, 64, 96, 128, 160, 256, 288, 512])
+@pytest.mark.parametrize("T", [1, 7, 64, 1001])
+def test_norm_of_short_rows(T, K):
+    # several rows a wave: heads' norms. fp32 throughout: r, s * r and its product with gain are
+    # rounded, 2^-24 each
+    x, add, gain = randn(T, K, seed=T, dtype=BF16, scale=2.0), randn(T, K, seed=K), randn(K, seed=3)
+    x[T // 2] = 0.0
+    add[T // 2] = 0.0
+    s = (x.float() + add).to(BF16)
+    y, got = bqm.rms_norm(x, gain, add=add, out_dtype=F32)
+    assert torch.equal(got, s)
+    d = s.double()
+    want = d / (d.square().mean(-1, keepdim=True) + 1e-6).sqrt() * gain.double()
+    room = ((1 + 2.0 ** -24) ** 3 - 1 + 2.0 ** -45) * want.abs() + 2.0 ** -148
+    assert bool(((y.double() - want).abs() <= room).all())
+    a, _ = bqm.rms_norm_q8_1(x, gain, add=add)
+    assert torch.equal(a, bqm.q8_1_quantize(y))
+    # each row as it is alone
+    for t in {0, T // 2, T - 1}:
+        one, _ = bqm.rms_norm(x[t:t + 1], gain, add=add[t:t + 1], out_dtype=F32)
+        assert torch.equal(one, y[t:t + 1])
