@@ -13,9 +13,9 @@
 // Weights are whole numbers of 2^-44: sums are exact, atomics in any order give the
 // same bits.
 //
-// A row is a workgroup's. Where there are fewer rows than would fill the device, the
-// two passes over all of a row (its largest logit; its bins) are shared by several
-// workgroups each, launches of their own before it.
+// A row is a workgroup's. Where rows are few and long, the two passes over all of a row
+// (its largest logit; its bins) are shared by several workgroups each, launches of their
+// own before it.
 #include <algorithm>
 #include <type_traits>
 
@@ -805,14 +805,13 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs g)
             q.weight = q.weight > left ? left : q.weight;
         }
         const int b = find_bin(s, q);
-        const int next = b + 2 < kBins ? b + 2 : kBins, before = b > 0 ? b - 1 : 0;
-        if ((b < lo || b > hi) && s.count[next] - s.count[before] > (uint32_t)kFew) {
+        if ((b < lo || b > hi) && s.count[b + 1] - s.count[b] > (uint32_t)kFew) {
             lo = 0;
             hi = -1;  // (the few's memory is used for the search)
             answer_many(row, q, b, s.weight[b], s.count[b]);
         } else {
             if (b < lo || b > hi) {
-                lo = turn < 2 && s.count[next] <= (uint32_t)kFew ? 0 : b;
+                lo = turn < 2 && s.count[b + 1] <= (uint32_t)kFew ? 0 : b;
                 hi = b;
                 load_few(row, Range{lo, hi, 0, 0xffffffffu}, s.weight[lo]);
             }
@@ -853,13 +852,16 @@ int launch(const SampleArgs &g, int64_t T, hipStream_t stream)
     return row(sample_kernel<V, true>);
 }
 
-// Workgroups that share a row: none but its own from 128 rows on (256 rows of 100003: 92 us
-// by one each, 105 by two), else as many as give the device 512, of 2048 logits at least.
+// Workgroups that share a row: as many as give the device 512, of 2048 logits at least, where
+// that is faster than its own alone, which spares two launches. Measured over 1 to 192 rows of
+// 4096 to 1000000 logits, the border runs from 45000 logits (one row: 30 us alone, 27 shared,
+// of 50000; 25 and 27 of 32001) by 64000 (32 rows: 43 and 41) to 131071 (128 rows: 75 and 71;
+// 69 and 74 of 100003).
 int parts_of(int64_t T, int64_t V)
 {
-    if (T < 1 || T >= 128)
+    if (T < 1 || T > 128 || V < 40000 + 700 * T)
         return 1;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({512 / T, V / 2048, kPartsMax}));
+    return (int)std::min<int64_t>({512 / T, V / 2048, kPartsMax});
 }
 
 }  // namespace

@@ -154,7 +154,7 @@ def test_a_stream_of_another_device_is_refused():
 
 def test_given_workspaces_and_outputs():
     # workspaces with anything in them, and no byte behind what is asked for touched
-    e = Ends(vocab=20011)
+    e = Ends(vocab=80021)
     for n in (1, 40, 200):
         a = bqm.q8_1_quantize(torch.randn(n, e.dim, device="cuda"))
         u = torch.rand(n, device="cuda")
@@ -171,10 +171,10 @@ def test_given_workspaces_and_outputs():
             ws = torch.full((need + 512,), fill, device="cuda", dtype=torch.uint8)
             t, lp = bqm.sample(logits, u, workspace=ws[:max(need, 1)])
             assert torch.equal(t, tokens[0]) and torch.equal(lp, tokens[1]) and bool((ws[need:] == fill).all())
-    need = bqm.sample_workspace_bytes(1, 20011)
+    need = bqm.sample_workspace_bytes(1, 80021)
     assert need > 0
     with pytest.raises(ValueError):
-        bqm.sample(torch.randn(1, 20011, device="cuda"), u[:1], workspace=torch.empty(need - 1, device="cuda", dtype=torch.uint8))
+        bqm.sample(torch.randn(1, 80021, device="cuda"), u[:1], workspace=torch.empty(need - 1, device="cuda", dtype=torch.uint8))
 
 
 def test_results_do_not_depend_on_the_turn():
