@@ -34,7 +34,9 @@ __device__ __forceinline__ int near8(float v)  // the nearest code, -8 .. 7
 }
 
 // Four lanes a run of 32 values, lane h holding 8h .. 8h + 7; a group is 4, 8 or 16
-// lanes. One pass: extremes over the group by lane exchanges, then the codes.
+// lanes. One pass: extremes over the group by lane exchanges, then the codes. Bound by the
+// fp32 quotients, a division a value as the definition has it: 100003 x 4096 bf16 in 363 us
+// (2.9 TB/s), once in a matrix's life.
 template <class V>
 __global__ __launch_bounds__(256) void q4_quantize_kernel(const V *__restrict__ x, uint8_t *codes,
                                                           uint16_t *scales, int8_t *zeros,
@@ -108,7 +110,9 @@ __device__ __forceinline__ void store8(V *p, const float (&x)[8])
 }
 
 // Eight bytes of codes a thread: values 8h .. 8h + 7 and 16 + 8h .. 23 + 8h of a run.
-// 1 << lt threads a row, which loop where a row has more pieces than that.
+// 1 << lt threads a row, which loop where a row has more pieces than that. Memory bounds it:
+// 8191 rows of 4096 to bf16 17.6 us (4.8 TB/s), all of 100003 to fp16 192 to 206 (5.1 to 5.4),
+// to fp32 325 (5.7).
 template <class V>
 __global__ __launch_bounds__(256) void q4_dequantize_kernel(const bqm_q4_matrix m,
                                                             const int32_t *__restrict__ rows,

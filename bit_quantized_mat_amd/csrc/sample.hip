@@ -15,7 +15,10 @@
 //
 // A row is a workgroup's. Where rows are few and long, the two passes over all of a row
 // (its largest logit; its bins) are shared by several workgroups each, launches of their
-// own before it.
+// own before it. What bounds it: of few rows the latency of a score of steps (one row of
+// 32001 logits 21.6 us), else the fp64 weights and the passes over a row by one compute unit
+// (256 rows of 100003 bf16 85 us: largest 9, bins 25, each gathering 6 to 9; 64 of fp32, shared
+// by 8: 7 + 14 us, then 32 of the row's own workgroup).
 #include <algorithm>
 #include <type_traits>
 
@@ -307,7 +310,7 @@ struct Row {
     {
         // (a comparison spares most tokens their weight)
         const float least = w.least(r.hi), most = w.most(r.lo);
-        each<1>(x, 0, n, kThreads, [&](int i, float v) {
+        each<4>(x, 0, n, kThreads, [&](int i, float v) {
             uint32_t key;
             u64 weight;
             if (v >= least && v <= most && takes(r, v, key, weight))
