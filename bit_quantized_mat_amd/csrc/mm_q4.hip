@@ -587,8 +587,8 @@ int launch_mfma(const Q4Args &g, const Laid &l, hipStream_t stream)
 //
 // Up to 32 columns that fit in LDS stay there, as int8 operands, and every wave goes through
 // rows by itself, without a barrier between its loads: what counts is bytes on their way, then
-// issue (160 instructions for four runs). 100003 x 4096: 9 columns 55 us, 17 69 (the matrix
-// alone 42; by tiles 108); 4096 x 4096 and 8 columns 7.0.
+// issue (160 instructions for four runs). 100003 x 4096: 9 columns 51 us, 17 64 (the matrix
+// alone 42; by tiles 108), 72 with whole tiles dealt to waves; 4096 x 4096 and 9 columns 7.2.
 // A code in the high half of its byte is 16 times the code, so an operand takes three
 // instructions; a zero's share goes into the products' start, -16 * zero * sum of q. The
 // products' rows are columns of the call and their columns rows of the matrix: a lane's
@@ -603,9 +603,10 @@ constexpr int kFewRun = 512 + 32 + 32;
 
 size_t few_lds(int ct, int nb) { return (size_t)((nb + 3) / 4 * 4) * ct * kFewRun; }
 
-// W waves of 16 rows, CT tiles of 16 columns, groups of 32 << SH. A workgroup has an
-// even share of the row tiles, one a wave at a time; where fewer than half its waves have
-// one left, or there are few rows at all, waves share a tile, a part of the runs each.
+// W waves of 16 rows, CT tiles of 16 columns, groups of 32 << SH. A workgroup has an even
+// share of the row tiles, and a wave an even share of the runs of those, one after another
+// (in periods of four groups): the end of a tile that the wave before it began, whole tiles,
+// the beginning of one that others end, whose parts are added at last, in their order.
 template <int CT, int W, int SH, bool Z>
 __global__ __launch_bounds__(64 * W) void q4_few_kernel(const Q4Args g, int tiles)
 {
@@ -617,11 +618,16 @@ __global__ __launch_bounds__(64 * W) void q4_few_kernel(const Q4Args g, int tile
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int c = lane & 15, h = lane >> 4;
     const int chunks = (g.nb + 3) / 4, groups = g.nb >> SH;
-    int tile = (int)((int64_t)tiles * blockIdx.x / gridDim.x);
-    const int tile_end = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+    const int tile0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x);
+    const int own_tiles = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x) - tile0;
+    const int periods = (chunks + kPeriod - 1) / kPeriod;  // of a tile
+    // (below 2^31: rows are short where they are many)
+    auto share = [&](int w) { return (int)((uint32_t)(own_tiles * periods * w) / W); };
+    const int share_end = share(wave + 1);
+    int at = share(wave), tile = (int)((uint32_t)(own_tiles * wave) / W);
 
-    // The waves' next tiles: log2 of the waves a tile has, this wave's part.
-    int ks, first, end;
+    // The next part of a tile: the period behind the tile's last, chunks.
+    int tile_end, first, end;
     __amdgpu_buffer_rsrc_t codes;
     int64_t n0;
     u32x4 next[kAhead];
@@ -668,30 +674,22 @@ __global__ __launch_bounds__(64 * W) void q4_few_kernel(const Q4Args g, int tile
         if constexpr (Z)
             zeros = __builtin_amdgcn_ds_bpermute(from, (int)zeros_held);
     };
-    auto begin = [&]() {  // the next tiles' first loads
-        const int left = tile_end - tile;
-        ks = 0;
-        while ((2 << ks) <= W && (left << (ks + 1)) <= W && (chunks >> ks) >= 4)
-            ks++;
-        const int mine = tile + (wave >> ks), part = wave & ((1 << ks) - 1);
-        // whole periods of four groups
-        const int periods = (chunks + kPeriod - 1) / kPeriod;
-        first = (periods * part >> ks) * kPeriod;
-        end = (periods * (part + 1) >> ks) * kPeriod;
-        end = end < chunks ? end : chunks;
-        n0 = (int64_t)mine * 16;
-        int64_t rows = mine < tile_end ? g.m.N - n0 : 0;
-        rows = rows < 16 ? rows : 16;
-        codes = make_rsrc(static_cast<const char *>(g.m.codes) + (rows ? n0 : 0) * g.nb * 16,
+    auto begin = [&]() {  // the first loads of what is left from `at` on
+        tile_end = (tile + 1) * periods;
+        const int part_end = (share_end < tile_end ? share_end : tile_end) - tile * periods;
+        first = (at - tile * periods) * kPeriod;
+        end = part_end * kPeriod < chunks ? part_end * kPeriod : chunks;
+        n0 = (int64_t)(tile0 + tile) * 16;
+        const int64_t rows = g.m.N - n0 < 16 ? g.m.N - n0 : 16;
+        codes = make_rsrc(static_cast<const char *>(g.m.codes) + n0 * g.nb * 16,
                           (uint64_t)rows * g.nb * 16);
-        if (rows == 0)
-            n0 = g.m.N;  // (a wave without a tile goes along)
 #pragma unroll
         for (int i = 0; i < kAhead; i++)
             fetch(i, first + i);
         gather(first / kPeriod / 4);
     };
-    begin();
+    if (at < share_end)
+        begin();
 
     // the columns: a thread a column's run
     for (int i = threadIdx.x; i < chunks * 4 * CT * 16; i += 64 * W) {
@@ -717,14 +715,27 @@ __global__ __launch_bounds__(64 * W) void q4_few_kernel(const Q4Args g, int tile
     }
     __syncthreads();
 
-    for (;;) {
-        float acc[CT][4] = {}, sums[CT][4];
-        const int shared = ks;
-        const int64_t n1 = n0;
-        for (int at = first; at < end; at += kAhead) {
+    auto store = [&](const float (&v)[CT][4], int64_t row0) {
+        const int64_t n = row0 + c;
+#pragma unroll
+        for (int t = 0; t < CT; t++)
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const int col = 16 * t + 4 * h + k;
+                if (n < g.m.N && col < g.T)
+                    g.y[(int64_t)col * g.m.N + n] = v[t][k];
+            }
+    };
+    float acc[CT][4], sums[CT][4], head[CT][4] = {};  // head: of a tile that another wave began
+    bool tail = false;                                // acc: of one that others end
+    while (at < share_end) {
+#pragma unroll
+        for (int i = 0; i < CT * 4; i++)
+            acc[i / 4][i % 4] = 0.0f;
+        for (int start = first; start < end; start += kAhead) {
 #pragma unroll
             for (int slot = 0; slot < kAhead; slot++) {
-                const int chunk = at + slot;
+                const int chunk = start + slot;
                 if (chunk >= end)
                     break;
                 if (chunk % kPeriod == 0)
@@ -774,36 +785,43 @@ __global__ __launch_bounds__(64 * W) void q4_few_kernel(const Q4Args g, int tile
                 }
             }
         }
-        tile += W >> shared;
-        const bool again = tile < tile_end;  // (the same for all waves; never after a shared tile)
-        if (again)
+        const bool begun = first == 0;
+        const int64_t n1 = n0;
+        tail = begun && share_end < tile_end;
+        at = share_end < tile_end ? share_end : tile_end;
+        tile++;
+        if (at < share_end)
             begin();
-        if (shared) {  // the parts' sums, in order; the columns are done with
-            __syncthreads();
-            float *const mine = reinterpret_cast<float *>(lds) + wave * CT * 4 * 64 + lane;
+        if (!begun) {
 #pragma unroll
             for (int i = 0; i < CT * 4; i++)
-                mine[i * 64] = acc[i / 4][i % 4];
-            __syncthreads();
-            if (wave & ((1 << shared) - 1))
-                return;
-            for (int o = 1; o < 1 << shared; o++)
-#pragma unroll
-                for (int i = 0; i < CT * 4; i++)
-                    acc[i / 4][i % 4] += mine[(o * CT * 4 + i) * 64];
+                head[i / 4][i % 4] = acc[i / 4][i % 4];
+        } else if (!tail) {
+            store(acc, n1);
         }
-        const int64_t n = n1 + c;
-#pragma unroll
-        for (int t = 0; t < CT; t++)
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const int col = 16 * t + 4 * h + k;
-                if (n < g.m.N && col < g.T)
-                    g.y[(int64_t)col * g.m.N + n] = acc[t][k];
-            }
-        if (!again)
-            return;
     }
+    if (own_tiles % W == 0)
+        return;  // (no tile is shared)
+    __syncthreads();  // the columns are done with
+    float *const heads = reinterpret_cast<float *>(lds) + wave * CT * 4 * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < CT * 4; i++)
+        heads[i * 64] = head[i / 4][i % 4];
+    __syncthreads();
+    if (!tail)
+        return;
+    int others = W - 1 - wave;
+    if (own_tiles > 1) {  // (counting takes 0.3 us)
+        others = 0;
+        while (wave + others + 1 < W && share(wave + others + 1) < tile_end)
+            others++;
+    }
+#pragma unroll 4
+    for (int o = 1; o <= others; o++)
+#pragma unroll
+        for (int i = 0; i < CT * 4; i++)
+            acc[i / 4][i % 4] += heads[(o * CT * 4 + i) * 64];
+    store(acc, n0);
 }
 
 template <int CT, int W, int SH>
@@ -828,12 +846,13 @@ int launch_few_waves(const Q4Args &g, hipStream_t stream)
                           : launch_few_group<CT, W, 2>(g, stream);
 }
 
-// Sixteen waves where each has a tile of its own: 55 us against 64 for 100003 rows of 4096
-// and 9 columns; for 4096 rows eight are faster (7.3 against 9.0).
+// Sixteen waves where a workgroup has at least seven tiles: of 4096 values a row and 17 columns
+// 100003 rows take 64 us, with eight waves 75, 32000 rows 26 and 27; 14336 rows 17.6 and 17.9,
+// but with 9 columns 12.7 and 12.3, 20000 rows of 512 values 5.8 and 5.4; 4096 rows 12.4 and 9.9.
 template <int CT>
 int launch_few(const Q4Args &g, hipStream_t stream)
 {
-    return g.m.N >= (int64_t)compute_units() * 256 ? launch_few_waves<CT, 16>(g, stream)
+    return g.m.N >= (int64_t)compute_units() * 112 ? launch_few_waves<CT, 16>(g, stream)
                                                    : launch_few_waves<CT, 8>(g, stream);
 }
 

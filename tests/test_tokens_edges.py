@@ -135,3 +135,20 @@ def test_norm_of_short_rows(T, K):
     for t in {0, T // 2, T - 1}:
         one, _ = bqm.rms_norm(x[t:t + 1], gain, add=add[t:t + 1], out_dtype=F32)
         assert torch.equal(one, y[t:t + 1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 20])
+@pytest.mark.parametrize("K,group,zeros", [(32, 32, True), (544, 32, False), (1152, 128, True), (2112, 64, False)])
+@pytest.mark.parametrize("N", [16, 4111, 8200, 12300, 28688, 30001, 45007, 66001])
+def test_mm_q4_rows_shared_by_waves(N, K, group, zeros, T):
+    # one tile a workgroup to dozens, tiles of which waves have a part: the header's bound
+    m = matrix(N, K, group, zeros, seed=N)
+    a = bqm.q8_1_quantize(randn(T, K, seed=K, scale=2.0))
+    y = bqm.mm_q4(m, a, out=torch.full((T, N), float("nan"), device="cuda"))
+    w = bqm.q4_dequantize(m, dtype=F32).double()
+    b = a.view(T, K // 32, 36)
+    c = (b[:, :, :32].contiguous().view(torch.int8).double() * b[:, :, 32:34].contiguous().view(F16).double()).view(T, K)
+    # (dequantized values are rounded to fp32: 2^-24 of each)
+    room = (1e-5 + 2.0 ** -24) * (c.abs() @ w.abs().t().contiguous())
+    assert bool(((y.double() - c @ w.t().contiguous()).abs() <= room).all())
