@@ -587,7 +587,7 @@ int launch_mfma(const Q4Args &g, const Laid &l, hipStream_t stream)
 //
 // Up to 32 columns that fit in LDS stay there, as int8 operands, and every wave goes through
 // rows by itself, without a barrier between its loads: what counts is bytes on their way, then
-// issue (160 instructions for four runs). 100003 x 4096: 9 columns 51 us, 17 64 (the matrix
+// issue (150 instructions for four runs). 100003 x 4096: 9 columns 51 us, 17 64 (the matrix
 // alone 42; by tiles 108), 72 with whole tiles dealt to waves; 4096 x 4096 and 9 columns 7.2.
 // A code in the high half of its byte is 16 times the code, so an operand takes three
 // instructions; a zero's share goes into the products' start, -16 * zero * sum of q. The
