@@ -15,6 +15,20 @@ inline int check_launch()
     return e == hipSuccess ? BQM_OK : BQM_ERR_LAUNCH;
 }
 
+// A grid of many workgroups in two dimensions, each of which has to stay below 2^32 threads
+// (workgroups of up to 1024), and a workgroup's place in it; places behind the last occur.
+inline dim3 grid_of(int64_t blocks)
+{
+    constexpr int64_t kRow = 1 << 20;
+    return blocks <= kRow ? dim3((unsigned)blocks)
+                          : dim3((unsigned)kRow, (unsigned)((blocks + kRow - 1) / kRow));
+}
+
+__device__ __forceinline__ int64_t block_of_grid()
+{
+    return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+}
+
 // Dynamic LDS: 64 KiB is always available; beyond that the launcher raises
 // the kernel's limit up to what the device reports (160 KiB on gfx950).
 constexpr size_t kLdsDefault = 64 * 1024;

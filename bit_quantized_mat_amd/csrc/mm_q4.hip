@@ -29,7 +29,7 @@ struct Q4Args {
 
 constexpr int kStageRuns = 128;  // runs of a column staged at once
 
-// Columns t0 .. t0 + TC - 1 of runs b0 .. b0 + n - 1, as two planes of 16 bytes a run
+// Columns 0 .. TC - 1 of runs b0 .. b0 + n - 1, as two planes of 16 bytes a run
 // (a lane reads each with one load, neighbours next to each other), d / 16 and sums.
 template <int TC>
 struct Stage {
@@ -39,14 +39,13 @@ struct Stage {
 };
 
 template <int TC, bool Z>
-__device__ __forceinline__ void stage_columns(Stage<TC> &s, const Q4Args &g, int64_t t0, int b0,
-                                              int n)
+__device__ __forceinline__ void stage_columns(Stage<TC> &s, const Q4Args &g, int b0, int n)
 {
     for (int i = threadIdx.x; i < TC * kStageRuns; i += 256) {
         const int t = i / kStageRuns, b = i % kStageRuns;
         if (b >= n)
             continue;
-        const int64_t col = t0 + t < g.T ? t0 + t : g.T - 1;
+        const int64_t col = t < g.T ? t : g.T - 1;
         const uint32_t *p = reinterpret_cast<const uint32_t *>(
             g.a + (col * g.nb + b0 + b) * kQ81BlockBytes);
         uint32_t q[8];
@@ -76,14 +75,13 @@ __global__ __launch_bounds__(256) void q4_dot_kernel(const Q4Args g, int lr)
     __shared__ Stage<TC> s;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int per = 64 >> lr;  // rows side by side
-    const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * (per * R) + (lane >> lr);
-    const int64_t t0 = (int64_t)blockIdx.y * TC;
+    const int64_t first = (block_of_grid() * 4 + wave) * (per * R) + (lane >> lr);
     float acc[R][TC] = {};
     for (int b0 = 0; b0 < g.nb; b0 += kStageRuns) {
         const int n = g.nb - b0 < kStageRuns ? g.nb - b0 : kStageRuns;
         if (b0)
             __syncthreads();
-        stage_columns<TC, Z>(s, g, t0, b0, n);
+        stage_columns<TC, Z>(s, g, b0, n);
         __syncthreads();
         for (int b = lane & ((1 << lr) - 1); b < n; b += 1 << lr) {
 #pragma unroll
@@ -118,8 +116,8 @@ __global__ __launch_bounds__(256) void q4_dot_kernel(const Q4Args g, int lr)
 #pragma unroll
         for (int t = 0; t < TC; t++) {
             const float v = row_sum(acc[r][t], lr);
-            if ((lane & ((1 << lr) - 1)) == 0 && row < g.m.N && t0 + t < g.T)
-                g.y[(t0 + t) * g.m.N + row] = v;
+            if ((lane & ((1 << lr) - 1)) == 0 && row < g.m.N && t < g.T)
+                g.y[t * g.m.N + row] = v;
         }
     }
 }
@@ -131,7 +129,7 @@ int launch_dot(const Q4Args &g, hipStream_t stream)
     while (lr < 6 && (1 << lr) < g.nb)
         lr++;
     const int rows = 4 * R * (64 >> lr);
-    const dim3 grid((unsigned)((g.m.N + rows - 1) / rows), (unsigned)((g.T + TC - 1) / TC));
+    const dim3 grid = grid_of((g.m.N + rows - 1) / rows);
     if (g.m.zeros)
         hipLaunchKernelGGL((q4_dot_kernel<TC, R, true>), grid, dim3(256), 0, stream, g, lr);
     else

@@ -79,7 +79,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(const NormArgs g)
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & ((1 << g.lanes) - 1);
     const int rows = (int)(blockDim.x >> g.lanes) / g.waves;
     const int w = wave % g.waves;
-    const int64_t row = (int64_t)blockIdx.x * rows + (threadIdx.x >> g.lanes) / g.waves;
+    const int64_t row = block_of_grid() * rows + (threadIdx.x >> g.lanes) / g.waves;
     const bool live = row < g.T;
     const int64_t at = row * g.K;
     float s[C][8];
@@ -172,7 +172,7 @@ int launch(const NormArgs &g0, hipStream_t stream)
     while (g.K <= 4 << g.lanes)  // (half the lanes hold it)
         g.lanes--;
     const int rows = g.waves >= 4 ? 1 : (256 >> g.lanes) / g.waves;
-    const dim3 grid((unsigned)((g.T + rows - 1) / rows));
+    const dim3 grid = grid_of((g.T + rows - 1) / rows);
     const dim3 block((unsigned)(rows * g.waves << g.lanes));
     if (c == 1)
         hipLaunchKernelGGL((rms_norm_kernel<S, A, 1>), grid, block, 0, stream, g);

@@ -42,7 +42,7 @@ __global__ __launch_bounds__(256) void q4_quantize_kernel(const V *__restrict__ 
                                                           uint16_t *scales, int8_t *zeros,
                                                           int64_t eights, int group)
 {
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t at = block_of_grid() * 256 + threadIdx.x;
     // (lanes behind the end work on the last group again and store nothing: whole
     // groups, as the end of the values is the end of one)
     const int per = group / 8;
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(256) void q4_dequantize_kernel(const bqm_q4_matrix 
                                                             V *__restrict__ out, int64_t n_rows,
                                                             float factor, int lt)
 {
-    const int64_t i = ((int64_t)blockIdx.x << (8 - lt)) + (threadIdx.x >> lt);
+    const int64_t i = (block_of_grid() << (8 - lt)) + (threadIdx.x >> lt);
     if (i >= n_rows)
         return;
     int64_t row = i;
@@ -158,8 +158,8 @@ int launch_rows(const bqm_q4_matrix *m, const int32_t *rows, void *out, int64_t 
     while (lt < 8 && (16 << lt) < m->K)
         lt++;
     const int64_t grid = (n_rows + (256 >> lt) - 1) >> (8 - lt);
-    hipLaunchKernelGGL((q4_dequantize_kernel<V>), dim3((unsigned)grid), dim3(256), 0, stream, *m,
-                       rows, static_cast<V *>(out), n_rows, factor, lt);
+    hipLaunchKernelGGL((q4_dequantize_kernel<V>), grid_of(grid), dim3(256), 0, stream, *m, rows,
+                       static_cast<V *>(out), n_rows, factor, lt);
     return check_launch();
 }
 
@@ -167,8 +167,8 @@ template <class V>
 int launch_quantize(const void *x, const bqm_q4_matrix *m, hipStream_t stream)
 {
     const int64_t eights = m->N * (m->K / 8);
-    hipLaunchKernelGGL((q4_quantize_kernel<V>), dim3((unsigned)((eights + 255) / 256)), dim3(256),
-                       0, stream, static_cast<const V *>(x),
+    hipLaunchKernelGGL((q4_quantize_kernel<V>), grid_of((eights + 255) / 256), dim3(256), 0, stream,
+                       static_cast<const V *>(x),
                        static_cast<uint8_t *>(const_cast<void *>(m->codes)),
                        static_cast<uint16_t *>(const_cast<void *>(m->scales)),
                        const_cast<int8_t *>(m->zeros), eights, m->group);

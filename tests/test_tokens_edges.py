@@ -152,3 +152,40 @@ def test_mm_q4_rows_shared_by_waves(N, K, group, zeros, T):
     # (dequantized values are rounded to fp32: 2^-24 of each)
     room = (1e-5 + 2.0 ** -24) * (c.abs() @ w.abs().t().contiguous())
     assert bool(((y.double() - c @ w.t().contiguous()).abs() <= room).all())
+
+
+@pytest.mark.gpu
+def test_more_workgroups_than_a_row_of_the_grid():
+    # above 2^20 workgroups the grid has a second dimension: rows behind that are right, and the
+    # last place's neighbour stays as it was
+    T, K = (1 << 21) + 3, 1024  # two rows a workgroup
+    x = torch.empty(T, K, device="cuda", dtype=BF16).fill_(1.0)
+    few = randn(5, K, seed=1, dtype=BF16)
+    x[-5:] = few
+    y, _ = bqm.rms_norm(x)
+    assert torch.equal(y[-5:], bqm.rms_norm(few)[0]) and torch.equal(y[:1], bqm.rms_norm(x[:1])[0])
+    assert torch.equal(y[:-5], y[:1].expand(T - 5, K))
+    del y
+    m = bqm.q4_quantize(x, group=32, zeros=True)  # 256 threads of eight values: 2^20 and more workgroups
+    want = bqm.q4_quantize(few, group=32, zeros=True)
+    assert torch.equal(m.codes[-5:], want.codes) and torch.equal(m.scales[-5:], want.scales)
+    assert torch.equal(m.zeros[-5:], want.zeros) and torch.equal(m.codes[:-5], m.codes[:1].expand(T - 5, K // 2))
+    del x
+    out = torch.full(((1 << 22) + 9, K), 7.0, device="cuda", dtype=F16)  # four rows a workgroup
+    ids = torch.full(((1 << 22) + 8,), T - 1, device="cuda", dtype=torch.int32)
+    ids[-1] = T - 5
+    bqm.q4_dequantize(m, ids, out=out[:-1])
+    rows = bqm.q4_dequantize(want, dtype=F16)
+    assert torch.equal(out[-2], rows[0]) and bool((out[-1] == 7.0).all())
+    assert torch.equal(out[:-2], rows[4:].expand((1 << 22) + 7, K))
+    del out
+    # products of one and two columns: 1024 rows of 32 values a workgroup
+    N = (1 << 30) + 2048
+    codes = torch.zeros(N, 16, device="cuda", dtype=torch.uint8)
+    scales = torch.ones(N, 1, device="cuda", dtype=F16)
+    codes[-1] = 0x11
+    a = bqm.q8_1_quantize(torch.full((2, 32), 127.0, device="cuda"))
+    for t in (1, 2):
+        y = bqm.mm_q4(bqm.Q4Matrix(codes, scales), a[:t])
+        assert bool((y[:, :-1] == 0).all()) and bool((y[:, -1] == 32 * 127.0).all())
+        del y
