@@ -708,7 +708,7 @@ size_t mm_q4_workspace_bytes(const bqm_q4_matrix *w, int64_t T)
 {
     if (!w || !q4_sizes_ok(w) || T < 1 || T > BQM_MM_MAX_COLS)
         return 0;
-    return bqm::mm_q4_workspace(w->N, T, w->K);
+    return bqm::mm_q4_workspace(w->N, T, w->K, w->group);
 }
 
 int mm_q4(const bqm_q4_matrix *w, const void *a, float *y, int64_t T, void *workspace,
@@ -722,7 +722,7 @@ int mm_q4(const bqm_q4_matrix *w, const void *a, float *y, int64_t T, void *work
         return BQM_ERR_SHAPE;
     if (!aligned4(a) || !aligned4(y))
         return BQM_ERR_ALIGN;
-    if (const size_t need = bqm::mm_q4_workspace(w->N, T, w->K)) {
+    if (const size_t need = bqm::mm_q4_workspace(w->N, T, w->K, w->group)) {
         if (!workspace || workspace_bytes < need)
             return BQM_ERR_WORKSPACE;
         if (!aligned(workspace, 256))

@@ -201,7 +201,7 @@ int launch_rms_norm(const void *x, const void *add, const float *gain, void *sum
                     int64_t T, int K, double eps, int dtype, int add_dtype, int y_dtype,
                     hipStream_t stream);
 int launch_q4_quantize(const void *x, const bqm_q4_matrix *m, int dtype, hipStream_t stream);
-size_t mm_q4_workspace(int64_t N, int64_t T, int64_t K);
+size_t mm_q4_workspace(int64_t N, int64_t T, int64_t K, int group);
 int launch_mm_q4(const bqm_q4_matrix *m, const void *a, float *y, int64_t T, void *workspace,
                  hipStream_t stream);
 int launch_q4_dequantize(const bqm_q4_matrix *m, const int32_t *rows, void *out, int64_t n_rows,

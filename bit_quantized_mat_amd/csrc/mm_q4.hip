@@ -163,36 +163,59 @@ struct Laid {
     char *ops;
     float *d, *sums;
     int runs, tiles, parts;
+    int stretch;  // chunks that go into one sum
 };
+
+// A term's roundings, 2^-24 each, have to stay below the 167 that are the header's 1e-5: those of
+// its group (1 << SH), one a group that follows in its sum, one a sum that is added to it. So a
+// part is cut into the fewest stretches that keep within that, summed one after another in y; one
+// sum takes 164 groups of 32 (5248 values), 162 of 128 (20736). Returns a stretch's chunks, 0 if no
+// number of stretches does.
+constexpr int kMostRoundings = 166;
+int stretch_of(int64_t chunks, int parts, int shift)
+{
+    const int64_t part = (chunks + parts - 1) / parts;
+    for (int n = 1; n <= kMostRoundings; n++) {
+        const int64_t each = (part + n - 1) / n;
+        if ((1 << shift) + each * kChunkRuns / (1 << shift) + n - 1 + parts - 1 <= kMostRoundings)
+            return (int)each;
+    }
+    return 0;
+}
 
 // Parts for N rows and T columns: as many as fill the device's 512 places, of four chunks
 // (512 values) at least. 4096 x 4096 and 64 columns: 22 us in 16 parts, 41 in one; two parts
-// cost more than they give (14336 x 4096, 256 columns: 76 us in two, 70 in one).
-int parts_of(int64_t N, int64_t T, int64_t nb)
+// cost more than they give (14336 x 4096, 256 columns: 76 us in two, 70 in one). The longest
+// rows are cut in any case (2^20 values in groups of 32: six parts).
+int parts_of(int64_t N, int64_t T, int64_t nb, int shift)
 {
     const int64_t tiles = (T + kTileCols - 1) / kTileCols;
     const int64_t groups = (N + 127) / 128 * (tiles <= 2 ? 1 : (tiles + 3) / 4);
     const int64_t chunks = (nb + kChunkRuns - 1) / kChunkRuns;
-    const int parts = (int)std::min<int64_t>({512 / groups, chunks / 4, 16});
-    return parts > 2 ? parts : 1;
+    int parts = (int)std::min<int64_t>({512 / groups, chunks / 4, 16});
+    parts = parts > 2 ? parts : 1;
+    while (!stretch_of(chunks, parts, shift))
+        parts++;
+    return parts;
 }
 
 size_t padded_runs(int64_t nb) { return (nb + kChunkRuns - 1) / kChunkRuns * kChunkRuns; }
 
-size_t laid_out_bytes(int64_t N, int64_t T, int64_t nb)
+size_t laid_out_bytes(int64_t N, int64_t T, int64_t nb, int shift)
 {
-    const int64_t parts = parts_of(N, T, nb);
+    const int64_t parts = parts_of(N, T, nb, shift);
     return (size_t)((T + kTileCols - 1) / kTileCols) * padded_runs(nb) *
                (kOperand + kTileCols * 4) +
            (parts > 1 ? (size_t)parts * T * N * 4 : 0);
 }
 
-Laid laid_out(void *workspace, int64_t N, int64_t T, int nb)
+Laid laid_out(void *workspace, int64_t N, int64_t T, int nb, int shift)
 {
     Laid l;
     l.runs = (int)padded_runs(nb);
     l.tiles = (int)((T + kTileCols - 1) / kTileCols);
-    l.parts = parts_of(N, T, nb);
+    l.parts = parts_of(N, T, nb, shift);
+    l.stretch = stretch_of(l.runs / kChunkRuns, l.parts, shift);
     l.ops = static_cast<char *>(workspace);
     l.d = reinterpret_cast<float *>(l.ops + (size_t)l.tiles * l.runs * kOperand);
     l.sums = l.d + (size_t)l.tiles * l.runs * kTileCols;
@@ -282,7 +305,9 @@ __device__ __forceinline__ f16x8 codes_of(uint32_t w, f16x2 low, f16x2 high)
 // columns each time: kKept groups at once.
 constexpr int kKept = 8;
 
-template <int NT, int SH, bool Z>
+// LONG: rows of several stretches. Those that one sum takes keep a kernel without (a check a
+// chunk costs them 1 to 3%).
+template <int NT, int SH, bool Z, bool LONG>
 __global__ __launch_bounds__(256, 2) void q4_mfma_kernel(const Q4Args g, const Laid l)
 {
     // a chunk's operands and d: [tile][run]; two of each
@@ -428,6 +453,35 @@ __global__ __launch_bounds__(256, 2) void q4_mfma_kernel(const Q4Args g, const L
     };
     const int begin = (int)((int64_t)chunks * blockIdx.z / gridDim.z);
     const int end = (int)((int64_t)chunks * (blockIdx.z + 1) / gridDim.z);
+    float *const y = gridDim.z > 1 ? l.sums + (size_t)blockIdx.z * g.T * g.m.N : g.y;
+    // The tile's sums to y, or added to those of the stretches before, by the thread that wrote
+    // them.
+    auto put = [&](bool first) {
+#pragma unroll
+        for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int m = 0; m < 4; m++) {
+                const int64_t col = (int64_t)(tile0 + t) * kTileCols + 16 * (m & 1) + (lane & 15);
+                if (col >= g.T)
+                    continue;
+                const int64_t n = n0 + 16 * (m >> 1) + 4 * h;
+                float *const to = y + col * g.m.N + n;
+                if (LONG && n + 4 <= g.m.N) {
+                    f32x4 v = acc[t][m];
+                    if (!first) {
+                        f32x4 before;
+                        __builtin_memcpy(&before, to, 16);
+                        v = before + v;
+                    }
+                    __builtin_memcpy(to, &v, 16);
+                    continue;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    if (n + i < g.m.N)
+                        to[i] = !LONG || first ? acc[t][m][i] : to[i] + acc[t][m][i];
+            }
+    };
     constexpr int kPeriod = kKept / kGroups;  // chunks
     fetch(begin);
     gather(begin / kPeriod);
@@ -519,29 +573,23 @@ __global__ __launch_bounds__(256, 2) void q4_mfma_kernel(const Q4Args g, const L
             }
         }
         store(buf ^ 1, 1);
-    }
-    float *const y = gridDim.z > 1 ? l.sums + (size_t)blockIdx.z * g.T * g.m.N : g.y;
+        if constexpr (LONG) {
+            if ((chunk + 1 - begin) % l.stretch == 0 && chunk + 1 < end) {
+                put(chunk + 1 - begin == l.stretch);
 #pragma unroll
-    for (int t = 0; t < NT; t++)
-#pragma unroll
-        for (int m = 0; m < 4; m++) {
-            const int64_t col = (int64_t)(tile0 + t) * kTileCols + 16 * (m & 1) + (lane & 15);
-            if (col >= g.T)
-                continue;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int64_t n = n0 + 16 * (m >> 1) + 4 * h + i;
-                if (n < g.m.N)
-                    y[col * g.m.N + n] = acc[t][m][i];
+                for (int i = 0; i < NT * 4; i++)
+                    acc[i / 4][i % 4] = f32x4{};
             }
         }
+    }
+    put(!LONG || end - begin <= l.stretch);
 }
 
 // y = the parts' sums, in their order.
 __global__ __launch_bounds__(256) void q4_parts_kernel(const float *__restrict__ sums,
                                                        float *__restrict__ y, int64_t n, int parts)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = block_of_grid() * 256 + threadIdx.x;
     if (i >= n)
         return;
     float v = sums[i];
@@ -555,11 +603,17 @@ int launch_mfma_group(const Q4Args &g, const Laid &l, hipStream_t stream)
 {
     const dim3 grid((unsigned)((g.m.N + 127) / 128), (unsigned)((l.tiles + NT - 1) / NT),
                     (unsigned)l.parts);
+    const int chunks = l.runs / kChunkRuns;
+    const bool several = l.stretch < (chunks + l.parts - 1) / l.parts;
+    auto run = [&](auto *kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, g, l);
+        return check_launch();
+    };
     if (g.m.zeros)
-        hipLaunchKernelGGL((q4_mfma_kernel<NT, SH, true>), grid, dim3(256), 0, stream, g, l);
-    else
-        hipLaunchKernelGGL((q4_mfma_kernel<NT, SH, false>), grid, dim3(256), 0, stream, g, l);
-    return check_launch();
+        return several ? run(q4_mfma_kernel<NT, SH, true, true>)
+                       : run(q4_mfma_kernel<NT, SH, true, false>);
+    return several ? run(q4_mfma_kernel<NT, SH, false, true>)
+                   : run(q4_mfma_kernel<NT, SH, false, false>);
 }
 
 template <int NT>
@@ -576,8 +630,8 @@ int launch_mfma(const Q4Args &g, const Laid &l, hipStream_t stream)
     if (l.parts == 1)
         return BQM_OK;
     const int64_t n = g.T * g.m.N;
-    hipLaunchKernelGGL(q4_parts_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream,
-                       l.sums, g.y, n, l.parts);
+    hipLaunchKernelGGL(q4_parts_kernel, grid_of((n + 255) / 256), dim3(256), 0, stream, l.sums,
+                       g.y, n, l.parts);
     return check_launch();
 }
 
@@ -864,21 +918,24 @@ constexpr int64_t kMostCols = 8192;  // laid out at once
 
 }  // namespace
 
-size_t mm_q4_workspace(int64_t N, int64_t T, int64_t K)
+static int shift_of(int group) { return group == 32 ? 0 : group == 64 ? 1 : 2; }
+
+size_t mm_q4_workspace(int64_t N, int64_t T, int64_t K, int group)
 {
     if (T <= kDotCols || few_supported(T, (int)(K / 32)))
         return 0;
     // (the columns of the last turn, where there are several, may be few enough for parts)
     const int64_t last = (T - 1) % kMostCols + 1;
-    return std::max(laid_out_bytes(N, std::min(T, kMostCols), K / 32),
-                    laid_out_bytes(N, last, K / 32));
+    const int shift = shift_of(group);
+    return std::max(laid_out_bytes(N, std::min(T, kMostCols), K / 32, shift),
+                    laid_out_bytes(N, last, K / 32, shift));
 }
 
 int launch_mm_q4(const bqm_q4_matrix *m, const void *a, float *y, int64_t T, void *workspace,
                  hipStream_t stream)
 {
     Q4Args g = {*m, static_cast<const uint8_t *>(a), y, T, (int)(m->K / 32),
-                m->group == 32 ? 0 : m->group == 64 ? 1 : 2};
+                shift_of(m->group)};
     if (T == 1)
         return launch_dot<1, 4>(g, stream);
     if (T <= kDotCols)
@@ -889,7 +946,7 @@ int launch_mm_q4(const bqm_q4_matrix *m, const void *a, float *y, int64_t T, voi
         g.T = std::min(T - t, kMostCols);
         g.a = static_cast<const uint8_t *>(a) + t * g.nb * kQ81BlockBytes;
         g.y = y + t * m->N;
-        const Laid l = laid_out(workspace, m->N, g.T, g.nb);
+        const Laid l = laid_out(workspace, m->N, g.T, g.nb, g.shift);
         const int rc = g.T <= 32 ? launch_mfma<1>(g, l, stream)
                        : g.T <= 64 ? launch_mfma<2>(g, l, stream)
                                    : launch_mfma<4>(g, l, stream);
