@@ -659,7 +659,12 @@ size_t few_lds(int ct, int nb) { return (size_t)((nb + 3) / 4 * 4) * ct * kFewRu
 // share of the row tiles, and a wave an even share of the runs of those, one after another
 // (in periods of four groups): the end of a tile that the wave before it began, whole tiles,
 // the beginning of one that others end, whose parts are added at last, in their order.
-template <int CT, int W, int SH, bool Z>
+//
+// LONG: one tile of columns leaves room for 284 runs. In groups of 32 that is more roundings of
+// one sum than the bound allows (see stretch_of), so a part's first chunks have a sum of their
+// own: 1 + 144 + 1 roundings, and 15 at most where waves' parts are added. Shorter rows do without
+// (2% of 9 columns' time).
+template <int CT, int W, int SH, bool Z, bool LONG>
 __global__ __launch_bounds__(64 * W) void q4_few_kernel(const Q4Args g, int tiles)
 {
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -780,11 +785,23 @@ __global__ __launch_bounds__(64 * W) void q4_few_kernel(const Q4Args g, int tile
     };
     float acc[CT][4], sums[CT][4], head[CT][4] = {};  // head: of a tile that another wave began
     bool tail = false;                                // acc: of one that others end
+    constexpr int kFirstSum = 36;  // chunks, of 71 at most
+    static_assert(kFirstSum % kAhead == 0);
+    float before[4];
     while (at < share_end) {
 #pragma unroll
         for (int i = 0; i < CT * 4; i++)
             acc[i / 4][i % 4] = 0.0f;
         for (int start = first; start < end; start += kAhead) {
+            if constexpr (LONG) {
+                if (start - first == kFirstSum) {
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        before[k] = acc[0][k];
+                        acc[0][k] = 0.0f;
+                    }
+                }
+            }
 #pragma unroll
             for (int slot = 0; slot < kAhead; slot++) {
                 const int chunk = start + slot;
@@ -837,6 +854,13 @@ __global__ __launch_bounds__(64 * W) void q4_few_kernel(const Q4Args g, int tile
                 }
             }
         }
+        if constexpr (LONG) {
+            if (end - first > kFirstSum) {
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    acc[0][k] = before[k] + acc[0][k];
+            }
+        }
         const bool begun = first == 0;
         const int64_t n1 = n0;
         tail = begun && share_end < tile_end;
@@ -876,6 +900,11 @@ __global__ __launch_bounds__(64 * W) void q4_few_kernel(const Q4Args g, int tile
     store(acc, n0);
 }
 
+// Groups of one sum: the roundings of a group (4 at most) and of 15 parts' additions beside them.
+// Two tiles of columns have at most 142 runs, one tile's groups of 64 and 128 are as many or fewer.
+constexpr int kFewOneSum = kMostRoundings - 4 - 15;
+static_assert(kLdsMax / (4 * kFewRun) * 4 / 2 <= kFewOneSum);
+
 template <int CT, int W, int SH>
 int launch_few_group(const Q4Args &g, hipStream_t stream)
 {
@@ -887,7 +916,13 @@ int launch_few_group(const Q4Args &g, hipStream_t stream)
         hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * W), bytes, stream, g, tiles);
         return check_launch();
     };
-    return g.m.zeros ? run(q4_few_kernel<CT, W, SH, true>) : run(q4_few_kernel<CT, W, SH, false>);
+    if constexpr (CT == 1 && SH == 0) {
+        if (g.nb > kFewOneSum)
+            return g.m.zeros ? run(q4_few_kernel<CT, W, SH, true, true>)
+                             : run(q4_few_kernel<CT, W, SH, false, true>);
+    }
+    return g.m.zeros ? run(q4_few_kernel<CT, W, SH, true, false>)
+                     : run(q4_few_kernel<CT, W, SH, false, false>);
 }
 
 template <int CT, int W>

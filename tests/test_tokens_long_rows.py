@@ -51,10 +51,12 @@ def one_and_little(K, group, first):
     return blocks(q, d), float((q * d).sum())
 
 
-# tiles of 32, 64 and 128 columns; rows so many that no part is cut for want of work
+# the few columns that fit in LDS; tiles of 32, 64 and 128 columns; rows so many that no part is cut for want of work
 @pytest.mark.gpu
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("N,K,group,T,first", [
+    (65536, 9088, 32, 3, 1), (28671, 9088, 32, 16, 1), (65536, 6016, 32, 9, 1), (30000, 4544, 32, 32, 1),
+    (65536, 9088, 64, 5, 1), (28671, 9088, 128, 16, 1),
     (21888, 16384, 32, 40, 1), (21888, 16384, 32, 20, 1), (21888, 32768, 64, 64, 1), (14336, 32768, 32, 256, 1),
     (2816, 65536, 32, 1024, 1), (2816, 1 << 18, 128, 1024, 1), (2816, 1 << 20, 32, 1024, 1), (21888, 65568, 32, 33, 1)])
 def test_roundings_of_one_side(N, K, group, T, first, zeros):
