@@ -69,16 +69,32 @@ __device__ __forceinline__ void stage_columns(Stage<TC> &s, const Q4Args &g, int
 // the row's runs in turn. Rows are read once, 16 bytes a lane, R loads on their way. 100003 x
 // 4096 and one column: 41.6 us, 5.2 TB/s (a large copy: 5.1); 4096 x 4096 4.5, latency. Two
 // columns 48; four took 67 to 75 and eight 120, where the next kernel takes 52.
-template <int TC, int R, bool Z>
+//
+// A term goes through a rounding of its own, one a run that follows in its lane's sum and six where
+// lanes are added; the header's 1e-5 are 167. LONG: rows of which a lane has more runs than that
+// have a sum of each kSumRuns, 128 of a lane, added up one after another (four at most).
+constexpr int kSumRuns = 64 * kStageRuns;
+
+template <int TC, int R, bool Z, bool LONG>
 __global__ __launch_bounds__(256) void q4_dot_kernel(const Q4Args g, int lr)
 {
     __shared__ Stage<TC> s;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int per = 64 >> lr;  // rows side by side
     const int64_t first = (block_of_grid() * 4 + wave) * (per * R) + (lane >> lr);
-    float acc[R][TC] = {};
+    float acc[R][TC] = {}, before[R][TC];
     for (int b0 = 0; b0 < g.nb; b0 += kStageRuns) {
         const int n = g.nb - b0 < kStageRuns ? g.nb - b0 : kStageRuns;
+        if constexpr (LONG) {
+            if (b0 % kSumRuns == 0) {
+#pragma unroll
+                for (int i = 0; i < R * TC; i++) {
+                    before[i / TC][i % TC] =
+                        b0 ? before[i / TC][i % TC] + acc[i / TC][i % TC] : 0.0f;
+                    acc[i / TC][i % TC] = 0.0f;
+                }
+            }
+        }
         if (b0)
             __syncthreads();
         stage_columns<TC, Z>(s, g, b0, n);
@@ -115,7 +131,7 @@ __global__ __launch_bounds__(256) void q4_dot_kernel(const Q4Args g, int lr)
         const int64_t row = first + r * per;
 #pragma unroll
         for (int t = 0; t < TC; t++) {
-            const float v = row_sum(acc[r][t], lr);
+            const float v = row_sum(LONG ? before[r][t] + acc[r][t] : acc[r][t], lr);
             if ((lane & ((1 << lr) - 1)) == 0 && row < g.m.N && t < g.T)
                 g.y[t * g.m.N + row] = v;
         }
@@ -130,11 +146,15 @@ int launch_dot(const Q4Args &g, hipStream_t stream)
         lr++;
     const int rows = 4 * R * (64 >> lr);
     const dim3 grid = grid_of((g.m.N + rows - 1) / rows);
-    if (g.m.zeros)
-        hipLaunchKernelGGL((q4_dot_kernel<TC, R, true>), grid, dim3(256), 0, stream, g, lr);
-    else
-        hipLaunchKernelGGL((q4_dot_kernel<TC, R, false>), grid, dim3(256), 0, stream, g, lr);
-    return check_launch();
+    auto run = [&](auto *kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, g, lr);
+        return check_launch();
+    };
+    if (g.nb > kSumRuns)
+        return g.m.zeros ? run(q4_dot_kernel<TC, R, true, true>)
+                         : run(q4_dot_kernel<TC, R, false, true>);
+    return g.m.zeros ? run(q4_dot_kernel<TC, R, true, false>)
+                     : run(q4_dot_kernel<TC, R, false, false>);
 }
 
 // ---- many columns: the matrix cores ------------------------------------------------

@@ -51,10 +51,12 @@ def one_and_little(K, group, first):
     return blocks(q, d), float((q * d).sum())
 
 
-# the few columns that fit in LDS; tiles of 32, 64 and 128 columns; rows so many that no part is cut for want of work
+# kernels: of one and two columns (64 lanes a row, each its own sum), of the few that fit in LDS, of tiles of
+# 32, 64 and 128 columns; rows so many that no kernel cuts them by itself
 @pytest.mark.gpu
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("N,K,group,T,first", [
+    (70, 1 << 20, 32, 1, 64), (70, 1 << 20, 32, 2, 64), (33, 1 << 19, 32, 1, 64), (9, 1 << 20, 128, 2, 64),
     (65536, 9088, 32, 3, 1), (28671, 9088, 32, 16, 1), (65536, 6016, 32, 9, 1), (30000, 4544, 32, 32, 1),
     (65536, 9088, 64, 5, 1), (28671, 9088, 128, 16, 1),
     (21888, 16384, 32, 40, 1), (21888, 16384, 32, 20, 1), (21888, 32768, 64, 64, 1), (14336, 32768, 32, 256, 1),
@@ -66,7 +68,7 @@ def test_roundings_of_one_side(N, K, group, T, first, zeros):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("N,K,group,T", [(14336, 32768, 32, 256), (2816, 65536, 32, 1024), (2816, 1 << 20, 32, 1024),
-                                         (2816, 1 << 20, 128, 1024), (40, 1 << 20, 32, 150)])
+                                         (2816, 1 << 20, 128, 1024), (40, 1 << 20, 32, 150), (40, 1 << 20, 32, 1)])
 def test_equal_terms(N, K, group, T):
     scale, d = np.float16(0.1), np.float16(0.3)
     nb = K // 32
