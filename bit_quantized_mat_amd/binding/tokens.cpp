@@ -261,7 +261,8 @@ PYBIND11_MODULE(_tokens, m)
           "not centred.");
     m.def("mm_q4_workspace_bytes",
           [](const Q4Matrix &q, int64_t T) { return mm_q4_workspace_bytes(&q.m, T); }, py::arg("m"),
-          py::arg("T"), "Bytes of the uint8 tensor that mm_q4(..., workspace=) takes (0: none).");
+          py::arg("T"),
+          "Bytes of the uint8 tensor that mm_q4(..., workspace=) takes for up to T columns (0: none).");
     m.def("mm_q4", &mm_q4_, py::arg("m"), py::arg("a"), out, py::arg("workspace") = py::none(),
           stream,
           "y fp32 [T, N] = a Q4Matrix times T Q8_1 activation columns a, uint8 [T, K / 32 * 36].");

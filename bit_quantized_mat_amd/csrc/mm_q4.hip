@@ -975,15 +975,25 @@ constexpr int64_t kMostCols = 8192;  // laid out at once
 
 static int shift_of(int group) { return group == 32 ? 0 : group == 64 ? 1 : 2; }
 
+// What the largest call of up to T columns needs, so that a workspace serves smaller calls too:
+// columns laid out grow with T, but parts are the more the fewer columns there are, so those calls
+// are looked at whose columns are the most that get their number of parts. (The last turn of
+// several may be such a call as well.)
 size_t mm_q4_workspace(int64_t N, int64_t T, int64_t K, int group)
 {
-    if (T <= kDotCols || few_supported(T, (int)(K / 32)))
+    const int64_t nb = K / 32;
+    if (T <= kDotCols || few_supported(T, (int)nb))
         return 0;
-    // (the columns of the last turn, where there are several, may be few enough for parts)
-    const int64_t last = (T - 1) % kMostCols + 1;
     const int shift = shift_of(group);
-    return std::max(laid_out_bytes(N, std::min(T, kMostCols), K / 32, shift),
-                    laid_out_bytes(N, last, K / 32, shift));
+    T = std::min(T, kMostCols);
+    size_t need = laid_out_bytes(N, T, nb, shift);
+    constexpr int64_t kFour = 4 * kTileCols;  // columns that count alike in parts_of
+    for (int64_t parts = 16; parts > 2; parts--) {
+        const int64_t most = 512 / ((N + 127) / 128 * parts) * kFour;
+        if (most > 0)
+            need = std::max(need, laid_out_bytes(N, std::min(T, most), nb, shift));
+    }
+    return need;
 }
 
 int launch_mm_q4(const bqm_q4_matrix *m, const void *a, float *y, int64_t T, void *workspace,

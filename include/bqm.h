@@ -600,7 +600,8 @@ BQM_API int mm_q4(const bqm_q4_matrix *w, const void *a, float *y, int64_t T, vo
                   size_t workspace_bytes, void *stream);
 
 /* Workspace mm_q4 needs for T columns (0 also for what it refuses; of the matrix
- * only the sizes are read). */
+ * only the sizes are read). It never falls as T grows: a workspace for T columns
+ * serves calls of fewer. */
 BQM_API size_t mm_q4_workspace_bytes(const bqm_q4_matrix *w, int64_t T);
 
 /* Rows of a 4-bit matrix (a table's look-up):
