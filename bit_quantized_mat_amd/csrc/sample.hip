@@ -860,18 +860,25 @@ int launch(const SampleArgs &g, int64_t T, hipStream_t stream)
 // 4096 to 1000000 logits, the border runs from 45000 logits (one row: 30 us alone, 27 shared,
 // of 50000; 25 and 27 of 32001) by 64000 (32 rows: 43 and 41) to 131071 (128 rows: 75 and 71;
 // 69 and 74 of 100003).
+constexpr int64_t kSharedRows = 128;
+
+// The most rows that are shared, of V logits.
+int64_t shared_rows(int64_t V) { return V < 40000 ? 0 : std::min((V - 40000) / 700, kSharedRows); }
+
 int parts_of(int64_t T, int64_t V)
 {
-    if (T < 1 || T > 128 || V < 40000 + 700 * T)
+    if (T < 1 || T > shared_rows(V))
         return 1;
     return (int)std::min<int64_t>({512 / T, V / 2048, kPartsMax});
 }
 
 }  // namespace
 
+// What the largest call of up to T rows needs, so that a workspace serves smaller calls too (more
+// rows than are shared need none themselves).
 size_t sample_workspace(int64_t T, int64_t V)
 {
-    return parts_of(T, V) == 1 ? 0 : ((size_t)T * sizeof(RowSums) + 255) / 256 * 256;
+    return ((size_t)std::min(T, shared_rows(V)) * sizeof(RowSums) + 255) / 256 * 256;
 }
 
 int launch_sample(const void *logits, int64_t row_stride, const float *temperature,

@@ -34,5 +34,5 @@ _tokens.set_python(BqmError, torch._C._cuda_getCurrentRawStream)
 
 
 def sample_workspace_bytes(T, V):
-    """Bytes of the uint8 tensor that ``sample(..., workspace=)`` takes (0: none)."""
+    """Bytes of the uint8 tensor that ``sample(..., workspace=)`` takes for up to T rows (0: none)."""
     return int(library().sample_workspace_bytes(T, V))

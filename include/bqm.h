@@ -641,7 +641,8 @@ BQM_API int sample(const void *logits, int64_t row_stride, const float *temperat
                    int32_t *tokens, float *logprobs, int64_t T, int64_t V, int32_t dtype,
                    void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace sample needs for these sizes (0 also for sizes it refuses). */
+/* Workspace sample needs for these sizes (0 also for sizes it refuses). It never
+ * falls as T grows: a workspace for T rows serves calls of fewer, of as many logits. */
 BQM_API size_t sample_workspace_bytes(int64_t T, int64_t V);
 
 /* Human-readable text for a status code (static storage). */

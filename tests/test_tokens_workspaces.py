@@ -22,6 +22,29 @@ def test_mm_q4_workspace_never_falls(N, K, group):
         last = need
 
 
+@pytest.mark.parametrize("V", [1, 2000, 40000, 40699, 40700, 100003, 129599, 129600, 131071, (1 << 20) - 1])
+def test_sample_workspace_never_falls(V):
+    last = 0
+    for T in [0, *range(1, 300), *range(300, 65535, 991), 65535]:
+        need = bqm.sample_workspace_bytes(T, V)
+        assert need >= last, (T, need, last)
+        last = need
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [41000, 100003])
+def test_sample_in_the_workspace_of_a_larger_call(V):
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x, u = torch.randn(256, V, generator=g, device="cuda"), torch.rand(256, generator=g, device="cuda")
+    need = bqm.sample_workspace_bytes(256, V)
+    room = torch.full((need + 4096,), 0xff, device="cuda", dtype=torch.uint8)
+    for T in (256, 1, 2, 64, 85, 86, 128, 0):
+        tokens, logprobs = bqm.sample(x[:T], u[:T], workspace=room[:need])
+        assert bool((room[need:] == 0xff).all())
+        want = bqm.sample(x[:T], u[:T])
+        assert torch.equal(tokens, want[0]) and torch.equal(logprobs, want[1]), T
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("N,K,group", [(4096, 4096, 128), (300, 9120, 32), (40, 65536, 64)])
 def test_mm_q4_in_the_workspace_of_a_larger_call(N, K, group):
