@@ -196,8 +196,9 @@ struct Weights {
         const double f = floor(y);
         const int k = (int)f;
         bin = (-k) >> 5;
-        // 2^(y / kSteps) = power of the whole part times e^r, r below 2^-10: the series'
-        // third power leaves 2^-46, its fp32 rounding 2^-34
+        // 2^(y / kSteps) = power of the whole part times e^r, r below 2^-10.5: the series'
+        // third power leaves 2^-46, five roundings to fp32 of e^r - 1 at most 2^-32.2 (2^-33.0
+        // is the most that 40 million values showed)
         const float r = (float)(y - f) * 6.7690154351557158e-4f;  // ln(2) / kSteps
         const float p = r * fmaf(r, fmaf(r, 0.16666667f, 0.5f), 1.0f);
         double w = power[k & (kSteps - 1)];

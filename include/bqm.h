@@ -626,8 +626,10 @@ BQM_API int q4_dequantize(const bqm_q4_matrix *w, const int32_t *rows, void *out
  * -infinity are never taken; if there are others of +infinity, those alone have
  * weight, 1 each. A row with nothing to take gives token -1. logprobs[t] is the
  * logarithm of the token's share of the weights left (-infinity for token -1).
- * Weights are formed in fp64 and summed as whole numbers of 2^-44, so results do
- * not depend on an order of sums; weights below 2^-45 count as none.
+ * A weight is formed to within 2^-32 of itself and rounded to a whole number of
+ * 2^-44: closer than that to a border of top_p, min_p or u, a token may fall on
+ * either side of it. Sums are exact, so results do not depend on their order;
+ * weights below 2^-45 count as none.
  *   logits [T][V] of dtype (BQM_DTYPE_*), rows row_stride elements apart;
  *   temperature, top_p, min_p, u [T] fp32, top_k [T] int32; each but u may be NULL
  *   (1; 1; 0; 0); u in [0, 1), clamped; tokens [T] int32; logprobs [T] fp32 or
