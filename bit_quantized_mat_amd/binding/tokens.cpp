@@ -241,7 +241,8 @@ PYBIND11_MODULE(_tokens, m)
           "out_dtype. sum_out takes s\n(x itself: in place).");
     m.def("rms_norm_q8_1", &rms_norm_q8_1_, py::arg("x"), gain, add, py::arg("eps") = 1e-6, sum, out,
           stream,
-          "(a, s) as rms_norm, y as Q8_1 blocks: uint8 [T, K / 32 * 36], the products' activations.");
+          "(a, s) as rms_norm, y as Q8_1 blocks: uint8 [T, K / 32 * 36], the products' activations. A NaN of "
+          "y is 0 in\nthem, as in q8_1_quantize.");
     py::class_<Q4Matrix>(m, "Q4Matrix",
                          "A matrix in 4 bits: codes uint8 [rows, values / 2] (each run of 16 bytes 32 "
                          "values: low halves the first 16,\nhigh halves the rest, two's complement), scales "

@@ -556,7 +556,8 @@ BQM_API size_t kv_pages_workspace_bytes(const bqm_kv_pages *pages);
  *   [K] fp32 or NULL (ones); sum [T][K] of dtype, where s goes (may be x itself,
  *   or add if of the same type; may be NULL without add); y [T][K] of y_dtype or
  *   NULL; a [T][K/32] Q8_1 blocks of y's fp32 values (bitwise q8_1_quantize of
- *   them) or NULL. One of y and a is given, or both.
+ *   them, which takes a NaN as 0: of a row of NaN the blocks are zeros, and y alone
+ *   shows it) or NULL. One of y and a is given, or both.
  * Shapes: 0 <= T <= 2^23 (0: nothing is done), K a multiple of 32, 32 .. 65536,
  * eps >= 0 and finite. Alignment: 16 bytes, a 4 bytes. */
 BQM_API int rms_norm(const void *x, const void *add, const float *gain, void *sum, void *y,
