@@ -803,7 +803,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs g)
             q.weight = q.weight < 1 ? 1 : q.weight > all ? all : q.weight;
         } else {
             float u = g.u[t];
-            u = u > 0.0f ? u : 0.0f;
+            u = u > 0.0f ? fminf(u, 1.0f) : 0.0f;  // (the product stays below 2^64)
             left = set.floor > 0.0f && left < all ? left : all;
             q.weight = (u64)((double)u * (double)left) + 1;
             q.weight = q.weight > left ? left : q.weight;
