@@ -57,7 +57,7 @@ def one_and_little(K, group, first):
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("N,K,group,T,first", [
     (70, 1 << 20, 32, 1, 64), (70, 1 << 20, 32, 2, 64), (33, 1 << 19, 32, 1, 64), (9, 1 << 20, 128, 2, 64),
-    (65536, 9088, 32, 3, 1), (28671, 9088, 32, 16, 1), (65536, 6016, 32, 9, 1), (30000, 4544, 32, 32, 1),
+    (65536, 9088, 32, 3, 1), (28671, 9088, 32, 16, 1), (65536, 6016, 32, 9, 1), (30000, 4480, 32, 32, 1), (30000, 4544, 32, 32, 1),
     (65536, 9088, 64, 5, 1), (28671, 9088, 128, 16, 1),
     (21888, 16384, 32, 40, 1), (21888, 16384, 32, 20, 1), (21888, 32768, 64, 64, 1), (14336, 32768, 32, 256, 1),
     (2816, 65536, 32, 1024, 1), (2816, 1 << 18, 128, 1024, 1), (2816, 1 << 20, 32, 1024, 1), (21888, 65568, 32, 33, 1)])
