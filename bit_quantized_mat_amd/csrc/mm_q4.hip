@@ -8,7 +8,8 @@
 //
 // Three kernels: one or two columns go without the matrix cores, bound by reading the matrix;
 // columns that fit in LDS, at most 32, stay there while waves stream rows; more go by tiles,
-// bound by the issue of instructions. Figures are of one MI355X.
+// where vector and matrix instructions and waits add up. Each keeps the header's bound, 1e-5 of
+// the terms' sum, by the number of roundings that a term goes through. Figures are of one MI355X.
 #include <algorithm>
 
 #include "common.hpp"
@@ -306,10 +307,10 @@ __device__ __forceinline__ f16x8 codes_of(uint32_t w, f16x2 low, f16x2 high)
     return {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Bound by issue, where scaling each run's result costs more than the product: of a 14336 x
-// 4096 product of 2000 columns' 340 to 350 us (690 TFLOP/s; a large fp16 library product 1244)
-// vector instructions alone take 187, with LDS reads 202, with the products 245, with all but
-// global loads 265. 64 columns a workgroup took 392, eight waves 379, three waves a SIMD 425.
+// No unit is full: scaling each run's result costs more than the product, and both more or less
+// add up. Of a 14336 x 4096 product of 2000 columns' 340 to 350 us (690 TFLOP/s; a large fp16
+// library product 1244) vector instructions alone take 187, with LDS reads 202, with the products
+// 245, with all but global loads 265. 64 columns a workgroup took 392, eight waves 379, three waves a SIMD 425.
 //
 // Four waves of 32 rows, NT tiles of 32 columns; groups of 32 << SH. (Two workgroups a
 // compute unit: with at most 256 registers a wave products' results stay out of the
@@ -325,8 +326,8 @@ __device__ __forceinline__ f16x8 codes_of(uint32_t w, f16x2 low, f16x2 high)
 // columns each time: kKept groups at once.
 constexpr int kKept = 8;
 
-// LONG: rows of several stretches. Those that one sum takes keep a kernel without (a check a
-// chunk costs them 1 to 3%).
+// LONG: rows of several stretches (4096 x 14336, groups of 32, 2047 columns: 452 us, 435 as one
+// sum). Those that one sum takes keep a kernel without (a check a chunk costs them 1 to 3%).
 template <int NT, int SH, bool Z, bool LONG>
 __global__ __launch_bounds__(256, 2) void q4_mfma_kernel(const Q4Args g, const Laid l)
 {
@@ -659,7 +660,7 @@ int launch_mfma(const Q4Args &g, const Laid &l, hipStream_t stream)
 //
 // Up to 32 columns that fit in LDS stay there, as int8 operands, and every wave goes through
 // rows by itself, without a barrier between its loads: what counts is bytes on their way, then
-// issue (150 instructions for four runs). 100003 x 4096: 9 columns 51 us, 17 64 (the matrix
+// issue (150 instructions for four runs). 100003 x 4096: 9 columns 49 us, 17 60 (the matrix
 // alone 42; by tiles 108), 72 with whole tiles dealt to waves; 4096 x 4096 and 9 columns 7.2.
 // A code in the high half of its byte is 16 times the code, so an operand takes three
 // instructions; a zero's share goes into the products' start, -16 * zero * sum of q. The
@@ -921,7 +922,7 @@ __global__ __launch_bounds__(64 * W) void q4_few_kernel(const Q4Args g, int tile
 }
 
 // Groups of one sum: the roundings of a group (4 at most) and of 15 parts' additions beside them.
-// Two tiles of columns have at most 142 runs, one tile's groups of 64 and 128 are as many or fewer.
+// Two tiles of columns have at most 140 runs, one tile's 284 are at most 142 groups of 64 or 128.
 constexpr int kFewOneSum = kMostRoundings - 4 - 15;
 static_assert(kLdsMax / (4 * kFewRun) * 4 / 2 <= kFewOneSum);
 

@@ -17,8 +17,8 @@
 // (its largest logit; its bins) are shared by several workgroups each, launches of their
 // own before it. What bounds it: of few rows the latency of a score of steps (one row of
 // 32001 logits 21.6 us), else the fp64 weights and the passes over a row by one compute unit
-// (256 rows of 100003 bf16 85 us: largest 9, bins 25, each gathering 6 to 9; 64 of fp32, shared
-// by 8: 7 + 14 us, then 32 of the row's own workgroup).
+// (256 rows of 100003 bf16 82 us: largest 9, bins 25, each gathering 6 to 9, the rest not taken
+// apart; 64 of fp32, shared by 8: 7 + 14 us, then 32 of the row's own workgroup).
 #include <algorithm>
 #include <type_traits>
 
